@@ -1,6 +1,8 @@
 /*
  * ssm_scan.h -- C ABI of the MI355X (gfx950) fused selective scan: the
- * forward and its backward (ssm_selective_scan_bwd, further below).
+ * forward and its backward (ssm_selective_scan_bwd, further below), its form
+ * for single tokens on a cache of states, and the operators beside it in the
+ * block: the short causal convolution and the layer or RMS norm.
  *
  * The operation (Mamba's selective state-space scan).  For every
  * batch row b, channel d and state n, with A = -exp(A_log[d,n]):
@@ -294,6 +296,244 @@ int64_t ssm_scan_bwd_workspace_bytes(const ssm_scan_dims* dims);
 int ssm_selective_scan_bwd(ssm_scan_t handle, const void* x, const void* delta, const float* A_log, const void* B,
                            const void* C, const float* D, const int32_t* valid_len, const ssm_scan_dims* dims,
                            const ssm_scan_fwd_extras* extras, const ssm_scan_bwd_io* io, void* stream);
+
+/* ---- the scan for single tokens ---------------------------------------
+ *
+ * One step of the scan for every row of a batch, on a cache of states: with
+ * delta = clip(softplus(delta + delta_bias)) as in the forward,
+ *
+ *     h' = exp(delta * A) h + delta * B x,   y = (C . h' + D x) (* silu(z))
+ *
+ * dims is the forward's, with seqlen = 1; dim may be any number here.
+ *
+ *  x, delta, z, y  [batch, dim] io dtype, rows x_row_stride (...) elements
+ *               apart, dim fastest; z may be NULL (no gate).
+ *  B, C         [batch, dstate] io dtype, likewise.
+ *  A_log [dim, dstate], D [dim] or NULL, delta_bias [dim] or NULL: fp32.
+ *  h0, h_last   [n_slots, dim, dstate] fp32, or [batch, dim, dstate] without
+ *               slots: the cache read and the cache written.  They may be the
+ *               same buffer (the usual update in place); any other overlap is
+ *               rejected.  Only the rows that the batch's slots name are
+ *               written.
+ *  slots        [batch] int32 or NULL: the cache row of every batch row.  A
+ *               row whose slot lies outside [0, n_slots) (say -1, a row that
+ *               only pads the batch) is idle: it touches no state and its y is
+ *               +0.  Where several rows name one slot, the first of them takes
+ *               the step and the others are idle.  NULL: row b uses state b.
+ *
+ * Input strides must not be negative (0 repeats a row); rows of y must not
+ * overlap (SSM_ERR_INVALID_ARG).  batch is at most 65535, and sizes, slots
+ * included, below 2^31 (SSM_ERR_UNSUPPORTED).  Otherwise the conventions of
+ * the forward: checks first, asynchronous, bitwise reproducible. */
+typedef struct ssm_scan_step_io {
+  const void* x;
+  const void* delta;
+  const float* A_log;
+  const void* B;
+  const void* C;
+  const float* D;
+  const float* delta_bias;
+  const void* z;
+  const int32_t* slots;
+  const float* h0;
+  float* h_last;
+  void* y;
+  int64_t x_row_stride;
+  int64_t delta_row_stride;
+  int64_t B_row_stride;
+  int64_t C_row_stride;
+  int64_t z_row_stride;
+  int64_t y_row_stride;
+  int64_t n_slots;
+} ssm_scan_step_io;
+
+int ssm_selective_scan_step(ssm_scan_t handle, const ssm_scan_dims* dims, const ssm_scan_step_io* io, void* stream);
+
+/* ---- short causal convolution -----------------------------------------
+ *
+ * The depthwise convolution in front of the scan (the conv1d path of the
+ * block in the nxbn.cn article, section 3).  For every row b, channel d and
+ * step t < valid_len[b], over the row's inputs xs behind the width - 1 inputs
+ * carried from before it (conv0; zeros when NULL):
+ *
+ *     p[t] = bias[d] + sum_k weight[d,k] xs[t - (width-1) + k],   y[t] = p[t], or p[t] * sigmoid(p[t]) with silu
+ *
+ *  x, y         [batch, seqlen, dim] io dtype, dim fastest, rows and steps
+ *               x_batch_stride and x_time_stride (...) elements apart (x is
+ *               often one half of a projection's output).  Strides of inputs
+ *               must not be negative; outputs must not overlap themselves.
+ *  weight       [dim, width] fp32, width 2, 3 or 4; bias [dim] fp32 or NULL.
+ *  valid_len    [batch] int32 or NULL, as for the scan: y is +0 past it, and
+ *               nothing there is read.
+ *  conv0        [batch, width - 1, dim] io dtype or NULL, oldest first.
+ *  conv_last    like conv0, or NULL: the last width - 1 inputs of every row
+ *               (its conv0's for the part that a short row does not fill),
+ *               exact copies.
+ *
+ * dim may be any number.  Sizes are below 2^31 (SSM_ERR_UNSUPPORTED).  The
+ * conventions are the scan's: host-side checks first, asynchronous, nothing
+ * allocated, bitwise reproducible, fp32 arithmetic rounded once to the io
+ * dtype. */
+typedef struct ssm_conv_dims {
+  int64_t batch;
+  int64_t seqlen;
+  int64_t dim;
+  int32_t width;
+  int32_t io_dtype;
+  int32_t silu; /* 1: y = p * sigmoid(p); 0: y = p */
+} ssm_conv_dims;
+
+typedef struct ssm_conv_fwd_io {
+  const void* x;
+  const float* weight;
+  const float* bias;
+  const int32_t* valid_len;
+  const void* conv0;
+  void* y;
+  void* conv_last;
+  int64_t x_batch_stride;
+  int64_t x_time_stride;
+  int64_t y_batch_stride;
+  int64_t y_time_stride;
+} ssm_conv_fwd_io;
+
+int ssm_causal_conv_fwd(ssm_scan_t handle, const ssm_conv_dims* dims, const ssm_conv_fwd_io* io, void* stream);
+
+/* Gradients of the convolution for the loss sum(dy * y) + sum(dconv_last *
+ * conv_last); p is recomputed from x.
+ *
+ *  dy, dx       like y and x, with strides of their own; dx is +0 past
+ *               valid_len.
+ *  dconv_last   like conv_last, or NULL (zero).
+ *  dconv0       like conv0, or NULL (not written).
+ *  dweight      [dim, width] fp32;  dbias [dim] fp32 or NULL.
+ *  workspace    at least ssm_causal_conv_bwd_workspace_bytes(dims) bytes of
+ *               device scratch (4-byte aligned), overwritten: sums per
+ *               workgroup that a second kernel adds in a fixed order. */
+typedef struct ssm_conv_bwd_io {
+  const void* x;
+  const float* weight;
+  const float* bias;
+  const int32_t* valid_len;
+  const void* conv0;
+  const void* dy;
+  const void* dconv_last;
+  void* dx;
+  float* dweight;
+  float* dbias;
+  void* dconv0;
+  void* workspace;
+  int64_t workspace_bytes;
+  int64_t x_batch_stride;
+  int64_t x_time_stride;
+  int64_t dy_batch_stride;
+  int64_t dy_time_stride;
+  int64_t dx_batch_stride;
+  int64_t dx_time_stride;
+} ssm_conv_bwd_io;
+
+/* Workspace bytes of ssm_causal_conv_bwd; -1 for NULL or invalid dims. */
+int64_t ssm_causal_conv_bwd_workspace_bytes(const ssm_conv_dims* dims);
+
+int ssm_causal_conv_bwd(ssm_scan_t handle, const ssm_conv_dims* dims, const ssm_conv_bwd_io* io, void* stream);
+
+/* The convolution for single tokens, on a cache of the last width - 1 inputs:
+ * y from the cached inputs and x, and the cache moved on by one.  dims has
+ * seqlen = 1.  x, y [batch, dim] with row strides; conv0 and conv_last
+ * [n_slots, width - 1, dim] (or [batch, ...] without slots), the same buffer
+ * for an update in place; slots and idle rows as in ssm_selective_scan_step. */
+typedef struct ssm_conv_step_io {
+  const void* x;
+  const float* weight;
+  const float* bias;
+  const int32_t* slots;
+  const void* conv0;
+  void* conv_last;
+  void* y;
+  int64_t x_row_stride;
+  int64_t y_row_stride;
+  int64_t n_slots;
+} ssm_conv_step_io;
+
+int ssm_causal_conv_step(ssm_scan_t handle, const ssm_conv_dims* dims, const ssm_conv_step_io* io, void* stream);
+
+/* ---- layer norm and RMS norm ------------------------------------------
+ *
+ * The norm in front of a block, with the residual add: for every row (b, t)
+ * with t < valid_len[b],
+ *
+ *     v = x + residual,  m = mean(v) (rms: 0),  r = 1 / sqrt(mean((v - m)^2) + eps),
+ *     y = (v - m) r weight + bias
+ *
+ *  x, y         [batch, seqlen, dim] io dtype, contiguous.
+ *  residual     like x in residual_dtype, or NULL (zero).
+ *  residual_out like residual, or NULL (not written): v, rounded to
+ *               residual_dtype (y is computed from v before that rounding).
+ *               May be residual itself.
+ *  weight, bias [dim] fp32; bias may be NULL.
+ *  valid_len    [batch] int32 or NULL: rows past it give +0 in every output,
+ *               and their inputs are not read.
+ *  mean, rstd   [batch, seqlen] fp32 or NULL: m and r, for the backward.
+ *
+ * dim is at most 16384, eps positive.  Conventions as above. */
+typedef struct ssm_norm_dims {
+  int64_t batch;
+  int64_t seqlen;
+  int64_t dim;
+  int32_t io_dtype;
+  int32_t residual_dtype; /* SSM_IO_F32, or io_dtype */
+  int32_t rms;            /* 1: no mean is subtracted */
+  float eps;
+} ssm_norm_dims;
+
+typedef struct ssm_norm_fwd_io {
+  const void* x;
+  const void* residual;
+  const float* weight;
+  const float* bias;
+  const int32_t* valid_len;
+  void* y;
+  void* residual_out;
+  float* mean;
+  float* rstd;
+} ssm_norm_fwd_io;
+
+int ssm_layer_norm_fwd(ssm_scan_t handle, const ssm_norm_dims* dims, const ssm_norm_fwd_io* io, void* stream);
+
+/* Gradients of the norm for the loss sum(dy * y) + sum(dresidual_out *
+ * residual_out).
+ *
+ *  dy           like y.
+ *  v            what was normalised, in residual_dtype: the forward's
+ *               residual_out, or x itself (residual_dtype = io_dtype) where
+ *               there was no residual.
+ *  mean, rstd   the forward's (mean may be NULL for rms).
+ *  dresidual_out like v, or NULL (zero).
+ *  dx           like x; dresidual like v, or NULL: the same gradient in the
+ *               two types (x and the residual enter v alike).
+ *  dweight      [dim] fp32;  dbias [dim] fp32 or NULL.
+ *  workspace    at least ssm_layer_norm_bwd_workspace_bytes(dims) bytes of
+ *               device scratch (4-byte aligned), overwritten. */
+typedef struct ssm_norm_bwd_io {
+  const void* dy;
+  const void* v;
+  const float* weight;
+  const float* mean;
+  const float* rstd;
+  const int32_t* valid_len;
+  const void* dresidual_out;
+  void* dx;
+  void* dresidual;
+  float* dweight;
+  float* dbias;
+  void* workspace;
+  int64_t workspace_bytes;
+} ssm_norm_bwd_io;
+
+/* Workspace bytes of ssm_layer_norm_bwd; -1 for NULL or invalid dims. */
+int64_t ssm_layer_norm_bwd_workspace_bytes(const ssm_norm_dims* dims);
+
+int ssm_layer_norm_bwd(ssm_scan_t handle, const ssm_norm_dims* dims, const ssm_norm_bwd_io* io, void* stream);
 
 /* Release the handle.  NULL is accepted.  The caller must ensure no work
  * enqueued with the handle is still to be launched. */

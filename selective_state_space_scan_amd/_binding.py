@@ -34,7 +34,9 @@ SSM_COMBINE_WAVE_SCAN = 1
 EXPORTED = ("ssm_scan_create", "ssm_selective_scan_fwd", "ssm_selective_scan_fwd_ex", "ssm_scan_chunk_len",
             "ssm_scan_auto_time_parts", "ssm_scan_workspace_bytes", "ssm_scan_bwd_chunk_len",
             "ssm_scan_bwd_workspace_bytes", "ssm_selective_scan_bwd", "ssm_scan_destroy", "ssm_scan_error_string",
-            "ssm_selective_scan_fwd_noalloc")
+            "ssm_selective_scan_fwd_noalloc", "ssm_selective_scan_step", "ssm_causal_conv_fwd",
+            "ssm_causal_conv_bwd_workspace_bytes", "ssm_causal_conv_bwd", "ssm_causal_conv_step", "ssm_layer_norm_fwd",
+            "ssm_layer_norm_bwd_workspace_bytes", "ssm_layer_norm_bwd")
 
 
 class SsmScanError(RuntimeError):
@@ -85,6 +87,140 @@ class ssm_scan_bwd_io(ctypes.Structure):
         ("dD", ctypes.c_void_p),
         ("ddelta_bias", ctypes.c_void_p),
         ("dh0", ctypes.c_void_p),
+        ("workspace", ctypes.c_void_p),
+        ("workspace_bytes", ctypes.c_int64),
+    ]
+
+
+class ssm_scan_step_io(ctypes.Structure):
+    _fields_ = [
+        ("x", ctypes.c_void_p),
+        ("delta", ctypes.c_void_p),
+        ("A_log", ctypes.c_void_p),
+        ("B", ctypes.c_void_p),
+        ("C", ctypes.c_void_p),
+        ("D", ctypes.c_void_p),
+        ("delta_bias", ctypes.c_void_p),
+        ("z", ctypes.c_void_p),
+        ("slots", ctypes.c_void_p),
+        ("h0", ctypes.c_void_p),
+        ("h_last", ctypes.c_void_p),
+        ("y", ctypes.c_void_p),
+        ("x_row_stride", ctypes.c_int64),
+        ("delta_row_stride", ctypes.c_int64),
+        ("B_row_stride", ctypes.c_int64),
+        ("C_row_stride", ctypes.c_int64),
+        ("z_row_stride", ctypes.c_int64),
+        ("y_row_stride", ctypes.c_int64),
+        ("n_slots", ctypes.c_int64),
+    ]
+
+
+class ssm_conv_dims(ctypes.Structure):
+    _fields_ = [
+        ("batch", ctypes.c_int64),
+        ("seqlen", ctypes.c_int64),
+        ("dim", ctypes.c_int64),
+        ("width", ctypes.c_int32),
+        ("io_dtype", ctypes.c_int32),
+        ("silu", ctypes.c_int32),
+    ]
+
+
+class ssm_conv_fwd_io(ctypes.Structure):
+    _fields_ = [
+        ("x", ctypes.c_void_p),
+        ("weight", ctypes.c_void_p),
+        ("bias", ctypes.c_void_p),
+        ("valid_len", ctypes.c_void_p),
+        ("conv0", ctypes.c_void_p),
+        ("y", ctypes.c_void_p),
+        ("conv_last", ctypes.c_void_p),
+        ("x_batch_stride", ctypes.c_int64),
+        ("x_time_stride", ctypes.c_int64),
+        ("y_batch_stride", ctypes.c_int64),
+        ("y_time_stride", ctypes.c_int64),
+    ]
+
+
+class ssm_conv_bwd_io(ctypes.Structure):
+    _fields_ = [
+        ("x", ctypes.c_void_p),
+        ("weight", ctypes.c_void_p),
+        ("bias", ctypes.c_void_p),
+        ("valid_len", ctypes.c_void_p),
+        ("conv0", ctypes.c_void_p),
+        ("dy", ctypes.c_void_p),
+        ("dconv_last", ctypes.c_void_p),
+        ("dx", ctypes.c_void_p),
+        ("dweight", ctypes.c_void_p),
+        ("dbias", ctypes.c_void_p),
+        ("dconv0", ctypes.c_void_p),
+        ("workspace", ctypes.c_void_p),
+        ("workspace_bytes", ctypes.c_int64),
+        ("x_batch_stride", ctypes.c_int64),
+        ("x_time_stride", ctypes.c_int64),
+        ("dy_batch_stride", ctypes.c_int64),
+        ("dy_time_stride", ctypes.c_int64),
+        ("dx_batch_stride", ctypes.c_int64),
+        ("dx_time_stride", ctypes.c_int64),
+    ]
+
+
+class ssm_conv_step_io(ctypes.Structure):
+    _fields_ = [
+        ("x", ctypes.c_void_p),
+        ("weight", ctypes.c_void_p),
+        ("bias", ctypes.c_void_p),
+        ("slots", ctypes.c_void_p),
+        ("conv0", ctypes.c_void_p),
+        ("conv_last", ctypes.c_void_p),
+        ("y", ctypes.c_void_p),
+        ("x_row_stride", ctypes.c_int64),
+        ("y_row_stride", ctypes.c_int64),
+        ("n_slots", ctypes.c_int64),
+    ]
+
+
+class ssm_norm_dims(ctypes.Structure):
+    _fields_ = [
+        ("batch", ctypes.c_int64),
+        ("seqlen", ctypes.c_int64),
+        ("dim", ctypes.c_int64),
+        ("io_dtype", ctypes.c_int32),
+        ("residual_dtype", ctypes.c_int32),
+        ("rms", ctypes.c_int32),
+        ("eps", ctypes.c_float),
+    ]
+
+
+class ssm_norm_fwd_io(ctypes.Structure):
+    _fields_ = [
+        ("x", ctypes.c_void_p),
+        ("residual", ctypes.c_void_p),
+        ("weight", ctypes.c_void_p),
+        ("bias", ctypes.c_void_p),
+        ("valid_len", ctypes.c_void_p),
+        ("y", ctypes.c_void_p),
+        ("residual_out", ctypes.c_void_p),
+        ("mean", ctypes.c_void_p),
+        ("rstd", ctypes.c_void_p),
+    ]
+
+
+class ssm_norm_bwd_io(ctypes.Structure):
+    _fields_ = [
+        ("dy", ctypes.c_void_p),
+        ("v", ctypes.c_void_p),
+        ("weight", ctypes.c_void_p),
+        ("mean", ctypes.c_void_p),
+        ("rstd", ctypes.c_void_p),
+        ("valid_len", ctypes.c_void_p),
+        ("dresidual_out", ctypes.c_void_p),
+        ("dx", ctypes.c_void_p),
+        ("dresidual", ctypes.c_void_p),
+        ("dweight", ctypes.c_void_p),
+        ("dbias", ctypes.c_void_p),
         ("workspace", ctypes.c_void_p),
         ("workspace_bytes", ctypes.c_int64),
     ]
@@ -142,6 +278,19 @@ def lib() -> ctypes.CDLL:
         L.ssm_selective_scan_bwd.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, ctypes.POINTER(ssm_scan_dims),
                                              ctypes.POINTER(ssm_scan_fwd_extras), ctypes.POINTER(ssm_scan_bwd_io), vp]
         L.ssm_selective_scan_bwd.restype = ctypes.c_int
+        for name, dims, io in (("selective_scan_step", ssm_scan_dims, ssm_scan_step_io),
+                               ("causal_conv_fwd", ssm_conv_dims, ssm_conv_fwd_io),
+                               ("causal_conv_bwd", ssm_conv_dims, ssm_conv_bwd_io),
+                               ("causal_conv_step", ssm_conv_dims, ssm_conv_step_io),
+                               ("layer_norm_fwd", ssm_norm_dims, ssm_norm_fwd_io),
+                               ("layer_norm_bwd", ssm_norm_dims, ssm_norm_bwd_io)):
+            f = getattr(L, "ssm_" + name)
+            f.argtypes = [vp, ctypes.POINTER(dims), ctypes.POINTER(io), vp]
+            f.restype = ctypes.c_int
+        for name, dims in (("causal_conv", ssm_conv_dims), ("layer_norm", ssm_norm_dims)):
+            f = getattr(L, f"ssm_{name}_bwd_workspace_bytes")
+            f.argtypes = [ctypes.POINTER(dims)]
+            f.restype = ctypes.c_int64
         _lib = L
         return L
 

@@ -1,0 +1,374 @@
+"""torch front end of the operators beside the scan in its block: the scan for
+single tokens, the short causal convolution and the layer or RMS norm.
+
+As for the scan, every step runs in the HIP library; this module checks shapes,
+dtypes and devices, allocates outputs and scratch, and passes device pointers
+and the HIP stream across the C ABI.  There is no fallback.
+"""
+from __future__ import annotations
+
+import ctypes
+
+import torch
+
+from . import _binding as _b
+
+_IO = {torch.float32: _b.SSM_IO_F32, torch.bfloat16: _b.SSM_IO_BF16}
+
+
+def _io(x, what: str = "x") -> int:
+    if x.device.type != "cuda":
+        raise ValueError("tensors must be on a GPU device")
+    io = _IO.get(x.dtype)
+    if io is None:
+        raise TypeError(f"{what} must be float32 or bfloat16")
+    return io
+
+
+def _want(name: str, t, shape: tuple, dtype, dev, contiguous: bool = True) -> None:
+    """Refuses a tensor of another shape, type or device, or one whose last
+    dimension (all of it with ``contiguous``) is not laid out densely."""
+    if t.shape != shape or t.dtype != dtype or t.device != dev:
+        raise ValueError(f"{name} must be {shape} {dtype} on {dev}, got {tuple(t.shape)} {t.dtype} on {t.device}")
+    if contiguous:
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+    elif shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name} must have stride 1 in its last dimension")
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+class _On:
+    """The stream of a call, as a raw handle, with the call's allocations on it
+    (so that the caching allocator orders their reuse after its kernels)."""
+
+    def __init__(self, stream, dev):
+        self.dev = dev
+        if stream is None:  # allocations follow the current stream by themselves
+            self.stream, self.raw = None, torch.cuda.current_stream(dev).cuda_stream
+        else:
+            self.stream = _b._stream_for(stream, dev)
+            self.raw = self.stream.cuda_stream
+
+    def empty(self, shape, dtype):
+        if self.stream is None:
+            return torch.empty(shape, dtype=dtype, device=self.dev)
+        with torch.cuda.stream(self.stream):
+            return torch.empty(shape, dtype=dtype, device=self.dev)
+
+    def scratch(self, given, nbytes: int):
+        if nbytes < 0:
+            raise ValueError("unsupported sizes")
+        if given is None:
+            return self.empty((max(nbytes, 4),), torch.uint8)
+        if (given.dtype != torch.uint8 or given.device != self.dev or not given.is_contiguous()
+                or given.numel() < nbytes):
+            raise ValueError(f"workspace must be a contiguous uint8 tensor of at least {nbytes} bytes on {self.dev}")
+        return given
+
+    def call(self, name: str, dims, io) -> None:
+        fn = getattr(_b.lib(), name)
+        index = self.dev.index
+        if index == torch.cuda.current_device():
+            rc = fn(_b.handle_for(index), ctypes.byref(dims), ctypes.byref(io), self.raw)
+        else:
+            with torch.cuda.device(self.dev):
+                rc = fn(_b.handle_for(index), ctypes.byref(dims), ctypes.byref(io), self.raw)
+        if rc != _b.SSM_OK:
+            raise _b.SsmScanError(rc, name)
+
+
+# ---- single tokens ---------------------------------------------------------
+
+def _cache(name, cache, out, slots, batch: int, shape: tuple, dtype, dev):
+    """Checks a step's cache, where it goes and its slots; (rows, output)."""
+    rows = batch if slots is None else cache.shape[0]
+    _want(name, cache, (rows,) + shape, dtype, dev)
+    if out is None:
+        out = cache
+    elif out is not cache:
+        _want(name + "'s output", out, (rows,) + shape, dtype, dev)
+    if slots is not None:
+        _want("slots", slots, (batch,), torch.int32, dev)
+    return rows, out
+
+
+def selective_scan_step(x, delta, A_log, B, C, D, h, *, slots=None, h_last=None, delta_softplus: bool = True,
+                        delta_clamp=None, delta_bias=None, z=None, y=None, stream=None):
+    """One step of the selective scan for every row of a batch; returns y.
+
+    x, delta: [batch, dim]; B, C: [batch, dstate]; all of one dtype
+    (torch.float32 or torch.bfloat16), rows anywhere (any row stride, last
+    dimension dense).  A_log [dim, dstate], D [dim] or None and delta_bias
+    [dim] or None: float32.  z like x or None: output gate y * silu(z).
+    delta_softplus and delta_clamp as in ``selective_scan_fwd``.
+
+    h: the states, float32, [batch, dim, dstate], or with ``slots`` a cache
+    [n_slots, dim, dstate] of which batch row b uses row slots[b] (int32).  A
+    row whose slot lies outside the cache (-1, say) is idle: no state is touched
+    and its y is 0.  Where rows name one slot, the first takes the step and the
+    others are idle.  The states are updated in place, or with ``h_last`` (like
+    h) written there, the rows in use only.  Asynchronous on ``stream`` (default:
+    the current stream of x's device).
+    """
+    io = _io(x)
+    if x.dim() != 2:
+        raise ValueError("x must be [batch, dim]")
+    dev, dt = x.device, x.dtype
+    nb, nd = x.shape
+    if A_log.dim() != 2 or h.dim() != 3:
+        raise ValueError("A_log must be [dim, dstate] and h [rows, dim, dstate]")
+    N = A_log.shape[1]
+    _want("x", x, (nb, nd), dt, dev, False)
+    _want("delta", delta, (nb, nd), dt, dev, False)
+    _want("B", B, (nb, N), dt, dev, False)
+    _want("C", C, (nb, N), dt, dev, False)
+    _want("A_log", A_log, (nd, N), torch.float32, dev)
+    if D is not None:
+        _want("D", D, (nd,), torch.float32, dev)
+    if delta_bias is not None:
+        _want("delta_bias", delta_bias, (nd,), torch.float32, dev)
+    if z is not None:
+        _want("z", z, (nb, nd), dt, dev, False)
+    rows, h_last = _cache("h", h, h_last, slots, nb, (nd, N), torch.float32, dev)
+    on = _On(stream, dev)
+    if y is None:
+        y = on.empty((nb, nd), dt)
+    else:
+        _want("y", y, (nb, nd), dt, dev, False)
+    lo, hi = (0.0, 0.0) if delta_clamp is None else delta_clamp
+    dims = _b.ssm_scan_dims(nb, 1, nd, N, io, 1 if delta_softplus else 0, 0 if delta_clamp is None else 1, lo, hi)
+    args = _b.ssm_scan_step_io(x.data_ptr(), delta.data_ptr(), A_log.data_ptr(), B.data_ptr(), C.data_ptr(), _ptr(D),
+                               _ptr(delta_bias), _ptr(z), _ptr(slots), h.data_ptr(), h_last.data_ptr(), y.data_ptr(),
+                               x.stride(0), delta.stride(0), B.stride(0), C.stride(0),
+                               0 if z is None else z.stride(0), y.stride(0), rows)
+    on.call("ssm_selective_scan_step", dims, args)
+    return y
+
+
+def causal_conv_step(x, conv, weight, bias=None, *, silu: bool = True, slots=None, conv_last=None, y=None,
+                     stream=None):
+    """One step of the short causal convolution for every row of a batch; returns y.
+
+    x: [batch, dim] float32 or bfloat16, any row stride.  conv: the last
+    width - 1 inputs of every row, oldest first, [batch, width - 1, dim] in x's
+    dtype, or with ``slots`` a cache [n_slots, width - 1, dim]; it is moved on by
+    one in place, or with ``conv_last`` (like conv) written there.  slots and
+    idle rows as in ``selective_scan_step``.  weight [dim, width] (2, 3 or 4 taps)
+    and bias [dim] or None: float32.  silu: y = p * sigmoid(p).
+    """
+    io = _io(x)
+    if x.dim() != 2:
+        raise ValueError("x must be [batch, dim]")
+    dev, dt = x.device, x.dtype
+    nb, nd = x.shape
+    if weight.dim() != 2 or conv.dim() != 3:
+        raise ValueError("weight must be [dim, width] and conv [rows, width - 1, dim]")
+    W = weight.shape[1]
+    _want("x", x, (nb, nd), dt, dev, False)
+    _want("weight", weight, (nd, W), torch.float32, dev)
+    if bias is not None:
+        _want("bias", bias, (nd,), torch.float32, dev)
+    rows, conv_last = _cache("conv", conv, conv_last, slots, nb, (W - 1, nd), dt, dev)
+    on = _On(stream, dev)
+    if y is None:
+        y = on.empty((nb, nd), dt)
+    else:
+        _want("y", y, (nb, nd), dt, dev, False)
+    args = _b.ssm_conv_step_io(x.data_ptr(), weight.data_ptr(), _ptr(bias), _ptr(slots), conv.data_ptr(),
+                               conv_last.data_ptr(), y.data_ptr(), x.stride(0), y.stride(0), rows)
+    on.call("ssm_causal_conv_step", _b.ssm_conv_dims(nb, 1, nd, W, io, 1 if silu else 0), args)
+    return y
+
+
+# ---- short causal convolution ----------------------------------------------
+
+def _conv_shapes(x, weight, bias, valid_len, conv0):
+    if x.dim() != 3:
+        raise ValueError("x must be [batch, L, dim]")
+    if weight.dim() != 2:
+        raise ValueError("weight must be [dim, width]")
+    dev, dt = x.device, x.dtype
+    nb, L, nd = x.shape
+    W = weight.shape[1]
+    _want("x", x, (nb, L, nd), dt, dev, False)
+    _want("weight", weight, (nd, W), torch.float32, dev)
+    if bias is not None:
+        _want("bias", bias, (nd,), torch.float32, dev)
+    if valid_len is not None:
+        _want("valid_len", valid_len, (nb,), torch.int32, dev)
+    if conv0 is not None:
+        _want("conv0", conv0, (nb, W - 1, nd), dt, dev)
+    return nb, L, nd, W
+
+
+def causal_conv_fwd(x, weight, bias=None, valid_len=None, *, silu: bool = True, conv0=None, y=None, conv_last=None,
+                    return_conv_last: bool = True, stream=None):
+    """Short causal convolution of every channel, with silu; returns ``(y, conv_last)``.
+
+    x: [batch, L, dim] float32 or bfloat16, last dimension dense, other strides
+    any (one half of a projection's output, say).  weight [dim, width] (2, 3 or
+    4 taps, the last on the current step) and bias [dim] or None: float32.
+    valid_len [batch] int32 or None: y is 0 past it and nothing there is read.
+    conv0 [batch, width - 1, dim] like x: the inputs before the first, oldest
+    first (zeros if None).  conv_last, likewise: the last width - 1 inputs of
+    every row, to continue from (None if return_conv_last is False and none is
+    given).  Outputs are allocated unless given; y may be strided like x.
+    Asynchronous on ``stream``.
+    """
+    io = _io(x)
+    nb, L, nd, W = _conv_shapes(x, weight, bias, valid_len, conv0)
+    dev, dt = x.device, x.dtype
+    on = _On(stream, dev)
+    if y is None:
+        y = on.empty((nb, L, nd), dt)
+    else:
+        _want("y", y, (nb, L, nd), dt, dev, False)
+    if conv_last is not None:
+        _want("conv_last", conv_last, (nb, W - 1, nd), dt, dev)
+    elif return_conv_last:
+        conv_last = on.empty((nb, W - 1, nd), dt)
+    args = _b.ssm_conv_fwd_io(x.data_ptr(), weight.data_ptr(), _ptr(bias), _ptr(valid_len), _ptr(conv0), y.data_ptr(),
+                              _ptr(conv_last), x.stride(0), x.stride(1), y.stride(0), y.stride(1))
+    on.call("ssm_causal_conv_fwd", _b.ssm_conv_dims(nb, L, nd, W, io, 1 if silu else 0), args)
+    return y, conv_last
+
+
+def causal_conv_bwd(x, weight, bias, valid_len, dy, *, silu: bool = True, conv0=None, dconv_last=None, dx=None,
+                    workspace=None, stream=None) -> dict:
+    """Gradients of ``causal_conv_fwd`` for the loss sum(dy * y) + sum(dconv_last * conv_last).
+
+    The forward's inputs and flags must be given again.  dy like y (any
+    strides, last dimension dense); dconv_last like conv_last or None.  Returns
+    a dict: dx like x (contiguous unless given, strided like x then), dweight
+    [dim, width], dbias [dim] (None without bias), both float32, and dconv0
+    [batch, width - 1, dim] in x's dtype (None without conv0).
+    """
+    io = _io(x)
+    nb, L, nd, W = _conv_shapes(x, weight, bias, valid_len, conv0)
+    dev, dt = x.device, x.dtype
+    _want("dy", dy, (nb, L, nd), dt, dev, False)
+    if dconv_last is not None:
+        _want("dconv_last", dconv_last, (nb, W - 1, nd), dt, dev)
+    on = _On(stream, dev)
+    if dx is None:
+        dx = on.empty((nb, L, nd), dt)
+    else:
+        _want("dx", dx, (nb, L, nd), dt, dev, False)
+    dweight = on.empty((nd, W), torch.float32)
+    dbias = None if bias is None else on.empty((nd,), torch.float32)
+    dconv0 = None if conv0 is None else on.empty((nb, W - 1, nd), dt)
+    dims = _b.ssm_conv_dims(nb, L, nd, W, io, 1 if silu else 0)
+    ws = on.scratch(workspace, _b.lib().ssm_causal_conv_bwd_workspace_bytes(ctypes.byref(dims)))
+    args = _b.ssm_conv_bwd_io(x.data_ptr(), weight.data_ptr(), _ptr(bias), _ptr(valid_len), _ptr(conv0), dy.data_ptr(),
+                              _ptr(dconv_last), dx.data_ptr(), dweight.data_ptr(), _ptr(dbias), _ptr(dconv0),
+                              ws.data_ptr(), ws.numel(), x.stride(0), x.stride(1), dy.stride(0), dy.stride(1),
+                              dx.stride(0), dx.stride(1))
+    on.call("ssm_causal_conv_bwd", dims, args)
+    return dict(dx=dx, dweight=dweight, dbias=dbias, dconv0=dconv0)
+
+
+# ---- norms -----------------------------------------------------------------
+
+def _norm_shape(x, weight, valid_len):
+    if x.dim() not in (2, 3):
+        raise ValueError("rows must be [rows, dim] or [batch, L, dim]")
+    if valid_len is not None and x.dim() != 3:
+        raise ValueError("valid_len needs rows laid out as [batch, L, dim]")
+    nd = x.shape[-1]
+    nb, L = (x.shape[0], 1) if x.dim() == 2 else (x.shape[0], x.shape[1])
+    _want("weight", weight, (nd,), torch.float32, x.device)
+    if valid_len is not None:
+        _want("valid_len", valid_len, (nb,), torch.int32, x.device)
+    return nb, L, nd
+
+
+def layer_norm_fwd(x, weight, bias=None, valid_len=None, *, residual=None, eps: float = 1e-5, rms: bool = False,
+                   y=None, residual_out=None, return_stats: bool = False, stream=None):
+    """Layer norm (RMS norm with ``rms``) of x + residual over the last dimension.
+
+    x: [rows, dim] or [batch, L, dim], float32 or bfloat16, contiguous, dim at
+    most 16384.  residual like x, in x's dtype or float32, or None.  weight and
+    bias (or None): [dim] float32.  valid_len [batch] int32 or None (for
+    [batch, L, dim]): rows past it give 0 and are not read.
+
+    Returns ``(y, residual_out)``, or ``(y, residual_out, mean, rstd)`` with
+    ``return_stats`` (float32, what the backward takes; mean is None with rms).
+    residual_out is x + residual in residual's dtype (None without residual);
+    it may be given, as residual itself for an update in place, or without a
+    residual to start a residual stream in its own dtype.
+    """
+    io = _io(x)
+    nb, L, nd = _norm_shape(x, weight, valid_len)
+    dev, dt, shape = x.device, x.dtype, tuple(x.shape)
+    _want("x", x, shape, dt, dev)
+    if bias is not None:
+        _want("bias", bias, (nd,), torch.float32, dev)
+    like = residual if residual is not None else residual_out
+    rdt = dt if like is None else like.dtype
+    if rdt != dt and rdt != torch.float32:
+        raise TypeError("residual must be float32 or of x's dtype")
+    if residual is not None:
+        _want("residual", residual, shape, rdt, dev)
+    on = _On(stream, dev)
+    if y is None:
+        y = on.empty(shape, dt)
+    else:
+        _want("y", y, shape, dt, dev)
+    if residual_out is not None:
+        _want("residual_out", residual_out, shape, rdt, dev)
+    elif residual is not None:
+        residual_out = on.empty(shape, rdt)
+    mean = rstd = None
+    if return_stats:
+        rstd = on.empty(shape[:-1], torch.float32)
+        if not rms:
+            mean = on.empty(shape[:-1], torch.float32)
+    dims = _b.ssm_norm_dims(nb, L, nd, io, _IO[rdt], 1 if rms else 0, eps)
+    args = _b.ssm_norm_fwd_io(x.data_ptr(), _ptr(residual), weight.data_ptr(), _ptr(bias), _ptr(valid_len),
+                              y.data_ptr(), _ptr(residual_out), _ptr(mean), _ptr(rstd))
+    on.call("ssm_layer_norm_fwd", dims, args)
+    return (y, residual_out, mean, rstd) if return_stats else (y, residual_out)
+
+
+def layer_norm_bwd(dy, v, weight, mean, rstd, valid_len=None, *, dresidual_out=None, with_bias: bool = True,
+                   with_residual: bool | None = None, workspace=None, stream=None) -> dict:
+    """Gradients of ``layer_norm_fwd`` for the loss sum(dy * y) + sum(dresidual_out * residual_out).
+
+    dy like y.  v: what was normalised, the forward's residual_out (or x where
+    there was none).  mean and rstd: the forward's; mean None for RMS norm.
+    dresidual_out like v or None.  Returns a dict: dx like dy; dresidual like v
+    (the same gradient in v's dtype, and the same tensor where the dtypes are
+    one; None unless ``with_residual``, which follows dresidual_out if None);
+    dweight and dbias (None without ``with_bias``) [dim] float32.
+    """
+    io = _io(dy, "dy")
+    nb, L, nd = _norm_shape(dy, weight, valid_len)
+    dev, dt, shape = dy.device, dy.dtype, tuple(dy.shape)
+    if v.dtype != dt and v.dtype != torch.float32:
+        raise TypeError("v must be float32 or of dy's dtype")
+    _want("dy", dy, shape, dt, dev)
+    _want("v", v, shape, v.dtype, dev)
+    if mean is not None:
+        _want("mean", mean, shape[:-1], torch.float32, dev)
+    _want("rstd", rstd, shape[:-1], torch.float32, dev)
+    if dresidual_out is not None:
+        _want("dresidual_out", dresidual_out, shape, v.dtype, dev)
+    on = _On(stream, dev)
+    dx = on.empty(shape, dt)
+    wanted = dresidual_out is not None if with_residual is None else with_residual
+    apart = wanted and v.dtype != dt
+    dresidual = on.empty(shape, v.dtype) if apart else None
+    dweight = on.empty((nd,), torch.float32)
+    dbias = on.empty((nd,), torch.float32) if with_bias else None
+    # eps went into rstd; the library wants a positive one all the same
+    dims = _b.ssm_norm_dims(nb, L, nd, io, _IO[v.dtype], 1 if mean is None else 0, 1.0)
+    ws = on.scratch(workspace, _b.lib().ssm_layer_norm_bwd_workspace_bytes(ctypes.byref(dims)))
+    args = _b.ssm_norm_bwd_io(dy.data_ptr(), v.data_ptr(), weight.data_ptr(), _ptr(mean), rstd.data_ptr(),
+                              _ptr(valid_len), _ptr(dresidual_out), dx.data_ptr(), _ptr(dresidual), dweight.data_ptr(),
+                              _ptr(dbias), ws.data_ptr(), ws.numel())
+    on.call("ssm_layer_norm_bwd", dims, args)
+    return dict(dx=dx, dresidual=dresidual if apart else (dx if wanted else None), dweight=dweight, dbias=dbias)

@@ -17,7 +17,8 @@ import tempfile
 
 PKG_DIR = os.path.dirname(os.path.abspath(__file__))
 REPO_DIR = os.path.dirname(PKG_DIR)
-SRCS = [os.path.join(PKG_DIR, "csrc", f) for f in ("ssm_scan.hip", "ssm_scan_bwd.hip")]
+SRCS = [os.path.join(PKG_DIR, "csrc", f) for f in ("ssm_scan.hip", "ssm_scan_bwd.hip", "ssm_step.hip", "ssm_conv.hip",
+                                                 "ssm_norm.hip")]
 INCLUDE_DIR = os.path.join(REPO_DIR, "include")
 LIB_PATH = os.path.join(PKG_DIR, "libssmscan.so")
 # The peak-rate microbenchmarks the benchmark measures the roofline with: a

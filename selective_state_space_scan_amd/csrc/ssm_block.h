@@ -1,0 +1,284 @@
+// Internals shared by the operators around the scan (short convolution,
+// single-token steps, norms): vector access at any alignment, activations,
+// wave reductions, and the host's argument checks.
+#pragma once
+
+#include "ssm_internal.h"
+#include "ssm_scan.h"
+
+namespace {
+
+// ---- vector access -------------------------------------------------------
+//
+// A lane moves V consecutive elements (16 bytes) of a row at once.  Rows start
+// wherever strides and odd widths put them, so the vector types carry only
+// their element's alignment; gfx950 code objects run in unaligned access mode
+// and the compiler emits one 16-byte instruction for them all the same.  A
+// row's last n < V elements are moved one by one.
+
+template <typename IO>
+struct VecIO;
+
+template <>
+struct VecIO<float> {
+  static constexpr int kWide = 4;
+  typedef float vec4 __attribute__((ext_vector_type(4), aligned(4)));
+  template <int V>
+  static __device__ __forceinline__ void load(const float* p, float (&o)[V]) {
+    static_assert(V % 4 == 0, "whole 16-byte pieces");
+#pragma unroll
+    for (int i = 0; i < V; i += 4) {
+      const vec4 v = *reinterpret_cast<const vec4*>(p + i);
+      o[i] = v.x, o[i + 1] = v.y, o[i + 2] = v.z, o[i + 3] = v.w;
+    }
+  }
+  template <int V>
+  static __device__ __forceinline__ void store(float* p, const float (&o)[V]) {
+#pragma unroll
+    for (int i = 0; i < V; i += 4) {
+      vec4 v;
+      v.x = o[i], v.y = o[i + 1], v.z = o[i + 2], v.w = o[i + 3];
+      *reinterpret_cast<vec4*>(p + i) = v;
+    }
+  }
+  static __device__ __forceinline__ float get(const float* p) { return *p; }
+  static __device__ __forceinline__ void put(float* p, float v) { *p = v; }
+};
+
+// bf16 is carried as its 16-bit pattern; widening to fp32 is exact, narrowing
+// rounds to nearest even.
+template <>
+struct VecIO<uint16_t> {
+  static constexpr int kWide = 8;
+  typedef uint32_t vec4 __attribute__((ext_vector_type(4), aligned(2)));
+  typedef uint32_t vec2 __attribute__((ext_vector_type(2), aligned(2)));
+  static __device__ __forceinline__ float lo(uint32_t u) { return __builtin_bit_cast(float, u << 16); }
+  static __device__ __forceinline__ float hi(uint32_t u) { return __builtin_bit_cast(float, u & 0xffff0000u); }
+  static __device__ __forceinline__ uint16_t narrow(float v) {
+    return __builtin_bit_cast(uint16_t, static_cast<__bf16>(v));
+  }
+  static __device__ __forceinline__ uint32_t pack(float a, float b) {
+    return static_cast<uint32_t>(narrow(a)) | (static_cast<uint32_t>(narrow(b)) << 16);
+  }
+  template <int V>
+  static __device__ __forceinline__ void load(const uint16_t* p, float (&o)[V]) {
+    static_assert(V % 8 == 0 || V == 4, "whole 16- or 8-byte pieces");
+    if constexpr (V == 4) {
+      const vec2 v = *reinterpret_cast<const vec2*>(p);
+      o[0] = lo(v.x), o[1] = hi(v.x), o[2] = lo(v.y), o[3] = hi(v.y);
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; i += 8) {
+        const vec4 v = *reinterpret_cast<const vec4*>(p + i);
+        o[i] = lo(v.x), o[i + 1] = hi(v.x), o[i + 2] = lo(v.y), o[i + 3] = hi(v.y);
+        o[i + 4] = lo(v.z), o[i + 5] = hi(v.z), o[i + 6] = lo(v.w), o[i + 7] = hi(v.w);
+      }
+    }
+  }
+  template <int V>
+  static __device__ __forceinline__ void store(uint16_t* p, const float (&o)[V]) {
+    if constexpr (V == 4) {
+      vec2 v;
+      v.x = pack(o[0], o[1]), v.y = pack(o[2], o[3]);
+      *reinterpret_cast<vec2*>(p) = v;
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; i += 8) {
+        vec4 v;
+        v.x = pack(o[i], o[i + 1]), v.y = pack(o[i + 2], o[i + 3]);
+        v.z = pack(o[i + 4], o[i + 5]), v.w = pack(o[i + 6], o[i + 7]);
+        *reinterpret_cast<vec4*>(p + i) = v;
+      }
+    }
+  }
+  static __device__ __forceinline__ float get(const uint16_t* p) {
+    return __builtin_bit_cast(float, static_cast<uint32_t>(*p) << 16);
+  }
+  static __device__ __forceinline__ void put(uint16_t* p, float v) { *p = narrow(v); }
+};
+
+// The first n (0 <= n <= V) of V elements; the others read as zero and are not
+// written.
+template <typename IO, int V>
+__device__ __forceinline__ void load_n(const IO* p, int n, float (&o)[V]) {
+  if (n == V) {
+    VecIO<IO>::load(p, o);
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) o[i] = i < n ? VecIO<IO>::get(p + i) : 0.0f;
+  }
+}
+template <typename IO, int V>
+__device__ __forceinline__ void store_n(IO* p, int n, const float (&o)[V]) {
+  if (n == V) {
+    VecIO<IO>::store(p, o);
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (i < n) VecIO<IO>::put(p + i, o[i]);
+  }
+}
+
+// ---- activations ---------------------------------------------------------
+
+// sigmoid(v) = 1 / (1 + e^-v).  v_exp_f32 is 2^x: the rounding error of
+// v * log2(e), which would grow with |v| in the result, is recovered by an FMA
+// with the constant's low part and put back as a first-order factor.  |v| is
+// cut at 110, where e^-v has long left fp32's range (2^158.7 is infinite, and
+// the result 0), so that infinities stay out of the correction.
+__device__ __forceinline__ float sigmoid_exact(float v) {
+  constexpr float kLog2eLow = 1.925962991e-8f;  // log2(e) - kLog2e
+  const float c = __builtin_fminf(__builtin_fmaxf(v, -110.0f), 110.0f);
+  const float t = -c * kLog2e;
+  const float r = __builtin_fmaf(-c, kLog2e, -t) - c * kLog2eLow;
+  const float e = fast_exp2(t);
+  return __builtin_amdgcn_rcpf(__builtin_fmaf(e, __builtin_fmaf(r, kLn2, 1.0f), 1.0f));
+}
+
+// ---- wave reductions -----------------------------------------------------
+
+template <int CTRL>
+__device__ __forceinline__ float dpp_move(float v) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, v), CTRL, 0xf, 0xf, true));
+}
+
+// Sum over aligned groups of LANES (4, 8 or 16) consecutive lanes; every lane
+// of the group gets the total.  quad_perm [1,0,3,2] and [2,3,0,1], then
+// row_half_mirror (the other quad of eight lanes) and row_mirror (the other
+// eight of a row).
+template <int LANES>
+__device__ __forceinline__ float group_sum(float v) {
+  static_assert(LANES == 4 || LANES == 8 || LANES == 16, "within a row of 16 lanes");
+  v += dpp_move<0xB1>(v);
+  v += dpp_move<0x4E>(v);
+  if constexpr (LANES >= 8) v += dpp_move<0x141>(v);
+  if constexpr (LANES >= 16) v += dpp_move<0x140>(v);
+  return v;
+}
+
+// Sum over the 64 lanes of a wave; every lane gets the total.
+__device__ __forceinline__ float wave_sum(float v) {
+  v = group_sum<16>(v);
+  float a, b;
+  rows_swap16(v, a, b);
+  v = a + b;
+  rows_swap32(v, a, b);
+  return a + b;
+}
+
+// ---- steps on a cache ------------------------------------------------------
+
+// Whether batch row b of a single-token step runs on cache row `slot`: not if
+// it lies outside the cache (rows that pad the batch carry -1), nor if an
+// earlier batch row names the same cache row, whose update then stands alone
+// (two rows updating one would race).  Called by every thread of the workgroup
+// (it contains a barrier when slots are given).
+__device__ __forceinline__ bool step_row_active(const int32_t* slots, int64_t b, int64_t slot, int64_t n_slots) {
+  if (slots == nullptr) return true;
+  bool taken = false;
+  for (int64_t i = threadIdx.x; i < b; i += blockDim.x) taken |= slots[i] == slot;
+  return !__syncthreads_or(taken) && slot >= 0 && slot < n_slots;
+}
+
+// ---- host checks ---------------------------------------------------------
+
+// HIP counts a launch's work-items per dimension in 32 bits.
+inline bool grid_fits(int64_t blocks, int threads) { return blocks > 0 && blocks <= 0xffffffffLL / threads; }
+
+constexpr int64_t kMaxSize = 0x7fffffffLL;
+
+// Bytes from a strided [n0, n1, dim] tensor's first element to behind its last
+// (dim fastest, strides in elements); -1 if a stride is negative or the span
+// leaves 62 bits.
+inline int64_t span_bytes(int64_t n0, int64_t s0, int64_t n1, int64_t s1, int64_t dim, int64_t e) {
+  if (s0 < 0 || s1 < 0) return -1;
+  if (n0 == 0 || n1 == 0 || dim == 0) return 0;
+  const __int128 n = static_cast<__int128>(n0 - 1) * s0 + static_cast<__int128>(n1 - 1) * s1 + dim;
+  return n * e < (static_cast<__int128>(1) << 62) ? static_cast<int64_t>(n * e) : -1;
+}
+
+// Whether no two elements of a strided [n0, n1, dim] tensor share an address:
+// the outer dimension with the smaller stride steps over whole rows, the other
+// over all of those.
+inline bool rows_disjoint(int64_t n0, int64_t s0, int64_t n1, int64_t s1, int64_t dim) {
+  if (n0 <= 1 && n1 <= 1) return true;
+  if (n0 <= 1) return s1 >= dim;
+  if (n1 <= 1) return s0 >= dim;
+  const int64_t ns = s0 < s1 ? n0 : n1, ss = s0 < s1 ? s0 : s1, sl = s0 < s1 ? s1 : s0;
+  return ss >= dim && static_cast<__int128>(sl) >= static_cast<__int128>(ns - 1) * ss + dim;
+}
+
+// A byte range a call reads or writes.
+struct Range {
+  const void* p;
+  int64_t n;
+};
+
+// Whether an output overlaps an input or another output.
+template <int NI, int NO>
+inline bool any_overlap(const Range (&in)[NI], const Range (&out)[NO]) {
+  for (int o = 0; o < NO; ++o) {
+    for (int i = 0; i < NI; ++i)
+      if (overlaps(out[o].p, static_cast<size_t>(out[o].n), in[i].p, static_cast<size_t>(in[i].n))) return true;
+    for (int k = 0; k < o; ++k)
+      if (overlaps(out[o].p, static_cast<size_t>(out[o].n), out[k].p, static_cast<size_t>(out[k].n))) return true;
+  }
+  return false;
+}
+
+// The handle, and that the calling thread's current device is the handle's.
+inline int check_handle(ssm_scan_t handle) {
+  if (handle == nullptr) return SSM_ERR_INVALID_ARG;
+  int cur = -1;
+  if (hipGetDevice(&cur) != hipSuccess) {
+    (void)hipGetLastError();
+    return SSM_ERR_HIP;
+  }
+  return cur == handle->device ? SSM_OK : SSM_ERR_DEVICE_MISMATCH;
+}
+
+inline int launched() { return hipGetLastError() == hipSuccess ? SSM_OK : SSM_ERR_HIP; }
+
+// ---- partial sums --------------------------------------------------------
+
+// out(c) = sum over p of ws[p * cols + c]: the second pass of a weight
+// gradient, whose first pass left one row of sums per workgroup.  A workgroup
+// of 1024 takes 16 columns (64 bytes of a row) and 64 row lanes; each lane
+// adds every 64th row, eight loads in flight, and LDS joins the lanes in a
+// fixed order, so the result does not depend on timing.
+constexpr int kReduceCols = 16, kReduceLanes = 64;
+
+template <typename Out>
+__global__ __launch_bounds__(kReduceCols * kReduceLanes) void reduce_partials_kernel(const float* ws, int64_t parts,
+                                                                                    int64_t cols, Out out) {
+  __shared__ float lds[kReduceLanes][kReduceCols + 1];
+  const int c = threadIdx.x % kReduceCols, r = threadIdx.x / kReduceCols;
+  const int64_t col = static_cast<int64_t>(blockIdx.x) * kReduceCols + c;
+  float sum = 0.0f;
+  if (col < cols) {
+    int64_t p = r;
+    for (; p + 7 * kReduceLanes < parts; p += 8 * kReduceLanes) {
+      float v[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = ws[(p + i * kReduceLanes) * cols + col];
+      sum += ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7]));
+    }
+    for (; p < parts; p += kReduceLanes) sum += ws[p * cols + col];
+  }
+  lds[r][c] = sum;
+  __syncthreads();
+#pragma unroll
+  for (int half = kReduceLanes / 2; half > 0; half /= 2) {
+    if (r < half) lds[r][c] += lds[r + half][c];
+    __syncthreads();
+  }
+  if (r == 0 && col < cols) out(col, lds[0][c]);
+}
+
+template <typename Out>
+inline void launch_reduce(const float* ws, int64_t parts, int64_t cols, const Out& out, hipStream_t s) {
+  hipLaunchKernelGGL(reduce_partials_kernel<Out>, dim3(static_cast<unsigned>((cols + kReduceCols - 1) / kReduceCols)),
+                     dim3(kReduceCols * kReduceLanes), 0, s, ws, parts, cols, out);
+}
+
+}  // namespace

@@ -1,0 +1,585 @@
+// The short causal convolution in front of the scan, for MI355X (gfx950):
+// forward, backward, and one step on a cache.
+//
+// For every batch row b, channel d and step t < valid_len[b], with W taps:
+//
+//     p[t] = bias[d] + sum_k w[d,k] * xs[t - (W-1) + k],   y[t] = p or p * sigmoid(p)
+//
+// xs is the row's input behind the W-1 inputs carried from before it (or
+// zeros).  Each channel is its own convolution, so there is nothing for the
+// matrix units: 2W operations on 2 elements moved, bound by memory.
+//
+// Backward, with g[t] = dy[t] * (dy/dp)(p[t]) and g = 0 outside [0, valid_len):
+//
+//     dxs[t] = sum_k w[k] * g[t + (W-1) - k],  dw[k] = sum_{b,t} g[t] * xs[t - (W-1) + k],  dbias = sum_{b,t} g[t]
+//
+// Layout: dim is fastest, so a lane owns 16 bytes of adjacent channels and
+// walks a chunk of steps with the last W-1 inputs in registers; lanes of a
+// wave take adjacent pieces (1 KB of a row at a time).  Only the W-1 inputs in
+// front of a chunk are read twice.
+
+#include <hip/hip_runtime.h>
+
+#include <cstdint>
+
+#include "ssm_block.h"
+
+namespace {
+
+struct ConvParams {
+  const void* x;
+  const float* w;
+  const float* bias;
+  const int32_t* valid_len;
+  const void* conv0;
+  void* y;
+  void* conv_last;
+  int64_t x_bs, x_ts, y_bs, y_ts;
+  int64_t L, n_chunks, items;
+  int32_t nd, n_vec, T;
+};
+
+struct ConvBwdParams {
+  const void* x;
+  const float* w;
+  const float* bias;
+  const int32_t* valid_len;
+  const void* conv0;
+  const void* dy;
+  const void* dconv_last;
+  void* dx;
+  void* dconv0;
+  float* ws;
+  int64_t x_bs, x_ts, dy_bs, dy_ts, dx_bs, dx_ts;
+  int64_t L, n_groups;
+  int32_t nd, n_vec, T, cx, n_tiles;
+};
+
+struct ConvStepParams {
+  const void* x;
+  const float* w;
+  const float* bias;
+  const int32_t* slots;
+  const void* conv0;
+  void* conv_last;
+  void* y;
+  int64_t x_rs, y_rs, n_slots;
+  int32_t nd, n_vec;
+};
+
+__device__ __forceinline__ int64_t row_len(const int32_t* valid_len, int64_t b, int64_t L) {
+  if (valid_len == nullptr) return L;
+  const int64_t n = valid_len[b];
+  return n < 0 ? 0 : (n > L ? L : n);
+}
+
+template <int W, int V>
+struct Taps {
+  float w[W][V];
+  float bias[V];
+  __device__ __forceinline__ void load(const float* wp, const float* bp, int64_t d, int n) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+#pragma unroll
+      for (int k = 0; k < W; ++k) w[k][i] = i < n ? wp[(d + i) * W + k] : 0.0f;
+    }
+    if (bp != nullptr) {
+      load_n<float, V>(bp + d, n, bias);
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; ++i) bias[i] = 0.0f;
+    }
+  }
+  // p from the W inputs that end with this step's
+  __device__ __forceinline__ void apply(const float (&xs)[W][V], float (&p)[V]) const {
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      p[i] = bias[i];
+#pragma unroll
+      for (int k = 0; k < W; ++k) p[i] = __builtin_fmaf(w[k][i], xs[k][i], p[i]);
+    }
+  }
+};
+
+template <int W, int V>
+__device__ __forceinline__ void shift(float (&xs)[W][V]) {
+#pragma unroll
+  for (int k = 0; k + 1 < W; ++k) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) xs[k][i] = xs[k + 1][i];
+  }
+}
+
+// The input of step t (t >= -(W-1)) of a row; zeros where nothing is carried.
+template <typename IO, int W, int V>
+__device__ __forceinline__ void input_at(const IO* x, const IO* conv0, int64_t t, int64_t x_ts, int64_t nd, int n,
+                                         float (&o)[V]) {
+  if (t >= 0) {
+    load_n<IO, V>(x + t * x_ts, n, o);
+  } else if (conv0 != nullptr) {
+    load_n<IO, V>(conv0 + (W - 1 + t) * nd, n, o);
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) o[i] = 0.0f;
+  }
+}
+
+// ---- forward ---------------------------------------------------------------
+
+// One lane: T steps of V channels.  Chunks, not channels, run over the grid's
+// slow index, so that a workgroup's lanes cover whole rows where dim allows.
+template <typename IO, int W, bool SILU>
+__global__ __launch_bounds__(256) void conv_fwd_kernel(const ConvParams prm) {
+  constexpr int V = VecIO<IO>::kWide;
+  const int64_t item = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  if (item >= prm.items) return;
+  const int64_t row = item / prm.n_vec;
+  const int64_t d = (item - row * prm.n_vec) * V;
+  const int64_t b = row / prm.n_chunks, c0 = (row - b * prm.n_chunks) * prm.T;
+  const int n = prm.nd - d < V ? static_cast<int>(prm.nd - d) : V;
+  const int64_t len = row_len(prm.valid_len, b, prm.L);
+  const IO* x = static_cast<const IO*>(prm.x) + b * prm.x_bs + d;
+  const IO* conv0 = prm.conv0 == nullptr ? nullptr : static_cast<const IO*>(prm.conv0) + b * (W - 1) * prm.nd + d;
+  IO* y = static_cast<IO*>(prm.y) + b * prm.y_bs + d;
+
+  const int64_t c1 = c0 + prm.T < prm.L ? c0 + prm.T : prm.L;
+  const int64_t v1 = c1 < len ? c1 : len;
+  if (v1 > c0) {
+    Taps<W, V> taps;
+    taps.load(prm.w, prm.bias, d, n);
+    float xs[W][V];
+#pragma unroll
+    for (int k = 0; k + 1 < W; ++k) input_at<IO, W, V>(x, conv0, c0 - (W - 1) + k, prm.x_ts, prm.nd, n, xs[k]);
+#pragma unroll 4
+    for (int64_t t = c0; t < v1; ++t) {
+      load_n<IO, V>(x + t * prm.x_ts, n, xs[W - 1]);
+      float p[V];
+      taps.apply(xs, p);
+      if constexpr (SILU) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) p[i] *= sigmoid_exact(p[i]);
+      }
+      store_n<IO, V>(y + t * prm.y_ts, n, p);
+      shift<W, V>(xs);
+    }
+  }
+  const float zero[V] = {};
+  for (int64_t t = v1 > c0 ? v1 : c0; t < c1; ++t) store_n<IO, V>(y + t * prm.y_ts, n, zero);
+
+  // The row's last W-1 inputs, by the lanes of its first chunk.
+  if (c0 == 0 && prm.conv_last != nullptr) {
+    IO* last = static_cast<IO*>(prm.conv_last) + b * (W - 1) * prm.nd + d;
+#pragma unroll
+    for (int k = 0; k + 1 < W; ++k) {
+      float v[V];
+      input_at<IO, W, V>(x, conv0, len - (W - 1) + k, prm.x_ts, prm.nd, n, v);
+      store_n<IO, V>(last + k * prm.nd, n, v);
+    }
+  }
+}
+
+// ---- backward --------------------------------------------------------------
+
+// One lane: T steps of V channels, and the gradients g of the W-1 steps behind
+// them, which its last dxs need (computed twice, once by either chunk).  The
+// weights' sums of the workgroup's chunks join in LDS; each workgroup leaves
+// W+1 rows of sums.
+template <typename IO, int W, bool SILU>
+__global__ __launch_bounds__(256) void conv_bwd_kernel(const ConvBwdParams prm) {
+  constexpr int V = VecIO<IO>::kWide;
+  const int cx = prm.cx, ty = 256 / cx;
+  const int lane = threadIdx.x % cx, sub = threadIdx.x / cx;
+  const int64_t part = blockIdx.x / prm.n_tiles;
+  const int64_t vec = static_cast<int64_t>(blockIdx.x - part * prm.n_tiles) * cx + lane;
+  const int64_t b = part / prm.n_groups, group = part - b * prm.n_groups;
+  const int64_t c0 = (group * ty + sub) * prm.T;
+  const int64_t d = vec * V;
+  const int n = vec >= prm.n_vec ? 0 : (prm.nd - d < V ? static_cast<int>(prm.nd - d) : V);
+  const int64_t len = row_len(prm.valid_len, b, prm.L);
+  const int64_t c1 = c0 + prm.T < prm.L ? c0 + prm.T : prm.L;
+  float dw[W + 1][V] = {};
+
+  if (n > 0 && (c0 < prm.L || c0 == 0)) {
+    const IO* x = static_cast<const IO*>(prm.x) + b * prm.x_bs + d;
+    const IO* dy = static_cast<const IO*>(prm.dy) + b * prm.dy_bs + d;
+    const int64_t edge = b * (W - 1) * prm.nd + d;
+    const IO* conv0 = prm.conv0 == nullptr ? nullptr : static_cast<const IO*>(prm.conv0) + edge;
+    const IO* dlast = prm.dconv_last == nullptr ? nullptr : static_cast<const IO*>(prm.dconv_last) + edge;
+    IO* dx = static_cast<IO*>(prm.dx) + b * prm.dx_bs + d;
+    IO* d0 = prm.dconv0 == nullptr ? nullptr : static_cast<IO*>(prm.dconv0) + edge;
+
+    Taps<W, V> taps;
+    taps.load(prm.w, prm.bias, d, n);
+    float xs[W][V], g[W][V] = {};
+#pragma unroll
+    for (int k = 0; k + 1 < W; ++k) {
+      if (c0 - (W - 1) + k < len) {
+        input_at<IO, W, V>(x, conv0, c0 - (W - 1) + k, prm.x_ts, prm.nd, n, xs[k]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) xs[k][i] = 0.0f;
+      }
+    }
+    // Step t gives g[t], and with it dxs of step t - (W-1).
+#pragma unroll 2
+    for (int64_t t = c0; t < c1 + (W - 1); ++t) {
+      if (t < len) {
+        load_n<IO, V>(x + t * prm.x_ts, n, xs[W - 1]);
+        load_n<IO, V>(dy + t * prm.dy_ts, n, g[W - 1]);
+        if constexpr (SILU) {
+          float p[V];
+          taps.apply(xs, p);
+#pragma unroll
+          for (int i = 0; i < V; ++i) {
+            const float s = sigmoid_exact(p[i]);
+            g[W - 1][i] *= s * __builtin_fmaf(p[i], 1.0f - s, 1.0f);
+          }
+        }
+        if (t < c1) {
+#pragma unroll
+          for (int i = 0; i < V; ++i) {
+#pragma unroll
+            for (int k = 0; k < W; ++k) dw[k][i] = __builtin_fmaf(g[W - 1][i], xs[k][i], dw[k][i]);
+            dw[W][i] += g[W - 1][i];
+          }
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) g[W - 1][i] = 0.0f, xs[W - 1][i] = 0.0f;
+      }
+      const int64_t o = t - (W - 1);
+      if (o >= c0 || c0 == 0) {
+        float v[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          v[i] = 0.0f;
+#pragma unroll
+          for (int k = 0; k < W; ++k) v[i] = __builtin_fmaf(taps.w[k][i], g[W - 1 - k][i], v[i]);
+        }
+        if (dlast != nullptr && o < len && o >= len - (W - 1)) {
+          float e[V];
+          load_n<IO, V>(dlast + (o - len + (W - 1)) * prm.nd, n, e);
+#pragma unroll
+          for (int i = 0; i < V; ++i) v[i] += e[i];
+        }
+        if (o >= 0)
+          store_n<IO, V>(dx + o * prm.dx_ts, n, v);
+        else if (d0 != nullptr)
+          store_n<IO, V>(d0 + (o + (W - 1)) * prm.nd, n, v);
+      }
+      shift<W, V>(xs);
+      shift<W, V>(g);
+    }
+  }
+
+  // Join the workgroup's ty chunks, one row of sums at a time.
+  __shared__ float lds[256 * V];
+  for (int k = 0; k <= W; ++k) {
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      float m = dw[0][i];
+#pragma unroll
+      for (int q = 1; q <= W; ++q) m = k == q ? dw[q][i] : m;
+      lds[(sub * V + i) * cx + lane] = m;
+    }
+    __syncthreads();
+    for (int e = threadIdx.x; e < cx * V; e += 256) {
+      // e walks the tile's channels: the lane's element e % V of lane e / V
+      const int64_t ch = static_cast<int64_t>(blockIdx.x - part * prm.n_tiles) * cx * V + e;
+      float sum = 0.0f;
+      for (int r = 0; r < ty; ++r) sum += lds[(r * V + e % V) * cx + e / V];
+      if (ch < prm.nd) prm.ws[(part * (W + 1) + k) * prm.nd + ch] = sum;
+    }
+  }
+}
+
+// Columns of the partial sums, [W+1][dim], to dweight [dim][W] and dbias.
+struct ConvGrads {
+  float* dw;
+  float* db;
+  int64_t nd;
+  int32_t W;
+  __device__ __forceinline__ void operator()(int64_t col, float v) const {
+    const int64_t k = col / nd, d = col - k * nd;
+    if (k < W)
+      dw[d * W + k] = v;
+    else if (db != nullptr)
+      db[d] = v;
+  }
+};
+
+__global__ void conv_zero_kernel(float* p, int64_t n) {
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  if (i < n) p[i] = 0.0f;
+}
+
+// ---- one step --------------------------------------------------------------
+
+// One workgroup: 256 lanes' channels of one batch row.
+template <typename IO, int W, bool SILU>
+__global__ __launch_bounds__(256) void conv_step_kernel(const ConvStepParams prm) {
+  constexpr int V = VecIO<IO>::kWide;
+  const int64_t b = blockIdx.y;
+  const int64_t vec = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  const int64_t d = vec * V;
+  const int n = vec >= prm.n_vec ? 0 : (prm.nd - d < V ? static_cast<int>(prm.nd - d) : V);
+  const int64_t slot = prm.slots == nullptr ? b : prm.slots[b];
+  const bool active = step_row_active(prm.slots, b, slot, prm.n_slots);
+  if (n == 0) return;
+  IO* y = static_cast<IO*>(prm.y) + b * prm.y_rs + d;
+  float p[V] = {};
+  if (active) {
+    const int64_t at = slot * (W - 1) * prm.nd + d;
+    const IO* from = static_cast<const IO*>(prm.conv0) + at;
+    IO* to = static_cast<IO*>(prm.conv_last) + at;
+    float xs[W][V];
+#pragma unroll
+    for (int k = 0; k + 1 < W; ++k) load_n<IO, V>(from + k * prm.nd, n, xs[k]);
+    load_n<IO, V>(static_cast<const IO*>(prm.x) + b * prm.x_rs + d, n, xs[W - 1]);
+    Taps<W, V> taps;
+    taps.load(prm.w, prm.bias, d, n);
+    taps.apply(xs, p);
+    if constexpr (SILU) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) p[i] *= sigmoid_exact(p[i]);
+    }
+#pragma unroll
+    for (int k = 0; k + 1 < W; ++k) store_n<IO, V>(to + k * prm.nd, n, xs[k + 1]);
+  }
+  store_n<IO, V>(y, n, p);
+}
+
+// ---- host ------------------------------------------------------------------
+
+// Calls f.template operator()<IO, W, SILU>() for these dims.
+template <typename F>
+void for_conv(const ssm_conv_dims* dims, const F& f) {
+  const auto width = [&]<typename IO, bool SILU>() {
+    switch (dims->width) {
+      case 2:
+        f.template operator()<IO, 2, SILU>();
+        break;
+      case 3:
+        f.template operator()<IO, 3, SILU>();
+        break;
+      default:
+        f.template operator()<IO, 4, SILU>();
+    }
+  };
+  if (dims->io_dtype == SSM_IO_BF16) {
+    if (dims->silu)
+      width.template operator()<uint16_t, true>();
+    else
+      width.template operator()<uint16_t, false>();
+  } else {
+    if (dims->silu)
+      width.template operator()<float, true>();
+    else
+      width.template operator()<float, false>();
+  }
+}
+
+int check_conv_dims(const ssm_conv_dims* dims) {
+  if (dims == nullptr) return SSM_ERR_INVALID_ARG;
+  if (dims->batch < 0 || dims->seqlen < 0 || dims->dim < 0) return SSM_ERR_INVALID_ARG;
+  if (dims->io_dtype != SSM_IO_F32 && dims->io_dtype != SSM_IO_BF16) return SSM_ERR_INVALID_ARG;
+  if (dims->silu != 0 && dims->silu != 1) return SSM_ERR_INVALID_ARG;
+  if (dims->width < 2 || dims->width > 4) return SSM_ERR_UNSUPPORTED;
+  if (dims->batch > kMaxSize || dims->seqlen > kMaxSize || dims->dim > kMaxSize) return SSM_ERR_UNSUPPORTED;
+  return SSM_OK;
+}
+
+int64_t vec_of(int32_t io_dtype) {
+  return io_dtype == SSM_IO_BF16 ? VecIO<uint16_t>::kWide : VecIO<float>::kWide;
+}
+
+// Steps a lane of the forward walks.
+int64_t fwd_chunk(int64_t) { return 32; }
+
+// The backward's tiling: cx lanes over the channels and 256 / cx chunks of T
+// steps a workgroup.
+struct BwdTiling {
+  int64_t n_vec, cx, ty, n_tiles, T, n_groups, parts;
+};
+
+BwdTiling bwd_tiling(const ssm_conv_dims* dims) {
+  BwdTiling t;
+  const int64_t V = vec_of(dims->io_dtype);
+  t.n_vec = (dims->dim + V - 1) / V;
+  t.cx = 64;
+  while (t.cx > 1 && t.cx / 2 >= t.n_vec) t.cx /= 2;
+  t.ty = 256 / t.cx;
+  t.n_tiles = (t.n_vec + t.cx - 1) / t.cx;
+  t.T = 32;
+  t.n_groups = (dims->seqlen + t.T * t.ty - 1) / (t.T * t.ty);
+  if (t.n_groups < 1) t.n_groups = 1;
+  t.parts = dims->batch * t.n_groups;
+  return t;
+}
+
+}  // namespace
+
+extern "C" {
+
+int ssm_causal_conv_fwd(ssm_scan_t handle, const ssm_conv_dims* dims, const ssm_conv_fwd_io* io, void* stream) {
+  const int bad = check_conv_dims(dims);
+  if (bad != SSM_OK) return bad;
+  if (io == nullptr) return SSM_ERR_INVALID_ARG;
+  const int64_t nb = dims->batch, L = dims->seqlen, nd = dims->dim, W = dims->width;
+  const int64_t e = dims->io_dtype == SSM_IO_BF16 ? 2 : 4;
+  const bool empty = nb == 0 || nd == 0;
+  if (!empty) {
+    if (io->weight == nullptr) return SSM_ERR_INVALID_ARG;
+    if (L > 0 && (io->x == nullptr || io->y == nullptr)) return SSM_ERR_INVALID_ARG;
+    const int64_t bx = span_bytes(nb, io->x_batch_stride, L, io->x_time_stride, nd, e);
+    const int64_t by = span_bytes(nb, io->y_batch_stride, L, io->y_time_stride, nd, e);
+    if (bx < 0 || by < 0 || !rows_disjoint(nb, io->y_batch_stride, L, io->y_time_stride, nd))
+      return SSM_ERR_INVALID_ARG;
+    if (!aligned(io->x, e) || !aligned(io->y, e) || !aligned(io->conv0, e) || !aligned(io->conv_last, e) ||
+        !aligned(io->weight, 4) || !aligned(io->bias, 4) || !aligned(io->valid_len, 4))
+      return SSM_ERR_UNSUPPORTED;
+    const int64_t bc = nb * (W - 1) * nd * e;
+    const Range in[] = {{io->x, bx},       {io->weight, nd * W * 4}, {io->bias, nd * 4},
+                        {io->valid_len, nb * 4}, {io->conv0, bc}};
+    const Range out[] = {{io->y, by}, {io->conv_last, bc}};
+    if (any_overlap(in, out)) return SSM_ERR_ALIAS;
+  }
+  const int rc = check_handle(handle);
+  if (rc != SSM_OK || empty) return rc;
+  if (L == 0 && io->conv_last == nullptr) return SSM_OK;
+
+  ConvParams p;
+  p.x = io->x, p.w = io->weight, p.bias = io->bias, p.valid_len = io->valid_len, p.conv0 = io->conv0;
+  p.y = io->y, p.conv_last = io->conv_last;
+  p.x_bs = io->x_batch_stride, p.x_ts = io->x_time_stride, p.y_bs = io->y_batch_stride, p.y_ts = io->y_time_stride;
+  const int64_t V = vec_of(dims->io_dtype);
+  p.L = L, p.nd = static_cast<int32_t>(nd);
+  p.n_vec = static_cast<int32_t>((nd + V - 1) / V);
+  p.T = static_cast<int32_t>(fwd_chunk(nb * L * p.n_vec));
+  p.n_chunks = L > 0 ? (L + p.T - 1) / p.T : 1;
+  p.items = nb * p.n_chunks * p.n_vec;
+  const int64_t blocks = (p.items + 255) / 256;
+  if (!grid_fits(blocks, 256)) return SSM_ERR_UNSUPPORTED;
+  for_conv(dims, [&]<typename IO, int TAPS, bool SILU>() {
+    hipLaunchKernelGGL((conv_fwd_kernel<IO, TAPS, SILU>), dim3(static_cast<unsigned>(blocks)), dim3(256), 0,
+                       static_cast<hipStream_t>(stream), p);
+  });
+  return launched();
+}
+
+int64_t ssm_causal_conv_bwd_workspace_bytes(const ssm_conv_dims* dims) {
+  if (check_conv_dims(dims) != SSM_OK) return -1;
+  const __int128 n = static_cast<__int128>(bwd_tiling(dims).parts) * (dims->width + 1) * dims->dim * 4;
+  return n < (static_cast<__int128>(1) << 62) ? static_cast<int64_t>(n) : -1;
+}
+
+int ssm_causal_conv_bwd(ssm_scan_t handle, const ssm_conv_dims* dims, const ssm_conv_bwd_io* io, void* stream) {
+  const int bad = check_conv_dims(dims);
+  if (bad != SSM_OK) return bad;
+  if (io == nullptr) return SSM_ERR_INVALID_ARG;
+  const int64_t nb = dims->batch, L = dims->seqlen, nd = dims->dim, W = dims->width;
+  const int64_t e = dims->io_dtype == SSM_IO_BF16 ? 2 : 4;
+  const int64_t need = ssm_causal_conv_bwd_workspace_bytes(dims);
+  if (need < 0) return SSM_ERR_UNSUPPORTED;
+  if (io->workspace_bytes < 0) return SSM_ERR_INVALID_ARG;
+  if (nd > 0) {
+    if (io->weight == nullptr || io->dweight == nullptr) return SSM_ERR_INVALID_ARG;
+    if (nb > 0 && L > 0 && (io->x == nullptr || io->dy == nullptr || io->dx == nullptr)) return SSM_ERR_INVALID_ARG;
+    if (nb > 0 && (io->workspace == nullptr || io->workspace_bytes < need)) return SSM_ERR_INVALID_ARG;
+    const int64_t bx = span_bytes(nb, io->x_batch_stride, L, io->x_time_stride, nd, e);
+    const int64_t bdy = span_bytes(nb, io->dy_batch_stride, L, io->dy_time_stride, nd, e);
+    const int64_t bdx = span_bytes(nb, io->dx_batch_stride, L, io->dx_time_stride, nd, e);
+    if (bx < 0 || bdy < 0 || bdx < 0 || !rows_disjoint(nb, io->dx_batch_stride, L, io->dx_time_stride, nd))
+      return SSM_ERR_INVALID_ARG;
+    if (!aligned(io->x, e) || !aligned(io->dy, e) || !aligned(io->dx, e) || !aligned(io->conv0, e) ||
+        !aligned(io->dconv_last, e) || !aligned(io->dconv0, e) || !aligned(io->weight, 4) || !aligned(io->bias, 4) ||
+        !aligned(io->valid_len, 4) || !aligned(io->dweight, 4) || !aligned(io->dbias, 4) || !aligned(io->workspace, 4))
+      return SSM_ERR_UNSUPPORTED;
+    const int64_t bc = nb * (W - 1) * nd * e;
+    const Range in[] = {{io->x, bx},       {io->dy, bdy},    {io->weight, nd * W * 4}, {io->bias, nd * 4},
+                        {io->valid_len, nb * 4}, {io->conv0, bc}, {io->dconv_last, bc}};
+    const Range out[] = {{io->dx, bdx},     {io->dweight, nd * W * 4}, {io->dbias, nd * 4},
+                         {io->dconv0, bc}, {io->workspace, io->workspace_bytes}};
+    if (any_overlap(in, out)) return SSM_ERR_ALIAS;
+  }
+  const int rc = check_handle(handle);
+  if (rc != SSM_OK || nd == 0) return rc;
+
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  if (nb == 0) {  // sums over nothing
+    if (!grid_fits((nd * W + 255) / 256, 256)) return SSM_ERR_UNSUPPORTED;
+    hipLaunchKernelGGL(conv_zero_kernel, dim3(static_cast<unsigned>((nd * W + 255) / 256)), dim3(256), 0, s,
+                       io->dweight, nd * W);
+    if (io->dbias != nullptr)
+      hipLaunchKernelGGL(conv_zero_kernel, dim3(static_cast<unsigned>((nd + 255) / 256)), dim3(256), 0, s, io->dbias,
+                         nd);
+    return launched();
+  }
+  const BwdTiling t = bwd_tiling(dims);
+  ConvBwdParams p;
+  p.x = io->x, p.w = io->weight, p.bias = io->bias, p.valid_len = io->valid_len, p.conv0 = io->conv0;
+  p.dy = io->dy, p.dconv_last = io->dconv_last, p.dx = io->dx, p.dconv0 = io->dconv0;
+  p.ws = static_cast<float*>(io->workspace);
+  p.x_bs = io->x_batch_stride, p.x_ts = io->x_time_stride;
+  p.dy_bs = io->dy_batch_stride, p.dy_ts = io->dy_time_stride;
+  p.dx_bs = io->dx_batch_stride, p.dx_ts = io->dx_time_stride;
+  p.L = L, p.n_groups = t.n_groups, p.nd = static_cast<int32_t>(nd), p.n_vec = static_cast<int32_t>(t.n_vec);
+  p.T = static_cast<int32_t>(t.T), p.cx = static_cast<int32_t>(t.cx), p.n_tiles = static_cast<int32_t>(t.n_tiles);
+  const int64_t blocks = t.parts * t.n_tiles;
+  const int64_t cols = (W + 1) * nd;
+  if (!grid_fits(blocks, 256) || !grid_fits((cols + kReduceCols - 1) / kReduceCols, kReduceCols * kReduceLanes))
+    return SSM_ERR_UNSUPPORTED;
+  for_conv(dims, [&]<typename IO, int TAPS, bool SILU>() {
+    hipLaunchKernelGGL((conv_bwd_kernel<IO, TAPS, SILU>), dim3(static_cast<unsigned>(blocks)), dim3(256), 0, s, p);
+  });
+  if (launched() != SSM_OK) return SSM_ERR_HIP;
+  launch_reduce(p.ws, t.parts, cols, ConvGrads{io->dweight, io->dbias, nd, static_cast<int32_t>(W)}, s);
+  return launched();
+}
+
+int ssm_causal_conv_step(ssm_scan_t handle, const ssm_conv_dims* dims, const ssm_conv_step_io* io, void* stream) {
+  const int bad = check_conv_dims(dims);
+  if (bad != SSM_OK) return bad;
+  if (io == nullptr || dims->seqlen != 1 || io->n_slots < 0) return SSM_ERR_INVALID_ARG;
+  const int64_t nb = dims->batch, nd = dims->dim, W = dims->width;
+  const int64_t e = dims->io_dtype == SSM_IO_BF16 ? 2 : 4;
+  const int64_t rows = io->slots == nullptr ? nb : io->n_slots;
+  if (nb > 65535 || rows > kMaxSize) return SSM_ERR_UNSUPPORTED;
+  const bool empty = nb == 0 || nd == 0;
+  if (!empty) {
+    if (io->x == nullptr || io->y == nullptr || io->weight == nullptr ||
+        (rows > 0 && (io->conv0 == nullptr || io->conv_last == nullptr)))
+      return SSM_ERR_INVALID_ARG;
+    const int64_t bx = span_bytes(nb, io->x_row_stride, 1, 0, nd, e);
+    const int64_t by = span_bytes(nb, io->y_row_stride, 1, 0, nd, e);
+    const int64_t bc = span_bytes(rows, (W - 1) * nd, 1, 0, (W - 1) * nd, e);
+    if (bx < 0 || by < 0 || !rows_disjoint(nb, io->y_row_stride, 1, 0, nd)) return SSM_ERR_INVALID_ARG;
+    if (bc < 0) return SSM_ERR_UNSUPPORTED;
+    if (!aligned(io->x, e) || !aligned(io->y, e) || !aligned(io->conv0, e) || !aligned(io->conv_last, e) ||
+        !aligned(io->weight, 4) || !aligned(io->bias, 4) || !aligned(io->slots, 4))
+      return SSM_ERR_UNSUPPORTED;
+    // the cache in place is one range: conv0 is then left out of the inputs
+    const Range in[] = {{io->x, bx},       {io->weight, nd * W * 4}, {io->bias, nd * 4},
+                        {io->slots, nb * 4}, {io->conv0, io->conv0 == io->conv_last ? 0 : bc}};
+    const Range out[] = {{io->y, by}, {io->conv_last, bc}};
+    if (any_overlap(in, out)) return SSM_ERR_ALIAS;
+  }
+  const int rc = check_handle(handle);
+  if (rc != SSM_OK || empty) return rc;
+
+  ConvStepParams p;
+  p.x = io->x, p.w = io->weight, p.bias = io->bias, p.slots = io->slots, p.conv0 = io->conv0;
+  p.conv_last = io->conv_last, p.y = io->y, p.x_rs = io->x_row_stride, p.y_rs = io->y_row_stride, p.n_slots = rows;
+  const int64_t V = vec_of(dims->io_dtype);
+  p.nd = static_cast<int32_t>(nd), p.n_vec = static_cast<int32_t>((nd + V - 1) / V);
+  const int64_t tiles = (p.n_vec + 255) / 256;
+  if (!grid_fits(tiles, 256)) return SSM_ERR_UNSUPPORTED;
+  for_conv(dims, [&]<typename IO, int TAPS, bool SILU>() {
+    hipLaunchKernelGGL((conv_step_kernel<IO, TAPS, SILU>), dim3(static_cast<unsigned>(tiles), static_cast<unsigned>(nb)),
+                       dim3(256), 0, static_cast<hipStream_t>(stream), p);
+  });
+  return launched();
+}
+
+}  // extern "C"
