@@ -23,22 +23,37 @@ template <>
 struct VecIO<float> {
   static constexpr int kWide = 4;
   typedef float vec4 __attribute__((ext_vector_type(4), aligned(4)));
+  typedef float vec2 __attribute__((ext_vector_type(2), aligned(4)));
   template <int V>
   static __device__ __forceinline__ void load(const float* p, float (&o)[V]) {
-    static_assert(V % 4 == 0, "whole 16-byte pieces");
+    constexpr int kWhole = V / 4 * 4;
 #pragma unroll
-    for (int i = 0; i < V; i += 4) {
+    for (int i = 0; i < kWhole; i += 4) {
       const vec4 v = *reinterpret_cast<const vec4*>(p + i);
       o[i] = v.x, o[i + 1] = v.y, o[i + 2] = v.z, o[i + 3] = v.w;
     }
+    if constexpr (V % 4 >= 2) {
+      const vec2 v = *reinterpret_cast<const vec2*>(p + kWhole);
+      o[kWhole] = v.x, o[kWhole + 1] = v.y;
+    }
+    if constexpr (V % 2 == 1) o[V - 1] = p[V - 1];
   }
   template <int V>
   static __device__ __forceinline__ void store(float* p, const float (&o)[V]) {
+    static_assert(V <= 2 || V % 4 == 0, "whole 16-byte pieces, one or two elements");
+    if constexpr (V == 1) {
+      *p = o[0];
+    } else if constexpr (V == 2) {
+      vec2 v;
+      v.x = o[0], v.y = o[1];
+      *reinterpret_cast<vec2*>(p) = v;
+    } else {
 #pragma unroll
-    for (int i = 0; i < V; i += 4) {
-      vec4 v;
-      v.x = o[i], v.y = o[i + 1], v.z = o[i + 2], v.w = o[i + 3];
-      *reinterpret_cast<vec4*>(p + i) = v;
+      for (int i = 0; i < V; i += 4) {
+        vec4 v;
+        v.x = o[i], v.y = o[i + 1], v.z = o[i + 2], v.w = o[i + 3];
+        *reinterpret_cast<vec4*>(p + i) = v;
+      }
     }
   }
   static __device__ __forceinline__ float get(const float* p) { return *p; }
@@ -52,18 +67,28 @@ struct VecIO<uint16_t> {
   static constexpr int kWide = 8;
   typedef uint32_t vec4 __attribute__((ext_vector_type(4), aligned(2)));
   typedef uint32_t vec2 __attribute__((ext_vector_type(2), aligned(2)));
+  typedef uint32_t vec1 __attribute__((aligned(2)));
   static __device__ __forceinline__ float lo(uint32_t u) { return __builtin_bit_cast(float, u << 16); }
   static __device__ __forceinline__ float hi(uint32_t u) { return __builtin_bit_cast(float, u & 0xffff0000u); }
   static __device__ __forceinline__ uint16_t narrow(float v) {
     return __builtin_bit_cast(uint16_t, static_cast<__bf16>(v));
   }
-  static __device__ __forceinline__ uint32_t pack(float a, float b) {
-    return static_cast<uint32_t>(narrow(a)) | (static_cast<uint32_t>(narrow(b)) << 16);
+  static __device__ __forceinline__ uint32_t pack(float a, float b) {  // v_cvt_pk_bf16_f32
+    typedef float f32x2 __attribute__((ext_vector_type(2)));
+    typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+    f32x2 v;
+    v.x = a, v.y = b;
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf16x2));
   }
   template <int V>
   static __device__ __forceinline__ void load(const uint16_t* p, float (&o)[V]) {
-    static_assert(V % 8 == 0 || V == 4, "whole 16- or 8-byte pieces");
-    if constexpr (V == 4) {
+    static_assert(V % 8 == 0 || V == 4 || V == 2 || V == 1, "whole 16-, 8- or 4-byte pieces, or one element");
+    if constexpr (V == 1) {
+      o[0] = get(p);
+    } else if constexpr (V == 2) {
+      const vec1 v = *reinterpret_cast<const vec1*>(p);
+      o[0] = lo(v), o[1] = hi(v);
+    } else if constexpr (V == 4) {
       const vec2 v = *reinterpret_cast<const vec2*>(p);
       o[0] = lo(v.x), o[1] = hi(v.x), o[2] = lo(v.y), o[3] = hi(v.y);
     } else {
@@ -77,7 +102,11 @@ struct VecIO<uint16_t> {
   }
   template <int V>
   static __device__ __forceinline__ void store(uint16_t* p, const float (&o)[V]) {
-    if constexpr (V == 4) {
+    if constexpr (V == 1) {
+      put(p, o[0]);
+    } else if constexpr (V == 2) {
+      *reinterpret_cast<vec1*>(p) = pack(o[0], o[1]);
+    } else if constexpr (V == 4) {
       vec2 v;
       v.x = pack(o[0], o[1]), v.y = pack(o[2], o[3]);
       *reinterpret_cast<vec2*>(p) = v;
@@ -95,6 +124,50 @@ struct VecIO<uint16_t> {
     return __builtin_bit_cast(float, static_cast<uint32_t>(*p) << 16);
   }
   static __device__ __forceinline__ void put(uint16_t* p, float v) { *p = narrow(v); }
+};
+
+// V elements as they stand in memory: what a lane keeps of a load in flight,
+// unpacked when it is used.
+template <typename IO, int V>
+struct RawVec;
+
+template <int V>
+struct RawVec<float, V> {
+  float v[V];
+  __device__ __forceinline__ void load(const float* p) { VecIO<float>::load(p, v); }
+  __device__ __forceinline__ void unpack(float (&o)[V]) const {
+#pragma unroll
+    for (int i = 0; i < V; ++i) o[i] = v[i];
+  }
+};
+
+template <int V>
+struct RawVec<uint16_t, V> {
+  typedef uint32_t vec __attribute__((ext_vector_type(V / 2), aligned(2)));
+  vec v;
+  __device__ __forceinline__ void load(const uint16_t* p) { v = *reinterpret_cast<const vec*>(p); }
+  __device__ __forceinline__ void unpack(float (&o)[V]) const {
+#pragma unroll
+    for (int i = 0; i < V / 2; ++i) o[2 * i] = VecIO<uint16_t>::lo(v[i]), o[2 * i + 1] = VecIO<uint16_t>::hi(v[i]);
+  }
+};
+
+template <>
+struct RawVec<uint16_t, 2> {
+  uint32_t v;
+  __device__ __forceinline__ void load(const uint16_t* p) {
+    v = *reinterpret_cast<const VecIO<uint16_t>::vec1*>(p);
+  }
+  __device__ __forceinline__ void unpack(float (&o)[2]) const {
+    o[0] = VecIO<uint16_t>::lo(v), o[1] = VecIO<uint16_t>::hi(v);
+  }
+};
+
+template <>
+struct RawVec<uint16_t, 1> {
+  uint16_t v;
+  __device__ __forceinline__ void load(const uint16_t* p) { v = *p; }
+  __device__ __forceinline__ void unpack(float (&o)[1]) const { o[0] = VecIO<uint16_t>::lo(v); }
 };
 
 // The first n (0 <= n <= V) of V elements; the others read as zero and are not
@@ -119,6 +192,22 @@ __device__ __forceinline__ void store_n(IO* p, int n, const float (&o)[V]) {
   }
 }
 
+// ---- workgroups ------------------------------------------------------------
+
+// Workgroups are dealt to the 8 XCDs in turn, each with an L2 of its own.
+// Renumbered like this, an XCD gets runs of kRun consecutive pieces of work, so
+// that what neighbours share (rows in front of a chunk, the other part of a
+// line) is found in its L2, while the runs stay short enough that rows of
+// different lengths spread over all XCDs.  What is left over behind the last
+// whole round of runs keeps its numbers.
+constexpr uint32_t kRun = 8;
+
+__device__ __forceinline__ uint32_t xcd_run(uint32_t block, uint32_t blocks) {
+  if (block >= blocks / (8 * kRun) * (8 * kRun)) return block;
+  const uint32_t x = block % 8, i = block / 8;
+  return (i / kRun * 8 + x) * kRun + i % kRun;
+}
+
 // ---- activations ---------------------------------------------------------
 
 // sigmoid(v) = 1 / (1 + e^-v).  v_exp_f32 is 2^x: the rounding error of
@@ -128,11 +217,26 @@ __device__ __forceinline__ void store_n(IO* p, int n, const float (&o)[V]) {
 // the result 0), so that infinities stay out of the correction.
 __device__ __forceinline__ float sigmoid_exact(float v) {
   constexpr float kLog2eLow = 1.925962991e-8f;  // log2(e) - kLog2e
-  const float c = __builtin_fminf(__builtin_fmaxf(v, -110.0f), 110.0f);
+  const float c = __builtin_amdgcn_fmed3f(v, -110.0f, 110.0f);
   const float t = -c * kLog2e;
-  const float r = __builtin_fmaf(-c, kLog2e, -t) - c * kLog2eLow;
+  const float r = __builtin_fmaf(-c, kLog2eLow, __builtin_fmaf(-c, kLog2e, -t));
   const float e = fast_exp2(t);
   return __builtin_amdgcn_rcpf(__builtin_fmaf(e, __builtin_fmaf(r, kLn2, 1.0f), 1.0f));
+}
+
+// The same for a result that is rounded to bf16: the exponent's rounding error
+// (|v| 2^-24 relative) is far below bf16's step wherever the result is not 0
+// or 1 to it, and the short form has half the instructions.
+__device__ __forceinline__ float sigmoid_short(float v) {
+  return __builtin_amdgcn_rcpf(1.0f + fast_exp2(-v * kLog2e));
+}
+
+template <typename IO>
+__device__ __forceinline__ float sigmoid_for(float v) {
+  if constexpr (sizeof(IO) == 2)
+    return sigmoid_short(v);
+  else
+    return sigmoid_exact(v);
 }
 
 // ---- wave reductions -----------------------------------------------------

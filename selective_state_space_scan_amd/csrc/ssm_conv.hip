@@ -26,6 +26,20 @@
 
 namespace {
 
+// Channels of a lane: 16 bytes of fp32, 8 of bf16 (16 there cost twice the
+// registers and lost 10 %); one where dim is smaller than that.
+constexpr int kVec = 4;
+
+// The first channel of a lane.  Where dim is no multiple of V the last lane
+// starts early and shares channels with its neighbour: both compute and store
+// the same values, and no lane is partly filled.  Not for a cache in place,
+// where a value must be written once.
+template <int V>
+__device__ __forceinline__ int64_t first_channel(int64_t vec, int64_t nd) {
+  const int64_t d = vec * V, last = nd - V;
+  return d < last ? d : last;
+}
+
 struct ConvParams {
   const void* x;
   const float* w;
@@ -35,8 +49,9 @@ struct ConvParams {
   void* y;
   void* conv_last;
   int64_t x_bs, x_ts, y_bs, y_ts;
-  int64_t L, n_chunks, items;
-  int32_t nd, n_vec, T;
+  int64_t L;
+  uint32_t n_chunks, items, n_vec;
+  int32_t nd;
 };
 
 struct ConvBwdParams {
@@ -51,8 +66,9 @@ struct ConvBwdParams {
   void* dconv0;
   float* ws;
   int64_t x_bs, x_ts, dy_bs, dy_ts, dx_bs, dx_ts;
-  int64_t L, n_groups;
-  int32_t nd, n_vec, T, cx, n_tiles;
+  int64_t L;
+  uint32_t n_groups, n_tiles;
+  int32_t nd, n_vec, M, log2_cx;
 };
 
 struct ConvStepParams {
@@ -77,11 +93,15 @@ template <int W, int V>
 struct Taps {
   float w[W][V];
   float bias[V];
-  __device__ __forceinline__ void load(const float* wp, const float* bp, int64_t d, int n) {
+  // n < V: the channels from the n-th on are zero
+  __device__ __forceinline__ void load(const float* wp, const float* bp, int64_t d, int n = V) {
+    // V channels' taps are adjacent
+    float f[V * W];
+    load_n<float, V * W>(wp + d * W, n * W, f);
 #pragma unroll
     for (int i = 0; i < V; ++i) {
 #pragma unroll
-      for (int k = 0; k < W; ++k) w[k][i] = i < n ? wp[(d + i) * W + k] : 0.0f;
+      for (int k = 0; k < W; ++k) w[k][i] = f[i * W + k];
     }
     if (bp != nullptr) {
       load_n<float, V>(bp + d, n, bias);
@@ -112,12 +132,12 @@ __device__ __forceinline__ void shift(float (&xs)[W][V]) {
 
 // The input of step t (t >= -(W-1)) of a row; zeros where nothing is carried.
 template <typename IO, int W, int V>
-__device__ __forceinline__ void input_at(const IO* x, const IO* conv0, int64_t t, int64_t x_ts, int64_t nd, int n,
+__device__ __forceinline__ void input_at(const IO* x, const IO* conv0, int64_t t, int64_t x_ts, int64_t nd,
                                          float (&o)[V]) {
   if (t >= 0) {
-    load_n<IO, V>(x + t * x_ts, n, o);
+    VecIO<IO>::load(x + t * x_ts, o);
   } else if (conv0 != nullptr) {
-    load_n<IO, V>(conv0 + (W - 1 + t) * nd, n, o);
+    VecIO<IO>::load(conv0 + (W - 1 + t) * nd, o);
   } else {
 #pragma unroll
     for (int i = 0; i < V; ++i) o[i] = 0.0f;
@@ -128,43 +148,58 @@ __device__ __forceinline__ void input_at(const IO* x, const IO* conv0, int64_t t
 
 // One lane: T steps of V channels.  Chunks, not channels, run over the grid's
 // slow index, so that a workgroup's lanes cover whole rows where dim allows.
-template <typename IO, int W, bool SILU>
+template <typename IO, int V, int W, bool SILU, int T>
 __global__ __launch_bounds__(256) void conv_fwd_kernel(const ConvParams prm) {
-  constexpr int V = VecIO<IO>::kWide;
-  const int64_t item = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  // a launch has fewer than 2^32 work-items
+  const uint32_t item = xcd_run(blockIdx.x, gridDim.x) * 256 + threadIdx.x;
   if (item >= prm.items) return;
-  const int64_t row = item / prm.n_vec;
-  const int64_t d = (item - row * prm.n_vec) * V;
-  const int64_t b = row / prm.n_chunks, c0 = (row - b * prm.n_chunks) * prm.T;
-  const int n = prm.nd - d < V ? static_cast<int>(prm.nd - d) : V;
+  const uint32_t row = item / prm.n_vec;
+  const int64_t d = first_channel<V>(item - row * prm.n_vec, prm.nd);
+  const uint32_t batch = row / prm.n_chunks;
+  const int64_t b = batch, c0 = static_cast<int64_t>(row - batch * prm.n_chunks) * T;
   const int64_t len = row_len(prm.valid_len, b, prm.L);
   const IO* x = static_cast<const IO*>(prm.x) + b * prm.x_bs + d;
   const IO* conv0 = prm.conv0 == nullptr ? nullptr : static_cast<const IO*>(prm.conv0) + b * (W - 1) * prm.nd + d;
   IO* y = static_cast<IO*>(prm.y) + b * prm.y_bs + d;
 
-  const int64_t c1 = c0 + prm.T < prm.L ? c0 + prm.T : prm.L;
+  const int64_t c1 = c0 + T < prm.L ? c0 + T : prm.L;
   const int64_t v1 = c1 < len ? c1 : len;
   if (v1 > c0) {
+    // The chunk's inputs are all in flight at once; those past its valid
+    // steps repeat its last.
+    RawVec<IO, V> in[T];
+    const IO* xp = x + c0 * prm.x_ts;
+    const int valid = static_cast<int>(v1 - c0);
+#pragma unroll
+    for (int u = 0; u < T; ++u) in[u].load(xp + (u < valid ? u : valid - 1) * prm.x_ts);
     Taps<W, V> taps;
-    taps.load(prm.w, prm.bias, d, n);
+    taps.load(prm.w, prm.bias, d);
     float xs[W][V];
 #pragma unroll
-    for (int k = 0; k + 1 < W; ++k) input_at<IO, W, V>(x, conv0, c0 - (W - 1) + k, prm.x_ts, prm.nd, n, xs[k]);
-#pragma unroll 4
-    for (int64_t t = c0; t < v1; ++t) {
-      load_n<IO, V>(x + t * prm.x_ts, n, xs[W - 1]);
+    for (int k = 0; k + 1 < W; ++k) input_at<IO, W, V>(x, conv0, c0 - (W - 1) + k, prm.x_ts, prm.nd, xs[k]);
+    IO* yp = y + c0 * prm.y_ts;
+    const auto step = [&](int u) {
+      in[u].unpack(xs[W - 1]);
       float p[V];
       taps.apply(xs, p);
       if constexpr (SILU) {
 #pragma unroll
-        for (int i = 0; i < V; ++i) p[i] *= sigmoid_exact(p[i]);
+        for (int i = 0; i < V; ++i) p[i] *= sigmoid_for<IO>(p[i]);
       }
-      store_n<IO, V>(y + t * prm.y_ts, n, p);
+      VecIO<IO>::store(yp + u * prm.y_ts, p);
       shift<W, V>(xs);
+    };
+    if (valid == T) {
+#pragma unroll
+      for (int u = 0; u < T; ++u) step(u);
+    } else {
+#pragma unroll
+      for (int u = 0; u < T; ++u)
+        if (u < valid) step(u);
     }
   }
   const float zero[V] = {};
-  for (int64_t t = v1 > c0 ? v1 : c0; t < c1; ++t) store_n<IO, V>(y + t * prm.y_ts, n, zero);
+  for (int64_t t = v1 > c0 ? v1 : c0; t < c1; ++t) VecIO<IO>::store(y + t * prm.y_ts, zero);
 
   // The row's last W-1 inputs, by the lanes of its first chunk.
   if (c0 == 0 && prm.conv_last != nullptr) {
@@ -172,125 +207,165 @@ __global__ __launch_bounds__(256) void conv_fwd_kernel(const ConvParams prm) {
 #pragma unroll
     for (int k = 0; k + 1 < W; ++k) {
       float v[V];
-      input_at<IO, W, V>(x, conv0, len - (W - 1) + k, prm.x_ts, prm.nd, n, v);
-      store_n<IO, V>(last + k * prm.nd, n, v);
+      input_at<IO, W, V>(x, conv0, len - (W - 1) + k, prm.x_ts, prm.nd, v);
+      VecIO<IO>::store(last + k * prm.nd, v);
     }
   }
 }
 
 // ---- backward --------------------------------------------------------------
 
-// One lane: T steps of V channels, and the gradients g of the W-1 steps behind
-// them, which its last dxs need (computed twice, once by either chunk).  The
-// weights' sums of the workgroup's chunks join in LDS; each workgroup leaves
-// W+1 rows of sums.
-template <typename IO, int W, bool SILU>
+// One lane: chunks of T steps of V channels, all in flight at once, and the gradients g of the W-1
+// steps behind each, which its last dxs need (computed twice, once by either
+// chunk).  A workgroup's ty chunks are adjacent, and it takes M such runs one
+// after the other, so what chunks share is read at about the same time.  The
+// weights' sums join in LDS at the end; each workgroup leaves W+1 rows of sums.
+constexpr int kBwdChunk = 13;
+constexpr int kBwdVec = 2;
+
+template <typename IO, int V, int W, bool SILU>
 __global__ __launch_bounds__(256) void conv_bwd_kernel(const ConvBwdParams prm) {
-  constexpr int V = VecIO<IO>::kWide;
-  const int cx = prm.cx, ty = 256 / cx;
-  const int lane = threadIdx.x % cx, sub = threadIdx.x / cx;
-  const int64_t part = blockIdx.x / prm.n_tiles;
-  const int64_t vec = static_cast<int64_t>(blockIdx.x - part * prm.n_tiles) * cx + lane;
-  const int64_t b = part / prm.n_groups, group = part - b * prm.n_groups;
-  const int64_t c0 = (group * ty + sub) * prm.T;
-  const int64_t d = vec * V;
-  const int n = vec >= prm.n_vec ? 0 : (prm.nd - d < V ? static_cast<int>(prm.nd - d) : V);
+  constexpr int T = kBwdChunk, H = W - 1;
+  const int shift_x = prm.log2_cx, cx = 1 << shift_x, ty = 256 >> shift_x;
+  const int lane = threadIdx.x & (cx - 1), sub = threadIdx.x >> shift_x;
+  const uint32_t block = xcd_run(blockIdx.x, gridDim.x);
+  const uint32_t part = block / prm.n_tiles, tile = block - part * prm.n_tiles;
+  const int64_t vec = static_cast<int64_t>(tile) * cx + lane;
+  const uint32_t batch = part / prm.n_groups, group = part - batch * prm.n_groups;
+  const int64_t b = batch;
+  const int64_t d = first_channel<V>(vec, prm.nd);
   const int64_t len = row_len(prm.valid_len, b, prm.L);
-  const int64_t c1 = c0 + prm.T < prm.L ? c0 + prm.T : prm.L;
   float dw[W + 1][V] = {};
 
-  if (n > 0 && (c0 < prm.L || c0 == 0)) {
+  if (vec < prm.n_vec) {
     const IO* x = static_cast<const IO*>(prm.x) + b * prm.x_bs + d;
     const IO* dy = static_cast<const IO*>(prm.dy) + b * prm.dy_bs + d;
-    const int64_t edge = b * (W - 1) * prm.nd + d;
+    IO* dx = static_cast<IO*>(prm.dx) + b * prm.dx_bs + d;
+    const int64_t edge = b * H * prm.nd + d;
     const IO* conv0 = prm.conv0 == nullptr ? nullptr : static_cast<const IO*>(prm.conv0) + edge;
     const IO* dlast = prm.dconv_last == nullptr ? nullptr : static_cast<const IO*>(prm.dconv_last) + edge;
-    IO* dx = static_cast<IO*>(prm.dx) + b * prm.dx_bs + d;
     IO* d0 = prm.dconv0 == nullptr ? nullptr : static_cast<IO*>(prm.dconv0) + edge;
-
     Taps<W, V> taps;
-    taps.load(prm.w, prm.bias, d, n);
-    float xs[W][V], g[W][V] = {};
+    taps.load(prm.w, prm.bias, d);
+
+    // EDGE: the row's first chunk, or one that reaches past its valid steps.
+    const auto chunk = [&]<bool EDGE>(int64_t c0) {
+      RawVec<IO, V> xr[T + 2 * H], gr[T + H];
+      const IO* xp = x + (c0 - H) * prm.x_ts;
+      const IO* gp = dy + c0 * prm.dy_ts;
+      IO* op = dx + c0 * prm.dx_ts;
 #pragma unroll
-    for (int k = 0; k + 1 < W; ++k) {
-      if (c0 - (W - 1) + k < len) {
-        input_at<IO, W, V>(x, conv0, c0 - (W - 1) + k, prm.x_ts, prm.nd, n, xs[k]);
-      } else {
-#pragma unroll
-        for (int i = 0; i < V; ++i) xs[k][i] = 0.0f;
+      for (int u = 0; u < T + 2 * H; ++u) {
+        if constexpr (EDGE) {
+          const int64_t t = c0 - H + u;
+          xr[u] = {};
+          if (t < 0) {
+            if (conv0 != nullptr) xr[u].load(conv0 + (H + t) * prm.nd);
+          } else if (t < len) {
+            xr[u].load(xp + u * prm.x_ts);
+          }
+        } else {
+          xr[u].load(xp + u * prm.x_ts);
+        }
       }
-    }
-    // Step t gives g[t], and with it dxs of step t - (W-1).
-#pragma unroll 2
-    for (int64_t t = c0; t < c1 + (W - 1); ++t) {
-      if (t < len) {
-        load_n<IO, V>(x + t * prm.x_ts, n, xs[W - 1]);
-        load_n<IO, V>(dy + t * prm.dy_ts, n, g[W - 1]);
+#pragma unroll
+      for (int u = 0; u < T + H; ++u) {
+        if constexpr (EDGE) {
+          gr[u] = {};
+          if (c0 + u < len) gr[u].load(gp + u * prm.dy_ts);
+        } else {
+          gr[u].load(gp + u * prm.dy_ts);
+        }
+      }
+      float xs[W][V], g[W][V] = {};
+#pragma unroll
+      for (int k = 0; k < H; ++k) xr[k].unpack(xs[k]);
+#pragma unroll
+      for (int j = 0; j < T + H; ++j) {
+        // step t = c0 + j gives g[t] (0 past the row's end), and with it dxs
+        // of step t - (W-1)
+        xr[j + H].unpack(xs[H]);
+        gr[j].unpack(g[H]);
         if constexpr (SILU) {
           float p[V];
           taps.apply(xs, p);
 #pragma unroll
           for (int i = 0; i < V; ++i) {
-            const float s = sigmoid_exact(p[i]);
-            g[W - 1][i] *= s * __builtin_fmaf(p[i], 1.0f - s, 1.0f);
+            const float s = sigmoid_for<IO>(p[i]);
+            g[H][i] *= s * __builtin_fmaf(p[i], 1.0f - s, 1.0f);
+          }
+          if (EDGE && c0 + j >= len) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) g[H][i] = 0.0f;
           }
         }
-        if (t < c1) {
+        if (j < T) {
 #pragma unroll
           for (int i = 0; i < V; ++i) {
 #pragma unroll
-            for (int k = 0; k < W; ++k) dw[k][i] = __builtin_fmaf(g[W - 1][i], xs[k][i], dw[k][i]);
-            dw[W][i] += g[W - 1][i];
+            for (int k = 0; k < W; ++k) dw[k][i] = __builtin_fmaf(g[H][i], xs[k][i], dw[k][i]);
+            dw[W][i] += g[H][i];
           }
         }
+        if (j >= H || (EDGE && c0 == 0)) {
+          float v[V];
+#pragma unroll
+          for (int i = 0; i < V; ++i) {
+            v[i] = 0.0f;  // the sum of products with g = 0 is +0 whatever their signs
+#pragma unroll
+            for (int k = 0; k < W; ++k) v[i] = __builtin_fmaf(taps.w[k][i], g[H - k][i], v[i]);
+          }
+          if constexpr (EDGE) {
+            const int64_t o = c0 + j - H;
+            if (dlast != nullptr && o < len && o >= len - H) {
+              float e[V];
+              VecIO<IO>::load(dlast + (o - len + H) * prm.nd, e);
+#pragma unroll
+              for (int i = 0; i < V; ++i) v[i] += e[i];
+            }
+            if (o < 0) {
+              if (d0 != nullptr) VecIO<IO>::store(d0 + (o + H) * prm.nd, v);
+            } else if (o < prm.L) {
+              VecIO<IO>::store(op + (j - H) * prm.dx_ts, v);
+            }
+          } else {
+            VecIO<IO>::store(op + (j - H) * prm.dx_ts, v);
+          }
+        }
+        shift<W, V>(xs);
+        shift<W, V>(g);
+      }
+    };
+    for (int m = 0; m < prm.M; ++m) {
+      const int64_t c0 = ((static_cast<int64_t>(group) * prm.M + m) * ty + sub) * T;
+      if (c0 > 0 && c0 + T + H <= len) {
+        chunk.template operator()<false>(c0);
+      } else if (c0 == 0 || c0 < len) {
+        chunk.template operator()<true>(c0);
       } else {
-#pragma unroll
-        for (int i = 0; i < V; ++i) g[W - 1][i] = 0.0f, xs[W - 1][i] = 0.0f;
+        const float zero[V] = {};
+        const int64_t c1 = c0 + T < prm.L ? c0 + T : prm.L;
+        for (int64_t t = c0; t < c1; ++t) VecIO<IO>::store(dx + t * prm.dx_ts, zero);
       }
-      const int64_t o = t - (W - 1);
-      if (o >= c0 || c0 == 0) {
-        float v[V];
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-          v[i] = 0.0f;
-#pragma unroll
-          for (int k = 0; k < W; ++k) v[i] = __builtin_fmaf(taps.w[k][i], g[W - 1 - k][i], v[i]);
-        }
-        if (dlast != nullptr && o < len && o >= len - (W - 1)) {
-          float e[V];
-          load_n<IO, V>(dlast + (o - len + (W - 1)) * prm.nd, n, e);
-#pragma unroll
-          for (int i = 0; i < V; ++i) v[i] += e[i];
-        }
-        if (o >= 0)
-          store_n<IO, V>(dx + o * prm.dx_ts, n, v);
-        else if (d0 != nullptr)
-          store_n<IO, V>(d0 + (o + (W - 1)) * prm.nd, n, v);
-      }
-      shift<W, V>(xs);
-      shift<W, V>(g);
     }
   }
 
-  // Join the workgroup's ty chunks, one row of sums at a time.
-  __shared__ float lds[256 * V];
+  // Join the workgroup's ty chunks.
+  __shared__ float lds[(W + 1) * V * 256];
+#pragma unroll
   for (int k = 0; k <= W; ++k) {
-    __syncthreads();
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      float m = dw[0][i];
-#pragma unroll
-      for (int q = 1; q <= W; ++q) m = k == q ? dw[q][i] : m;
-      lds[(sub * V + i) * cx + lane] = m;
-    }
-    __syncthreads();
-    for (int e = threadIdx.x; e < cx * V; e += 256) {
-      // e walks the tile's channels: the lane's element e % V of lane e / V
-      const int64_t ch = static_cast<int64_t>(blockIdx.x - part * prm.n_tiles) * cx * V + e;
-      float sum = 0.0f;
-      for (int r = 0; r < ty; ++r) sum += lds[(r * V + e % V) * cx + e / V];
-      if (ch < prm.nd) prm.ws[(part * (W + 1) + k) * prm.nd + ch] = sum;
-    }
+    for (int i = 0; i < V; ++i) lds[(k * V + i) * 256 + threadIdx.x] = dw[k][i];
+  }
+  __syncthreads();
+  for (int e = threadIdx.x; e < (W + 1) * cx * V; e += 256) {
+    const int k = e / V >> shift_x, c = e - (k * V << shift_x);
+    const int64_t v = static_cast<int64_t>(tile) * cx + c / V, ch = v * V + c % V;
+    if (ch >= prm.nd) continue;
+    const int i = static_cast<int>(ch - first_channel<V>(v, prm.nd));  // of lane c / V
+    float sum = 0.0f;
+    for (int r = 0; r < ty; ++r) sum += lds[(k * V + i) * 256 + r * cx + c / V];
+    prm.ws[(static_cast<int64_t>(part) * (W + 1) + k) * prm.nd + ch] = sum;
   }
 }
 
@@ -319,7 +394,7 @@ __global__ void conv_zero_kernel(float* p, int64_t n) {
 // One workgroup: 256 lanes' channels of one batch row.
 template <typename IO, int W, bool SILU>
 __global__ __launch_bounds__(256) void conv_step_kernel(const ConvStepParams prm) {
-  constexpr int V = VecIO<IO>::kWide;
+  constexpr int V = kVec;
   const int64_t b = blockIdx.y;
   const int64_t vec = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
   const int64_t d = vec * V;
@@ -342,7 +417,7 @@ __global__ __launch_bounds__(256) void conv_step_kernel(const ConvStepParams prm
     taps.apply(xs, p);
     if constexpr (SILU) {
 #pragma unroll
-      for (int i = 0; i < V; ++i) p[i] *= sigmoid_exact(p[i]);
+      for (int i = 0; i < V; ++i) p[i] *= sigmoid_for<IO>(p[i]);
     }
 #pragma unroll
     for (int k = 0; k + 1 < W; ++k) store_n<IO, V>(to + k * prm.nd, n, xs[k + 1]);
@@ -380,6 +455,9 @@ void for_conv(const ssm_conv_dims* dims, const F& f) {
   }
 }
 
+// Channels of a lane of the sequence kernels.
+int64_t vec_of(int64_t nd) { return nd < kVec ? 1 : kVec; }
+
 int check_conv_dims(const ssm_conv_dims* dims) {
   if (dims == nullptr) return SSM_ERR_INVALID_ARG;
   if (dims->batch < 0 || dims->seqlen < 0 || dims->dim < 0) return SSM_ERR_INVALID_ARG;
@@ -390,30 +468,39 @@ int check_conv_dims(const ssm_conv_dims* dims) {
   return SSM_OK;
 }
 
-int64_t vec_of(int32_t io_dtype) {
-  return io_dtype == SSM_IO_BF16 ? VecIO<uint16_t>::kWide : VecIO<float>::kWide;
-}
+// Steps a lane of the forward walks: long chunks read fewer of the inputs in
+// front of them twice, short ones fill the GPU sooner and answer sooner.  bf16,
+// us at 4 / 12 steps: 2 x 1000 steps x 512 channels 4.0 / 5.5, 2 x 2000 x 1024
+// 7.0 / 8.0, 4 x 2000 x 1024 11.3 / 10.7, 8 x 4096 x 1024 35.7 / 26.9.
+constexpr int kShortChunk = 4, kLongChunk = 12;
+constexpr int64_t kShortWork = 3 << 19;  // (step, lane) pairs
 
-// Steps a lane of the forward walks.
-int64_t fwd_chunk(int64_t) { return 32; }
-
-// The backward's tiling: cx lanes over the channels and 256 / cx chunks of T
-// steps a workgroup.
+// The backward's tiling: 2^log2_cx lanes over the channels and ty = 256 /
+// 2^log2_cx chunks a workgroup, M times.
 struct BwdTiling {
-  int64_t n_vec, cx, ty, n_tiles, T, n_groups, parts;
+  int64_t V, n_vec, ty, n_tiles, n_groups, parts;
+  int log2_cx, M;
 };
+
+constexpr int64_t kBwdBlocks = 1200;
 
 BwdTiling bwd_tiling(const ssm_conv_dims* dims) {
   BwdTiling t;
-  const int64_t V = vec_of(dims->io_dtype);
-  t.n_vec = (dims->dim + V - 1) / V;
-  t.cx = 64;
-  while (t.cx > 1 && t.cx / 2 >= t.n_vec) t.cx /= 2;
-  t.ty = 256 / t.cx;
-  t.n_tiles = (t.n_vec + t.cx - 1) / t.cx;
-  t.T = 32;
-  t.n_groups = (dims->seqlen + t.T * t.ty - 1) / (t.T * t.ty);
-  if (t.n_groups < 1) t.n_groups = 1;
+  t.V = dims->dim < kBwdVec ? 1 : kBwdVec;
+  t.n_vec = (dims->dim + t.V - 1) / t.V;
+  t.log2_cx = 6;
+  while (t.log2_cx > 0 && (1 << (t.log2_cx - 1)) >= t.n_vec) --t.log2_cx;
+  const int64_t cx = 1 << t.log2_cx;
+  t.ty = 256 / cx;
+  t.n_tiles = (t.n_vec + cx - 1) / cx;
+  const int64_t run = kBwdChunk * t.ty, runs = dims->seqlen > 0 ? (dims->seqlen + run - 1) / run : 1;
+  // Fewer, longer workgroups leave fewer sums; at least kBwdBlocks of them
+  // fill the GPU (us, M = 1 or 2 / 4: bf16 8 x 4096 x 1024 50.0 / 47.8, fp32 8 x 2048
+  // x 1024 43.1 / 46.0).
+  const __int128 all = static_cast<__int128>(dims->batch) * runs * t.n_tiles;
+  t.M = 1;
+  while (t.M < 8 && all >= (t.M + 1) * kBwdBlocks) ++t.M;
+  t.n_groups = (runs + t.M - 1) / t.M;
   t.parts = dims->batch * t.n_groups;
   return t;
 }
@@ -453,17 +540,21 @@ int ssm_causal_conv_fwd(ssm_scan_t handle, const ssm_conv_dims* dims, const ssm_
   p.x = io->x, p.w = io->weight, p.bias = io->bias, p.valid_len = io->valid_len, p.conv0 = io->conv0;
   p.y = io->y, p.conv_last = io->conv_last;
   p.x_bs = io->x_batch_stride, p.x_ts = io->x_time_stride, p.y_bs = io->y_batch_stride, p.y_ts = io->y_time_stride;
-  const int64_t V = vec_of(dims->io_dtype);
+  const int64_t V = vec_of(nd);
   p.L = L, p.nd = static_cast<int32_t>(nd);
-  p.n_vec = static_cast<int32_t>((nd + V - 1) / V);
-  p.T = static_cast<int32_t>(fwd_chunk(nb * L * p.n_vec));
-  p.n_chunks = L > 0 ? (L + p.T - 1) / p.T : 1;
-  p.items = nb * p.n_chunks * p.n_vec;
-  const int64_t blocks = (p.items + 255) / 256;
-  if (!grid_fits(blocks, 256)) return SSM_ERR_UNSUPPORTED;
+  const int64_t n_vec = (nd + V - 1) / V;
+  const bool brief = V == 1 || static_cast<__int128>(nb) * L * n_vec <= kShortWork;
+  const int64_t T = brief ? kShortChunk : kLongChunk, n_chunks = L > 0 ? (L + T - 1) / T : 1;
+  const __int128 items = static_cast<__int128>(nb) * n_chunks * n_vec;
+  if (items > 0xffffff00) return SSM_ERR_UNSUPPORTED;
+  p.n_vec = static_cast<uint32_t>(n_vec), p.n_chunks = static_cast<uint32_t>(n_chunks);
+  p.items = static_cast<uint32_t>(items);
+  const int64_t blocks = (static_cast<int64_t>(items) + 255) / 256;
   for_conv(dims, [&]<typename IO, int TAPS, bool SILU>() {
-    hipLaunchKernelGGL((conv_fwd_kernel<IO, TAPS, SILU>), dim3(static_cast<unsigned>(blocks)), dim3(256), 0,
-                       static_cast<hipStream_t>(stream), p);
+    const auto kernel = V == 1  ? conv_fwd_kernel<IO, 1, TAPS, SILU, kShortChunk>
+                        : brief ? conv_fwd_kernel<IO, kVec, TAPS, SILU, kShortChunk>
+                                : conv_fwd_kernel<IO, kVec, TAPS, SILU, kLongChunk>;
+    hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, static_cast<hipStream_t>(stream), p);
   });
   return launched();
 }
@@ -524,14 +615,18 @@ int ssm_causal_conv_bwd(ssm_scan_t handle, const ssm_conv_dims* dims, const ssm_
   p.x_bs = io->x_batch_stride, p.x_ts = io->x_time_stride;
   p.dy_bs = io->dy_batch_stride, p.dy_ts = io->dy_time_stride;
   p.dx_bs = io->dx_batch_stride, p.dx_ts = io->dx_time_stride;
-  p.L = L, p.n_groups = t.n_groups, p.nd = static_cast<int32_t>(nd), p.n_vec = static_cast<int32_t>(t.n_vec);
-  p.T = static_cast<int32_t>(t.T), p.cx = static_cast<int32_t>(t.cx), p.n_tiles = static_cast<int32_t>(t.n_tiles);
-  const int64_t blocks = t.parts * t.n_tiles;
+  p.L = L, p.n_groups = static_cast<uint32_t>(t.n_groups), p.n_tiles = static_cast<uint32_t>(t.n_tiles);
+  p.nd = static_cast<int32_t>(nd), p.n_vec = static_cast<int32_t>(t.n_vec), p.M = t.M;
+  p.log2_cx = t.log2_cx;
+  const __int128 all = static_cast<__int128>(t.parts) * t.n_tiles;
+  if (all > kMaxSize) return SSM_ERR_UNSUPPORTED;
+  const int64_t blocks = static_cast<int64_t>(all);
   const int64_t cols = (W + 1) * nd;
   if (!grid_fits(blocks, 256) || !grid_fits((cols + kReduceCols - 1) / kReduceCols, kReduceCols * kReduceLanes))
     return SSM_ERR_UNSUPPORTED;
   for_conv(dims, [&]<typename IO, int TAPS, bool SILU>() {
-    hipLaunchKernelGGL((conv_bwd_kernel<IO, TAPS, SILU>), dim3(static_cast<unsigned>(blocks)), dim3(256), 0, s, p);
+    const auto kernel = t.V == 1 ? conv_bwd_kernel<IO, 1, TAPS, SILU> : conv_bwd_kernel<IO, kBwdVec, TAPS, SILU>;
+    hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, s, p);
   });
   if (launched() != SSM_OK) return SSM_ERR_HIP;
   launch_reduce(p.ws, t.parts, cols, ConvGrads{io->dweight, io->dbias, nd, static_cast<int32_t>(W)}, s);
@@ -571,7 +666,7 @@ int ssm_causal_conv_step(ssm_scan_t handle, const ssm_conv_dims* dims, const ssm
   ConvStepParams p;
   p.x = io->x, p.w = io->weight, p.bias = io->bias, p.slots = io->slots, p.conv0 = io->conv0;
   p.conv_last = io->conv_last, p.y = io->y, p.x_rs = io->x_row_stride, p.y_rs = io->y_row_stride, p.n_slots = rows;
-  const int64_t V = vec_of(dims->io_dtype);
+  const int64_t V = kVec;
   p.nd = static_cast<int32_t>(nd), p.n_vec = static_cast<int32_t>((nd + V - 1) / V);
   const int64_t tiles = (p.n_vec + 255) / 256;
   if (!grid_fits(tiles, 256)) return SSM_ERR_UNSUPPORTED;
