@@ -41,44 +41,46 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
-class _On:
-    """The stream of a call, as a raw handle, with the call's allocations on it
-    (so that the caching allocator orders their reuse after its kernels)."""
+# The current stream's raw handle by device index; torch.cuda.current_stream
+# would build a Stream object for it, 1.9 us of a call's 11.
+_current_raw = torch._C._cuda_getCurrentRawStream
 
-    def __init__(self, stream, dev):
-        self.dev = dev
-        if stream is None:  # allocations follow the current stream by themselves
-            self.stream, self.raw = None, torch.cuda.current_stream(dev).cuda_stream
-        else:
-            self.stream = _b._stream_for(stream, dev)
-            self.raw = self.stream.cuda_stream
 
-    def empty(self, shape, dtype):
-        if self.stream is None:
-            return torch.empty(shape, dtype=dtype, device=self.dev)
-        with torch.cuda.stream(self.stream):
-            return torch.empty(shape, dtype=dtype, device=self.dev)
+def _stream(stream, dev):
+    """A call's stream as (torch stream or None for the current one, raw handle)."""
+    if stream is None:
+        return None, _current_raw(dev.index)
+    stream = _b._stream_for(stream, dev)
+    return stream, stream.cuda_stream
 
-    def scratch(self, given, nbytes: int):
-        if nbytes < 0:
-            raise ValueError("unsupported sizes")
-        if given is None:
-            return self.empty((max(nbytes, 4),), torch.uint8)
-        if (given.dtype != torch.uint8 or given.device != self.dev or not given.is_contiguous()
-                or given.numel() < nbytes):
-            raise ValueError(f"workspace must be a contiguous uint8 tensor of at least {nbytes} bytes on {self.dev}")
-        return given
 
-    def call(self, name: str, dims, io) -> None:
-        fn = getattr(_b.lib(), name)
-        index = self.dev.index
-        if index == torch.cuda.current_device():
-            rc = fn(_b.handle_for(index), ctypes.byref(dims), ctypes.byref(io), self.raw)
-        else:
-            with torch.cuda.device(self.dev):
-                rc = fn(_b.handle_for(index), ctypes.byref(dims), ctypes.byref(io), self.raw)
-        if rc != _b.SSM_OK:
-            raise _b.SsmScanError(rc, name)
+def _empty(stream, shape, dtype, dev):
+    """A tensor whose memory the caching allocator orders with the call's stream."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=dev)
+
+
+def _scratch(stream, given, nbytes: int, dev):
+    if nbytes < 0:
+        raise ValueError("unsupported sizes")
+    if given is None:
+        return _empty(stream, (max(nbytes, 4),), torch.uint8, dev)
+    if given.dtype != torch.uint8 or given.device != dev or not given.is_contiguous() or given.numel() < nbytes:
+        raise ValueError(f"workspace must be a contiguous uint8 tensor of at least {nbytes} bytes on {dev}")
+    return given
+
+
+def _call(fn, name: str, dims, io, raw, dev) -> None:
+    index = dev.index
+    if index == torch.cuda.current_device():
+        rc = fn(_b.handle_for(index), ctypes.byref(dims), ctypes.byref(io), raw)
+    else:
+        with torch.cuda.device(dev):
+            rc = fn(_b.handle_for(index), ctypes.byref(dims), ctypes.byref(io), raw)
+    if rc != _b.SSM_OK:
+        raise _b.SsmScanError(rc, name)
 
 
 # ---- single tokens ---------------------------------------------------------
@@ -134,9 +136,9 @@ def selective_scan_step(x, delta, A_log, B, C, D, h, *, slots=None, h_last=None,
     if z is not None:
         _want("z", z, (nb, nd), dt, dev, False)
     rows, h_last = _cache("h", h, h_last, slots, nb, (nd, N), torch.float32, dev)
-    on = _On(stream, dev)
+    stream, raw = _stream(stream, dev)
     if y is None:
-        y = on.empty((nb, nd), dt)
+        y = _empty(stream, (nb, nd), dt, dev)
     else:
         _want("y", y, (nb, nd), dt, dev, False)
     lo, hi = (0.0, 0.0) if delta_clamp is None else delta_clamp
@@ -145,7 +147,7 @@ def selective_scan_step(x, delta, A_log, B, C, D, h, *, slots=None, h_last=None,
                                _ptr(delta_bias), _ptr(z), _ptr(slots), h.data_ptr(), h_last.data_ptr(), y.data_ptr(),
                                x.stride(0), delta.stride(0), B.stride(0), C.stride(0),
                                0 if z is None else z.stride(0), y.stride(0), rows)
-    on.call("ssm_selective_scan_step", dims, args)
+    _call(_b.lib().ssm_selective_scan_step, "ssm_selective_scan_step", dims, args, raw, dev)
     return y
 
 
@@ -173,14 +175,15 @@ def causal_conv_step(x, conv, weight, bias=None, *, silu: bool = True, slots=Non
     if bias is not None:
         _want("bias", bias, (nd,), torch.float32, dev)
     rows, conv_last = _cache("conv", conv, conv_last, slots, nb, (W - 1, nd), dt, dev)
-    on = _On(stream, dev)
+    stream, raw = _stream(stream, dev)
     if y is None:
-        y = on.empty((nb, nd), dt)
+        y = _empty(stream, (nb, nd), dt, dev)
     else:
         _want("y", y, (nb, nd), dt, dev, False)
     args = _b.ssm_conv_step_io(x.data_ptr(), weight.data_ptr(), _ptr(bias), _ptr(slots), conv.data_ptr(),
                                conv_last.data_ptr(), y.data_ptr(), x.stride(0), y.stride(0), rows)
-    on.call("ssm_causal_conv_step", _b.ssm_conv_dims(nb, 1, nd, W, io, 1 if silu else 0), args)
+    dims = _b.ssm_conv_dims(nb, 1, nd, W, io, 1 if silu else 0)
+    _call(_b.lib().ssm_causal_conv_step, "ssm_causal_conv_step", dims, args, raw, dev)
     return y
 
 
@@ -222,18 +225,19 @@ def causal_conv_fwd(x, weight, bias=None, valid_len=None, *, silu: bool = True, 
     io = _io(x)
     nb, L, nd, W = _conv_shapes(x, weight, bias, valid_len, conv0)
     dev, dt = x.device, x.dtype
-    on = _On(stream, dev)
+    stream, raw = _stream(stream, dev)
     if y is None:
-        y = on.empty((nb, L, nd), dt)
+        y = _empty(stream, (nb, L, nd), dt, dev)
     else:
         _want("y", y, (nb, L, nd), dt, dev, False)
     if conv_last is not None:
         _want("conv_last", conv_last, (nb, W - 1, nd), dt, dev)
     elif return_conv_last:
-        conv_last = on.empty((nb, W - 1, nd), dt)
+        conv_last = _empty(stream, (nb, W - 1, nd), dt, dev)
     args = _b.ssm_conv_fwd_io(x.data_ptr(), weight.data_ptr(), _ptr(bias), _ptr(valid_len), _ptr(conv0), y.data_ptr(),
                               _ptr(conv_last), x.stride(0), x.stride(1), y.stride(0), y.stride(1))
-    on.call("ssm_causal_conv_fwd", _b.ssm_conv_dims(nb, L, nd, W, io, 1 if silu else 0), args)
+    dims = _b.ssm_conv_dims(nb, L, nd, W, io, 1 if silu else 0)
+    _call(_b.lib().ssm_causal_conv_fwd, "ssm_causal_conv_fwd", dims, args, raw, dev)
     return y, conv_last
 
 
@@ -253,21 +257,21 @@ def causal_conv_bwd(x, weight, bias, valid_len, dy, *, silu: bool = True, conv0=
     _want("dy", dy, (nb, L, nd), dt, dev, False)
     if dconv_last is not None:
         _want("dconv_last", dconv_last, (nb, W - 1, nd), dt, dev)
-    on = _On(stream, dev)
+    stream, raw = _stream(stream, dev)
     if dx is None:
-        dx = on.empty((nb, L, nd), dt)
+        dx = _empty(stream, (nb, L, nd), dt, dev)
     else:
         _want("dx", dx, (nb, L, nd), dt, dev, False)
-    dweight = on.empty((nd, W), torch.float32)
-    dbias = None if bias is None else on.empty((nd,), torch.float32)
-    dconv0 = None if conv0 is None else on.empty((nb, W - 1, nd), dt)
+    dweight = _empty(stream, (nd, W), torch.float32, dev)
+    dbias = None if bias is None else _empty(stream, (nd,), torch.float32, dev)
+    dconv0 = None if conv0 is None else _empty(stream, (nb, W - 1, nd), dt, dev)
     dims = _b.ssm_conv_dims(nb, L, nd, W, io, 1 if silu else 0)
-    ws = on.scratch(workspace, _b.lib().ssm_causal_conv_bwd_workspace_bytes(ctypes.byref(dims)))
+    ws = _scratch(stream, workspace, _b.lib().ssm_causal_conv_bwd_workspace_bytes(ctypes.byref(dims)), dev)
     args = _b.ssm_conv_bwd_io(x.data_ptr(), weight.data_ptr(), _ptr(bias), _ptr(valid_len), _ptr(conv0), dy.data_ptr(),
                               _ptr(dconv_last), dx.data_ptr(), dweight.data_ptr(), _ptr(dbias), _ptr(dconv0),
                               ws.data_ptr(), ws.numel(), x.stride(0), x.stride(1), dy.stride(0), dy.stride(1),
                               dx.stride(0), dx.stride(1))
-    on.call("ssm_causal_conv_bwd", dims, args)
+    _call(_b.lib().ssm_causal_conv_bwd, "ssm_causal_conv_bwd", dims, args, raw, dev)
     return dict(dx=dx, dweight=dweight, dbias=dbias, dconv0=dconv0)
 
 
@@ -313,24 +317,24 @@ def layer_norm_fwd(x, weight, bias=None, valid_len=None, *, residual=None, eps: 
         raise TypeError("residual must be float32 or of x's dtype")
     if residual is not None:
         _want("residual", residual, shape, rdt, dev)
-    on = _On(stream, dev)
+    stream, raw = _stream(stream, dev)
     if y is None:
-        y = on.empty(shape, dt)
+        y = _empty(stream, shape, dt, dev)
     else:
         _want("y", y, shape, dt, dev)
     if residual_out is not None:
         _want("residual_out", residual_out, shape, rdt, dev)
     elif residual is not None:
-        residual_out = on.empty(shape, rdt)
+        residual_out = _empty(stream, shape, rdt, dev)
     mean = rstd = None
     if return_stats:
-        rstd = on.empty(shape[:-1], torch.float32)
+        rstd = _empty(stream, shape[:-1], torch.float32, dev)
         if not rms:
-            mean = on.empty(shape[:-1], torch.float32)
+            mean = _empty(stream, shape[:-1], torch.float32, dev)
     dims = _b.ssm_norm_dims(nb, L, nd, io, _IO[rdt], 1 if rms else 0, eps)
     args = _b.ssm_norm_fwd_io(x.data_ptr(), _ptr(residual), weight.data_ptr(), _ptr(bias), _ptr(valid_len),
                               y.data_ptr(), _ptr(residual_out), _ptr(mean), _ptr(rstd))
-    on.call("ssm_layer_norm_fwd", dims, args)
+    _call(_b.lib().ssm_layer_norm_fwd, "ssm_layer_norm_fwd", dims, args, raw, dev)
     return (y, residual_out, mean, rstd) if return_stats else (y, residual_out)
 
 
@@ -357,18 +361,18 @@ def layer_norm_bwd(dy, v, weight, mean, rstd, valid_len=None, *, dresidual_out=N
     _want("rstd", rstd, shape[:-1], torch.float32, dev)
     if dresidual_out is not None:
         _want("dresidual_out", dresidual_out, shape, v.dtype, dev)
-    on = _On(stream, dev)
-    dx = on.empty(shape, dt)
+    stream, raw = _stream(stream, dev)
+    dx = _empty(stream, shape, dt, dev)
     wanted = dresidual_out is not None if with_residual is None else with_residual
     apart = wanted and v.dtype != dt
-    dresidual = on.empty(shape, v.dtype) if apart else None
-    dweight = on.empty((nd,), torch.float32)
-    dbias = on.empty((nd,), torch.float32) if with_bias else None
+    dresidual = _empty(stream, shape, v.dtype, dev) if apart else None
+    dweight = _empty(stream, (nd,), torch.float32, dev)
+    dbias = _empty(stream, (nd,), torch.float32, dev) if with_bias else None
     # eps went into rstd; the library wants a positive one all the same
     dims = _b.ssm_norm_dims(nb, L, nd, io, _IO[v.dtype], 1 if mean is None else 0, 1.0)
-    ws = on.scratch(workspace, _b.lib().ssm_layer_norm_bwd_workspace_bytes(ctypes.byref(dims)))
+    ws = _scratch(stream, workspace, _b.lib().ssm_layer_norm_bwd_workspace_bytes(ctypes.byref(dims)), dev)
     args = _b.ssm_norm_bwd_io(dy.data_ptr(), v.data_ptr(), weight.data_ptr(), _ptr(mean), rstd.data_ptr(),
                               _ptr(valid_len), _ptr(dresidual_out), dx.data_ptr(), _ptr(dresidual), dweight.data_ptr(),
                               _ptr(dbias), ws.data_ptr(), ws.numel())
-    on.call("ssm_layer_norm_bwd", dims, args)
+    _call(_b.lib().ssm_layer_norm_bwd, "ssm_layer_norm_bwd", dims, args, raw, dev)
     return dict(dx=dx, dresidual=dresidual if apart else (dx if wanted else None), dweight=dweight, dbias=dbias)

@@ -272,16 +272,37 @@ __device__ __forceinline__ float wave_sum(float v) {
 
 // ---- steps on a cache ------------------------------------------------------
 
-// Whether batch row b of a single-token step runs on cache row `slot`: not if
-// it lies outside the cache (rows that pad the batch carry -1), nor if an
-// earlier batch row names the same cache row, whose update then stands alone
-// (two rows updating one would race).  Called by every thread of the workgroup
-// (it contains a barrier when slots are given).
-__device__ __forceinline__ bool step_row_active(const int32_t* slots, int64_t b, int64_t slot, int64_t n_slots) {
-  if (slots == nullptr) return true;
-  bool taken = false;
-  for (int64_t i = threadIdx.x; i < b; i += blockDim.x) taken |= slots[i] == slot;
-  return !__syncthreads_or(taken) && slot >= 0 && slot < n_slots;
+// Which of the batch rows b .. b + R - 1 of a single-token step run on their
+// cache rows `slot`: not one whose slot lies outside the cache (rows that pad
+// the batch carry -1), nor one whose cache row an earlier batch row names, whose
+// update then stands alone (two rows updating one would race).  Every wave
+// looks through the earlier rows for itself, four a lane and load.
+template <int R>
+__device__ __forceinline__ void step_rows_active(const int32_t* slots, int32_t b, int32_t nb, const int32_t (&slot)[R],
+                                                 int64_t n_slots, bool (&active)[R]) {
+  bool taken[R] = {};
+  if (slots != nullptr) {
+    typedef int32_t vec4 __attribute__((ext_vector_type(4), aligned(4)));
+    for (int32_t i = static_cast<int32_t>(threadIdx.x % 64) * 4; i < b; i += 256) {
+      if (i + 4 <= b) {
+        const vec4 v = *reinterpret_cast<const vec4*>(slots + i);
+#pragma unroll
+        for (int r = 0; r < R; ++r) taken[r] |= v.x == slot[r] || v.y == slot[r] || v.z == slot[r] || v.w == slot[r];
+      } else {
+        for (int32_t k = i; k < b; ++k) {
+#pragma unroll
+          for (int r = 0; r < R; ++r) taken[r] |= slots[k] == slot[r];
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    bool free = !__any(taken[r]);
+#pragma unroll
+    for (int q = 0; q < r; ++q) free = free && slot[q] != slot[r];
+    active[r] = b + r < nb && slot[r] >= 0 && slot[r] < n_slots && free;
+  }
 }
 
 // ---- host checks ---------------------------------------------------------

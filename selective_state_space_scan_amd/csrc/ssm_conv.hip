@@ -395,17 +395,18 @@ __global__ void conv_zero_kernel(float* p, int64_t n) {
 template <typename IO, int W, bool SILU>
 __global__ __launch_bounds__(256) void conv_step_kernel(const ConvStepParams prm) {
   constexpr int V = kVec;
-  const int64_t b = blockIdx.y;
+  const int32_t b = blockIdx.y;
   const int64_t vec = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
   const int64_t d = vec * V;
   const int n = vec >= prm.n_vec ? 0 : (prm.nd - d < V ? static_cast<int>(prm.nd - d) : V);
-  const int64_t slot = prm.slots == nullptr ? b : prm.slots[b];
-  const bool active = step_row_active(prm.slots, b, slot, prm.n_slots);
+  const int32_t slot[1] = {prm.slots == nullptr ? b : prm.slots[b]};
+  bool active[1];
+  step_rows_active<1>(prm.slots, b, b + 1, slot, prm.n_slots, active);
   if (n == 0) return;
   IO* y = static_cast<IO*>(prm.y) + b * prm.y_rs + d;
   float p[V] = {};
-  if (active) {
-    const int64_t at = slot * (W - 1) * prm.nd + d;
+  if (active[0]) {
+    const int64_t at = static_cast<int64_t>(slot[0]) * (W - 1) * prm.nd + d;
     const IO* from = static_cast<const IO*>(prm.conv0) + at;
     IO* to = static_cast<IO*>(prm.conv_last) + at;
     float xs[W][V];

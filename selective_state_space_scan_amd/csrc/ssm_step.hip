@@ -38,66 +38,98 @@ struct StepParams {
   void* y;
   int64_t x_rs, delta_rs, B_rs, C_rs, z_rs, y_rs, n_slots;
   float dmin, dmax;
-  int32_t nd, softplus, clamp;
+  int32_t nb, nd, softplus, clamp;
 };
 
-// One workgroup: 1024 / N channels of one batch row.
-template <typename IO, int N>
+// One workgroup: 1024 / N channels of R batch rows, the states of all of them
+// in flight at once; what depends on the channel alone is read once.
+template <typename IO, int N, int R>
 __global__ __launch_bounds__(256) void scan_step_kernel(const StepParams prm) {
   constexpr int LPC = N / 4, CH = 256 / LPC;
-  const int64_t b = blockIdx.y;
+  const int32_t b = blockIdx.y * R;
   const int64_t d = static_cast<int64_t>(blockIdx.x) * CH + threadIdx.x / LPC;
   const int n0 = (threadIdx.x % LPC) * 4;
-  const int64_t slot = prm.slots == nullptr ? b : prm.slots[b];
-  const bool active = step_row_active(prm.slots, b, slot, prm.n_slots);
-  if (d >= prm.nd) return;  // whole groups of LPC lanes leave together
-  IO* y = static_cast<IO*>(prm.y) + b * prm.y_rs + d;
-  if (!active) {
-    if (n0 == 0) VecIO<IO>::put(y, 0.0f);
-    return;
-  }
-  const int64_t at = (slot * prm.nd + d) * N + n0;
-  float h[4], al[4], Bv[4], Cv[4];
-  VecIO<float>::load(prm.h0 + at, h);
-  VecIO<float>::load(prm.A_log + d * N + n0, al);
-  const float x = VecIO<IO>::get(static_cast<const IO*>(prm.x) + b * prm.x_rs + d);
-  float dt = VecIO<IO>::get(static_cast<const IO*>(prm.delta) + b * prm.delta_rs + d);
-  VecIO<IO>::load(static_cast<const IO*>(prm.B) + b * prm.B_rs + n0, Bv);
-  VecIO<IO>::load(static_cast<const IO*>(prm.C) + b * prm.C_rs + n0, Cv);
-  if (prm.delta_bias != nullptr) dt += prm.delta_bias[d];
-  if (prm.softplus) dt = softplus_f32(dt);
-  if (prm.clamp) dt = __builtin_fminf(__builtin_fmaxf(dt, prm.dmin), prm.dmax);
-  const float u = dt * x;
-  float sum = 0.0f;
+  const bool mine = d < prm.nd;  // a channel's lanes agree
+  int32_t slot[R];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float a = fast_exp2(al[i] * kLog2e) * kLog2e;
-    h[i] = __builtin_fmaf(fast_exp2(-dt * a), h[i], u * Bv[i]);
-    sum = __builtin_fmaf(Cv[i], h[i], sum);
-  }
-  VecIO<float>::store(prm.h_last + at, h);
-  sum = group_sum<LPC>(sum);
-  if (n0 == 0) {
-    if (prm.D != nullptr) sum = __builtin_fmaf(prm.D[d], x, sum);
-    if (prm.z != nullptr) {
-      const float z = VecIO<IO>::get(static_cast<const IO*>(prm.z) + b * prm.z_rs + d);
-      sum *= z * sigmoid_exact(z);
+  for (int r = 0; r < R; ++r)
+    slot[r] = b + r >= prm.nb ? -1 : (prm.slots == nullptr ? b + r : prm.slots[b + r]);
+  float h[R][4], al[4] = {}, Bv[R][4], Cv[R][4], x[R], dt[R], z[R], skip = 0.0f, bias = 0.0f;
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    const int64_t row = b + r;
+    // rows that turn out idle are read all the same, inside their bounds
+    if (mine && slot[r] >= 0 && slot[r] < prm.n_slots) {
+      VecIO<float>::load(prm.h0 + (slot[r] * static_cast<int64_t>(prm.nd) + d) * N + n0, h[r]);
+      x[r] = VecIO<IO>::get(static_cast<const IO*>(prm.x) + row * prm.x_rs + d);
+      dt[r] = VecIO<IO>::get(static_cast<const IO*>(prm.delta) + row * prm.delta_rs + d);
+      z[r] = prm.z == nullptr ? 0.0f : VecIO<IO>::get(static_cast<const IO*>(prm.z) + row * prm.z_rs + d);
+      VecIO<IO>::load(static_cast<const IO*>(prm.B) + row * prm.B_rs + n0, Bv[r]);
+      VecIO<IO>::load(static_cast<const IO*>(prm.C) + row * prm.C_rs + n0, Cv[r]);
     }
-    VecIO<IO>::put(y, sum);
+  }
+  if (mine) {
+    VecIO<float>::load(prm.A_log + d * N + n0, al);
+    if (prm.delta_bias != nullptr) bias = prm.delta_bias[d];
+    if (prm.D != nullptr) skip = prm.D[d];
+  }
+  bool active[R];
+  step_rows_active<R>(prm.slots, b, prm.nb, slot, prm.n_slots, active);
+  if (!mine) return;
+  float a[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) a[i] = -fast_exp2(al[i] * kLog2e) * kLog2e;
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    if (b + r >= prm.nb) return;
+    IO* y = static_cast<IO*>(prm.y) + (b + r) * prm.y_rs + d;
+    if (!active[r]) {
+      if (n0 == 0) VecIO<IO>::put(y, 0.0f);
+      continue;
+    }
+    float delta = dt[r] + bias;
+    if (prm.softplus) delta = softplus_f32(delta);
+    if (prm.clamp) delta = __builtin_fminf(__builtin_fmaxf(delta, prm.dmin), prm.dmax);
+    const float u = delta * x[r];
+    float sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      h[r][i] = __builtin_fmaf(fast_exp2(delta * a[i]), h[r][i], u * Bv[r][i]);
+      sum = __builtin_fmaf(Cv[r][i], h[r][i], sum);
+    }
+    VecIO<float>::store(prm.h_last + (slot[r] * static_cast<int64_t>(prm.nd) + d) * N + n0, h[r]);
+    sum = group_sum<LPC>(sum);
+    if (n0 == 0) {
+      if (prm.D != nullptr) sum = __builtin_fmaf(skip, x[r], sum);
+      if (prm.z != nullptr) sum *= z[r] * sigmoid_exact(z[r]);
+      VecIO<IO>::put(y, sum);
+    }
   }
 }
 
+// Rows of a workgroup where there are slots and kSeveral workgroups of one row:
+// they share the look through the slots and its latency.  us at 1 / 2 / 4 rows,
+// 2048 channels, dstate 16: 64 rows 6.3 / 6.4 / 7.5, 128 rows 10.4 / 10.2 / 10.6,
+// 256 rows 18.0 / 17.5 / 18.6, 1024 rows x 1024 channels 44.7 / 39.8 / 42.5.
+// Without slots one row is the faster (256 rows 15.3 / 15.9).
+constexpr int kStepRows = 2;
+constexpr int64_t kSeveral = 4096;
+
+template <typename IO, int N>
+void launch_step_n(bool several, dim3 grid, const StepParams& p, hipStream_t s) {
+  const auto kernel = several ? scan_step_kernel<IO, N, kStepRows> : scan_step_kernel<IO, N, 1>;
+  hipLaunchKernelGGL(kernel, grid, dim3(256), 0, s, p);
+}
+
 template <typename IO>
-void launch_step(int64_t N, dim3 grid, const StepParams& p, hipStream_t s) {
+void launch_step(int64_t N, bool several, dim3 grid, const StepParams& p, hipStream_t s) {
   switch (N) {
     case 16:
-      hipLaunchKernelGGL((scan_step_kernel<IO, 16>), grid, dim3(256), 0, s, p);
-      break;
+      return launch_step_n<IO, 16>(several, grid, p, s);
     case 32:
-      hipLaunchKernelGGL((scan_step_kernel<IO, 32>), grid, dim3(256), 0, s, p);
-      break;
+      return launch_step_n<IO, 32>(several, grid, p, s);
     default:
-      hipLaunchKernelGGL((scan_step_kernel<IO, 64>), grid, dim3(256), 0, s, p);
+      return launch_step_n<IO, 64>(several, grid, p, s);
   }
 }
 
@@ -153,15 +185,16 @@ int ssm_selective_scan_step(ssm_scan_t handle, const ssm_scan_dims* dims, const 
   p.delta_bias = io->delta_bias, p.z = io->z, p.slots = io->slots, p.h0 = io->h0, p.h_last = io->h_last, p.y = io->y;
   p.x_rs = io->x_row_stride, p.delta_rs = io->delta_row_stride, p.B_rs = io->B_row_stride;
   p.C_rs = io->C_row_stride, p.z_rs = io->z_row_stride, p.y_rs = io->y_row_stride, p.n_slots = rows;
-  p.dmin = dims->delta_min, p.dmax = dims->delta_max, p.nd = static_cast<int32_t>(nd);
+  p.dmin = dims->delta_min, p.dmax = dims->delta_max, p.nb = static_cast<int32_t>(nb), p.nd = static_cast<int32_t>(nd);
   p.softplus = dims->delta_softplus, p.clamp = dims->delta_clamp;
   const int64_t ch = 1024 / N, tiles = (nd + ch - 1) / ch;
   if (!grid_fits(tiles, 256)) return SSM_ERR_UNSUPPORTED;
-  const dim3 grid(static_cast<unsigned>(tiles), static_cast<unsigned>(nb));
+  const bool several = io->slots != nullptr && nb * tiles >= kSeveral;
+  const dim3 grid(static_cast<unsigned>(tiles), static_cast<unsigned>(several ? (nb + kStepRows - 1) / kStepRows : nb));
   if (dims->io_dtype == SSM_IO_BF16)
-    launch_step<uint16_t>(N, grid, p, static_cast<hipStream_t>(stream));
+    launch_step<uint16_t>(N, several, grid, p, static_cast<hipStream_t>(stream));
   else
-    launch_step<float>(N, grid, p, static_cast<hipStream_t>(stream));
+    launch_step<float>(N, several, grid, p, static_cast<hipStream_t>(stream));
   return launched();
 }
 
