@@ -1,9 +1,10 @@
 """torch front end of the operators beside the scan in its block: the scan for
 single tokens, the short causal convolution and the layer or RMS norm.
 
-As for the scan, every step runs in the HIP library; this module checks shapes,
-dtypes and devices, allocates outputs and scratch, and passes device pointers
-and the HIP stream across the C ABI.  There is no fallback.
+As for the scan, every step runs in the HIP library.  Shapes, dtypes and
+devices are checked, outputs and scratch allocated and the C ABI called by the
+CPython module ``_ssm_torch`` (``csrc/ssm_torch.cpp``): done here, that took up
+to 8 us of a single-token call whose launch takes 4.  There is no fallback.
 """
 from __future__ import annotations
 
@@ -13,90 +14,35 @@ import torch
 
 from . import _binding as _b
 
-_IO = {torch.float32: _b.SSM_IO_F32, torch.bfloat16: _b.SSM_IO_BF16}
+
+def _load():
+    """The marshalling module, with the HIP library's entry points bound to it."""
+    lib = _b.lib()
+    try:
+        from . import _ssm_torch
+    except ImportError as e:
+        raise ImportError("the torch marshalling module _ssm_torch is not built or does not load; run "
+                          "`python -m selective_state_space_scan_amd.build` (or __graft_entry__.build())") from e
+    entries = ("ssm_selective_scan_step", "ssm_causal_conv_step", "ssm_causal_conv_fwd", "ssm_causal_conv_bwd",
+               "ssm_causal_conv_bwd_workspace_bytes", "ssm_layer_norm_fwd", "ssm_layer_norm_bwd",
+               "ssm_layer_norm_bwd_workspace_bytes")
+    _ssm_torch.bind(*(ctypes.cast(getattr(lib, name), ctypes.c_void_p).value for name in entries), _b.handle_for,
+                    _b.SsmScanError)
+    return _ssm_torch
 
 
-def _io(x, what: str = "x") -> int:
-    if x.device.type != "cuda":
+_native = _load()
+
+
+def _on(stream, x):
+    """The context of a call on ``stream``: its kernels and the memory it allocates, which the caching allocator then
+    orders with them."""
+    if not torch.is_tensor(x) or x.device.type != "cuda":
         raise ValueError("tensors must be on a GPU device")
-    io = _IO.get(x.dtype)
-    if io is None:
-        raise TypeError(f"{what} must be float32 or bfloat16")
-    return io
-
-
-def _want(name: str, t, shape: tuple, dtype, dev, contiguous: bool = True) -> None:
-    """Refuses a tensor of another shape, type or device, or one whose last
-    dimension (all of it with ``contiguous``) is not laid out densely."""
-    if t.shape != shape or t.dtype != dtype or t.device != dev:
-        raise ValueError(f"{name} must be {shape} {dtype} on {dev}, got {tuple(t.shape)} {t.dtype} on {t.device}")
-    if contiguous:
-        if not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous")
-    elif shape[-1] > 1 and t.stride(-1) != 1:
-        raise ValueError(f"{name} must have stride 1 in its last dimension")
-
-
-def _ptr(t):
-    return None if t is None else t.data_ptr()
-
-
-# The current stream's raw handle by device index; torch.cuda.current_stream
-# would build a Stream object for it, 1.9 us of a call's 11.
-_current_raw = torch._C._cuda_getCurrentRawStream
-
-
-def _stream(stream, dev):
-    """A call's stream as (torch stream or None for the current one, raw handle)."""
-    if stream is None:
-        return None, _current_raw(dev.index)
-    stream = _b._stream_for(stream, dev)
-    return stream, stream.cuda_stream
-
-
-def _empty(stream, shape, dtype, dev):
-    """A tensor whose memory the caching allocator orders with the call's stream."""
-    if stream is None:
-        return torch.empty(shape, dtype=dtype, device=dev)
-    with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=dev)
-
-
-def _scratch(stream, given, nbytes: int, dev):
-    if nbytes < 0:
-        raise ValueError("unsupported sizes")
-    if given is None:
-        return _empty(stream, (max(nbytes, 4),), torch.uint8, dev)
-    if given.dtype != torch.uint8 or given.device != dev or not given.is_contiguous() or given.numel() < nbytes:
-        raise ValueError(f"workspace must be a contiguous uint8 tensor of at least {nbytes} bytes on {dev}")
-    return given
-
-
-def _call(fn, name: str, dims, io, raw, dev) -> None:
-    index = dev.index
-    if index == torch.cuda.current_device():
-        rc = fn(_b.handle_for(index), ctypes.byref(dims), ctypes.byref(io), raw)
-    else:
-        with torch.cuda.device(dev):
-            rc = fn(_b.handle_for(index), ctypes.byref(dims), ctypes.byref(io), raw)
-    if rc != _b.SSM_OK:
-        raise _b.SsmScanError(rc, name)
+    return torch.cuda.stream(_b._stream_for(stream, x.device))
 
 
 # ---- single tokens ---------------------------------------------------------
-
-def _cache(name, cache, out, slots, batch: int, shape: tuple, dtype, dev):
-    """Checks a step's cache, where it goes and its slots; (rows, output)."""
-    rows = batch if slots is None else cache.shape[0]
-    _want(name, cache, (rows,) + shape, dtype, dev)
-    if out is None:
-        out = cache
-    elif out is not cache:
-        _want(name + "'s output", out, (rows,) + shape, dtype, dev)
-    if slots is not None:
-        _want("slots", slots, (batch,), torch.int32, dev)
-    return rows, out
-
 
 def selective_scan_step(x, delta, A_log, B, C, D, h, *, slots=None, h_last=None, delta_softplus: bool = True,
                         delta_clamp=None, delta_bias=None, z=None, y=None, stream=None):
@@ -116,39 +62,12 @@ def selective_scan_step(x, delta, A_log, B, C, D, h, *, slots=None, h_last=None,
     h) written there, the rows in use only.  Asynchronous on ``stream`` (default:
     the current stream of x's device).
     """
-    io = _io(x)
-    if x.dim() != 2:
-        raise ValueError("x must be [batch, dim]")
-    dev, dt = x.device, x.dtype
-    nb, nd = x.shape
-    if A_log.dim() != 2 or h.dim() != 3:
-        raise ValueError("A_log must be [dim, dstate] and h [rows, dim, dstate]")
-    N = A_log.shape[1]
-    _want("x", x, (nb, nd), dt, dev, False)
-    _want("delta", delta, (nb, nd), dt, dev, False)
-    _want("B", B, (nb, N), dt, dev, False)
-    _want("C", C, (nb, N), dt, dev, False)
-    _want("A_log", A_log, (nd, N), torch.float32, dev)
-    if D is not None:
-        _want("D", D, (nd,), torch.float32, dev)
-    if delta_bias is not None:
-        _want("delta_bias", delta_bias, (nd,), torch.float32, dev)
-    if z is not None:
-        _want("z", z, (nb, nd), dt, dev, False)
-    rows, h_last = _cache("h", h, h_last, slots, nb, (nd, N), torch.float32, dev)
-    stream, raw = _stream(stream, dev)
-    if y is None:
-        y = _empty(stream, (nb, nd), dt, dev)
-    else:
-        _want("y", y, (nb, nd), dt, dev, False)
-    lo, hi = (0.0, 0.0) if delta_clamp is None else delta_clamp
-    dims = _b.ssm_scan_dims(nb, 1, nd, N, io, 1 if delta_softplus else 0, 0 if delta_clamp is None else 1, lo, hi)
-    args = _b.ssm_scan_step_io(x.data_ptr(), delta.data_ptr(), A_log.data_ptr(), B.data_ptr(), C.data_ptr(), _ptr(D),
-                               _ptr(delta_bias), _ptr(z), _ptr(slots), h.data_ptr(), h_last.data_ptr(), y.data_ptr(),
-                               x.stride(0), delta.stride(0), B.stride(0), C.stride(0),
-                               0 if z is None else z.stride(0), y.stride(0), rows)
-    _call(_b.lib().ssm_selective_scan_step, "ssm_selective_scan_step", dims, args, raw, dev)
-    return y
+    if stream is not None:
+        with _on(stream, x):
+            return selective_scan_step(x, delta, A_log, B, C, D, h, slots=slots, h_last=h_last,
+                                       delta_softplus=delta_softplus, delta_clamp=delta_clamp, delta_bias=delta_bias,
+                                       z=z, y=y)
+    return _native.scan_step(x, delta, A_log, B, C, D, h, slots, h_last, delta_softplus, delta_clamp, delta_bias, z, y)
 
 
 def causal_conv_step(x, conv, weight, bias=None, *, silu: bool = True, slots=None, conv_last=None, y=None,
@@ -162,51 +81,13 @@ def causal_conv_step(x, conv, weight, bias=None, *, silu: bool = True, slots=Non
     idle rows as in ``selective_scan_step``.  weight [dim, width] (2, 3 or 4 taps)
     and bias [dim] or None: float32.  silu: y = p * sigmoid(p).
     """
-    io = _io(x)
-    if x.dim() != 2:
-        raise ValueError("x must be [batch, dim]")
-    dev, dt = x.device, x.dtype
-    nb, nd = x.shape
-    if weight.dim() != 2 or conv.dim() != 3:
-        raise ValueError("weight must be [dim, width] and conv [rows, width - 1, dim]")
-    W = weight.shape[1]
-    _want("x", x, (nb, nd), dt, dev, False)
-    _want("weight", weight, (nd, W), torch.float32, dev)
-    if bias is not None:
-        _want("bias", bias, (nd,), torch.float32, dev)
-    rows, conv_last = _cache("conv", conv, conv_last, slots, nb, (W - 1, nd), dt, dev)
-    stream, raw = _stream(stream, dev)
-    if y is None:
-        y = _empty(stream, (nb, nd), dt, dev)
-    else:
-        _want("y", y, (nb, nd), dt, dev, False)
-    args = _b.ssm_conv_step_io(x.data_ptr(), weight.data_ptr(), _ptr(bias), _ptr(slots), conv.data_ptr(),
-                               conv_last.data_ptr(), y.data_ptr(), x.stride(0), y.stride(0), rows)
-    dims = _b.ssm_conv_dims(nb, 1, nd, W, io, 1 if silu else 0)
-    _call(_b.lib().ssm_causal_conv_step, "ssm_causal_conv_step", dims, args, raw, dev)
-    return y
+    if stream is not None:
+        with _on(stream, x):
+            return causal_conv_step(x, conv, weight, bias, silu=silu, slots=slots, conv_last=conv_last, y=y)
+    return _native.conv_step(x, conv, weight, bias, silu, slots, conv_last, y)
 
 
 # ---- short causal convolution ----------------------------------------------
-
-def _conv_shapes(x, weight, bias, valid_len, conv0):
-    if x.dim() != 3:
-        raise ValueError("x must be [batch, L, dim]")
-    if weight.dim() != 2:
-        raise ValueError("weight must be [dim, width]")
-    dev, dt = x.device, x.dtype
-    nb, L, nd = x.shape
-    W = weight.shape[1]
-    _want("x", x, (nb, L, nd), dt, dev, False)
-    _want("weight", weight, (nd, W), torch.float32, dev)
-    if bias is not None:
-        _want("bias", bias, (nd,), torch.float32, dev)
-    if valid_len is not None:
-        _want("valid_len", valid_len, (nb,), torch.int32, dev)
-    if conv0 is not None:
-        _want("conv0", conv0, (nb, W - 1, nd), dt, dev)
-    return nb, L, nd, W
-
 
 def causal_conv_fwd(x, weight, bias=None, valid_len=None, *, silu: bool = True, conv0=None, y=None, conv_last=None,
                     return_conv_last: bool = True, stream=None):
@@ -222,23 +103,11 @@ def causal_conv_fwd(x, weight, bias=None, valid_len=None, *, silu: bool = True, 
     given).  Outputs are allocated unless given; y may be strided like x.
     Asynchronous on ``stream``.
     """
-    io = _io(x)
-    nb, L, nd, W = _conv_shapes(x, weight, bias, valid_len, conv0)
-    dev, dt = x.device, x.dtype
-    stream, raw = _stream(stream, dev)
-    if y is None:
-        y = _empty(stream, (nb, L, nd), dt, dev)
-    else:
-        _want("y", y, (nb, L, nd), dt, dev, False)
-    if conv_last is not None:
-        _want("conv_last", conv_last, (nb, W - 1, nd), dt, dev)
-    elif return_conv_last:
-        conv_last = _empty(stream, (nb, W - 1, nd), dt, dev)
-    args = _b.ssm_conv_fwd_io(x.data_ptr(), weight.data_ptr(), _ptr(bias), _ptr(valid_len), _ptr(conv0), y.data_ptr(),
-                              _ptr(conv_last), x.stride(0), x.stride(1), y.stride(0), y.stride(1))
-    dims = _b.ssm_conv_dims(nb, L, nd, W, io, 1 if silu else 0)
-    _call(_b.lib().ssm_causal_conv_fwd, "ssm_causal_conv_fwd", dims, args, raw, dev)
-    return y, conv_last
+    if stream is not None:
+        with _on(stream, x):
+            return causal_conv_fwd(x, weight, bias, valid_len, silu=silu, conv0=conv0, y=y, conv_last=conv_last,
+                                   return_conv_last=return_conv_last)
+    return _native.conv_fwd(x, weight, bias, valid_len, silu, conv0, y, conv_last, return_conv_last)
 
 
 def causal_conv_bwd(x, weight, bias, valid_len, dy, *, silu: bool = True, conv0=None, dconv_last=None, dx=None,
@@ -251,44 +120,16 @@ def causal_conv_bwd(x, weight, bias, valid_len, dy, *, silu: bool = True, conv0=
     [dim, width], dbias [dim] (None without bias), both float32, and dconv0
     [batch, width - 1, dim] in x's dtype (None without conv0).
     """
-    io = _io(x)
-    nb, L, nd, W = _conv_shapes(x, weight, bias, valid_len, conv0)
-    dev, dt = x.device, x.dtype
-    _want("dy", dy, (nb, L, nd), dt, dev, False)
-    if dconv_last is not None:
-        _want("dconv_last", dconv_last, (nb, W - 1, nd), dt, dev)
-    stream, raw = _stream(stream, dev)
-    if dx is None:
-        dx = _empty(stream, (nb, L, nd), dt, dev)
-    else:
-        _want("dx", dx, (nb, L, nd), dt, dev, False)
-    dweight = _empty(stream, (nd, W), torch.float32, dev)
-    dbias = None if bias is None else _empty(stream, (nd,), torch.float32, dev)
-    dconv0 = None if conv0 is None else _empty(stream, (nb, W - 1, nd), dt, dev)
-    dims = _b.ssm_conv_dims(nb, L, nd, W, io, 1 if silu else 0)
-    ws = _scratch(stream, workspace, _b.lib().ssm_causal_conv_bwd_workspace_bytes(ctypes.byref(dims)), dev)
-    args = _b.ssm_conv_bwd_io(x.data_ptr(), weight.data_ptr(), _ptr(bias), _ptr(valid_len), _ptr(conv0), dy.data_ptr(),
-                              _ptr(dconv_last), dx.data_ptr(), dweight.data_ptr(), _ptr(dbias), _ptr(dconv0),
-                              ws.data_ptr(), ws.numel(), x.stride(0), x.stride(1), dy.stride(0), dy.stride(1),
-                              dx.stride(0), dx.stride(1))
-    _call(_b.lib().ssm_causal_conv_bwd, "ssm_causal_conv_bwd", dims, args, raw, dev)
+    if stream is not None:
+        with _on(stream, x):
+            return causal_conv_bwd(x, weight, bias, valid_len, dy, silu=silu, conv0=conv0, dconv_last=dconv_last,
+                                   dx=dx, workspace=workspace)
+    dx, dweight, dbias, dconv0 = _native.conv_bwd(x, weight, bias, valid_len, silu, conv0, dy, dconv_last, dx,
+                                                  workspace)
     return dict(dx=dx, dweight=dweight, dbias=dbias, dconv0=dconv0)
 
 
 # ---- norms -----------------------------------------------------------------
-
-def _norm_shape(x, weight, valid_len):
-    if x.dim() not in (2, 3):
-        raise ValueError("rows must be [rows, dim] or [batch, L, dim]")
-    if valid_len is not None and x.dim() != 3:
-        raise ValueError("valid_len needs rows laid out as [batch, L, dim]")
-    nd = x.shape[-1]
-    nb, L = (x.shape[0], 1) if x.dim() == 2 else (x.shape[0], x.shape[1])
-    _want("weight", weight, (nd,), torch.float32, x.device)
-    if valid_len is not None:
-        _want("valid_len", valid_len, (nb,), torch.int32, x.device)
-    return nb, L, nd
-
 
 def layer_norm_fwd(x, weight, bias=None, valid_len=None, *, residual=None, eps: float = 1e-5, rms: bool = False,
                    y=None, residual_out=None, return_stats: bool = False, stream=None):
@@ -305,37 +146,11 @@ def layer_norm_fwd(x, weight, bias=None, valid_len=None, *, residual=None, eps: 
     it may be given, as residual itself for an update in place, or without a
     residual to start a residual stream in its own dtype.
     """
-    io = _io(x)
-    nb, L, nd = _norm_shape(x, weight, valid_len)
-    dev, dt, shape = x.device, x.dtype, tuple(x.shape)
-    _want("x", x, shape, dt, dev)
-    if bias is not None:
-        _want("bias", bias, (nd,), torch.float32, dev)
-    like = residual if residual is not None else residual_out
-    rdt = dt if like is None else like.dtype
-    if rdt != dt and rdt != torch.float32:
-        raise TypeError("residual must be float32 or of x's dtype")
-    if residual is not None:
-        _want("residual", residual, shape, rdt, dev)
-    stream, raw = _stream(stream, dev)
-    if y is None:
-        y = _empty(stream, shape, dt, dev)
-    else:
-        _want("y", y, shape, dt, dev)
-    if residual_out is not None:
-        _want("residual_out", residual_out, shape, rdt, dev)
-    elif residual is not None:
-        residual_out = _empty(stream, shape, rdt, dev)
-    mean = rstd = None
-    if return_stats:
-        rstd = _empty(stream, shape[:-1], torch.float32, dev)
-        if not rms:
-            mean = _empty(stream, shape[:-1], torch.float32, dev)
-    dims = _b.ssm_norm_dims(nb, L, nd, io, _IO[rdt], 1 if rms else 0, eps)
-    args = _b.ssm_norm_fwd_io(x.data_ptr(), _ptr(residual), weight.data_ptr(), _ptr(bias), _ptr(valid_len),
-                              y.data_ptr(), _ptr(residual_out), _ptr(mean), _ptr(rstd))
-    _call(_b.lib().ssm_layer_norm_fwd, "ssm_layer_norm_fwd", dims, args, raw, dev)
-    return (y, residual_out, mean, rstd) if return_stats else (y, residual_out)
+    if stream is not None:
+        with _on(stream, x):
+            return layer_norm_fwd(x, weight, bias, valid_len, residual=residual, eps=eps, rms=rms, y=y,
+                                  residual_out=residual_out, return_stats=return_stats)
+    return _native.norm_fwd(x, weight, bias, valid_len, residual, eps, rms, y, residual_out, return_stats)
 
 
 def layer_norm_bwd(dy, v, weight, mean, rstd, valid_len=None, *, dresidual_out=None, with_bias: bool = True,
@@ -349,30 +164,10 @@ def layer_norm_bwd(dy, v, weight, mean, rstd, valid_len=None, *, dresidual_out=N
     one; None unless ``with_residual``, which follows dresidual_out if None);
     dweight and dbias (None without ``with_bias``) [dim] float32.
     """
-    io = _io(dy, "dy")
-    nb, L, nd = _norm_shape(dy, weight, valid_len)
-    dev, dt, shape = dy.device, dy.dtype, tuple(dy.shape)
-    if v.dtype != dt and v.dtype != torch.float32:
-        raise TypeError("v must be float32 or of dy's dtype")
-    _want("dy", dy, shape, dt, dev)
-    _want("v", v, shape, v.dtype, dev)
-    if mean is not None:
-        _want("mean", mean, shape[:-1], torch.float32, dev)
-    _want("rstd", rstd, shape[:-1], torch.float32, dev)
-    if dresidual_out is not None:
-        _want("dresidual_out", dresidual_out, shape, v.dtype, dev)
-    stream, raw = _stream(stream, dev)
-    dx = _empty(stream, shape, dt, dev)
-    wanted = dresidual_out is not None if with_residual is None else with_residual
-    apart = wanted and v.dtype != dt
-    dresidual = _empty(stream, shape, v.dtype, dev) if apart else None
-    dweight = _empty(stream, (nd,), torch.float32, dev)
-    dbias = _empty(stream, (nd,), torch.float32, dev) if with_bias else None
-    # eps went into rstd; the library wants a positive one all the same
-    dims = _b.ssm_norm_dims(nb, L, nd, io, _IO[v.dtype], 1 if mean is None else 0, 1.0)
-    ws = _scratch(stream, workspace, _b.lib().ssm_layer_norm_bwd_workspace_bytes(ctypes.byref(dims)), dev)
-    args = _b.ssm_norm_bwd_io(dy.data_ptr(), v.data_ptr(), weight.data_ptr(), _ptr(mean), rstd.data_ptr(),
-                              _ptr(valid_len), _ptr(dresidual_out), dx.data_ptr(), _ptr(dresidual), dweight.data_ptr(),
-                              _ptr(dbias), ws.data_ptr(), ws.numel())
-    _call(_b.lib().ssm_layer_norm_bwd, "ssm_layer_norm_bwd", dims, args, raw, dev)
-    return dict(dx=dx, dresidual=dresidual if apart else (dx if wanted else None), dweight=dweight, dbias=dbias)
+    if stream is not None:
+        with _on(stream, dy):
+            return layer_norm_bwd(dy, v, weight, mean, rstd, valid_len, dresidual_out=dresidual_out,
+                                  with_bias=with_bias, with_residual=with_residual, workspace=workspace)
+    dx, dresidual, dweight, dbias = _native.norm_bwd(dy, v, weight, mean, rstd, valid_len, dresidual_out, with_bias,
+                                                     with_residual, workspace)
+    return dict(dx=dx, dresidual=dresidual, dweight=dweight, dbias=dbias)

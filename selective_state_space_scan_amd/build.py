@@ -25,6 +25,10 @@ LIB_PATH = os.path.join(PKG_DIR, "libssmscan.so")
 # library of their own, not part of the scan.
 PEAKS_SRC = os.path.join(PKG_DIR, "csrc", "ssm_peaks.hip")
 PEAKS_LIB_PATH = os.path.join(PKG_DIR, "libssmpeaks.so")
+# The CPython module that marshals torch tensors for the operators beside the
+# scan: host code, compiled against torch's headers.
+TORCH_SRC = os.path.join(PKG_DIR, "csrc", "ssm_torch.cpp")
+TORCH_LIB_PATH = os.path.join(PKG_DIR, "_ssm_torch.so")
 ARCH = "gfx950"
 
 
@@ -55,6 +59,32 @@ def link_command(out: str, objs: list[str]) -> list[str]:
     return [hipcc(), f"--offload-arch={ARCH}", "-shared", "-fPIC", "-o", out, *objs]
 
 
+def torch_command(out: str) -> list[str]:
+    import sysconfig
+
+    import torch
+    from torch.utils import cpp_extension
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    return ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM=1",
+            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}", f"-I{INCLUDE_DIR}",
+            "-isystem", sysconfig.get_paths()["include"],
+            *(a for p in [*cpp_extension.include_paths(), "/opt/rocm/include"] for a in ("-isystem", p)),
+            TORCH_SRC, "-o", out, f"-L{lib}", "-lc10", "-lc10_hip", "-ltorch_cpu", "-ltorch", "-ltorch_python"]
+
+
+def _compile_torch(out: str, verbose: bool) -> str:
+    """The CPython module `out` (replaced only once its compilation succeeded)."""
+    tmp = out + f".tmp{os.getpid()}"
+    try:
+        _run(torch_command(tmp), verbose)
+    except RuntimeError:
+        if os.path.exists(tmp):
+            os.remove(tmp)
+        raise
+    os.replace(tmp, out)
+    return out
+
+
 def _run(cmd: list[str], verbose: bool) -> None:
     if verbose:
         print(" ".join(cmd), flush=True)
@@ -63,7 +93,7 @@ def _run(cmd: list[str], verbose: bool) -> None:
     noise = "is not a recognized feature for this target"
     msgs = "\n".join(l for l in (res.stdout + res.stderr).splitlines() if noise not in l)
     if res.returncode != 0:
-        raise RuntimeError(f"hipcc failed ({res.returncode}):\n{msgs}")
+        raise RuntimeError(f"{os.path.basename(cmd[0])} failed ({res.returncode}):\n{msgs}")
     if verbose and msgs.strip():
         print(msgs, file=sys.stderr)
 
@@ -89,9 +119,11 @@ def _compile(out: str, srcs: list[str], verbose: bool) -> str:
 
 
 def build(verbose: bool = False) -> str:
-    """Compile ``libssmscan.so`` (and the benchmark's ``libssmpeaks.so``) next
-    to this file and return the scan library's path."""
+    """Compile ``libssmscan.so`` (with the torch marshalling module and the
+    benchmark's ``libssmpeaks.so``) next to this file and return the scan
+    library's path."""
     _compile(PEAKS_LIB_PATH, [PEAKS_SRC], verbose)
+    _compile_torch(TORCH_LIB_PATH, verbose)
     return _compile(LIB_PATH, SRCS, verbose)
 
 

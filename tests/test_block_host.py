@@ -326,3 +326,29 @@ def test_binding_rejects_cpu_tensors():
               lambda: ssm.layer_norm_bwd(x, x, torch.zeros(16), None, torch.zeros(2))):
         with pytest.raises(ValueError):
             f()
+
+
+def test_marshalling_module_is_built_and_refuses_plainly():
+    """The CPython module loads, and what is no tensor, or too few arguments, is a Python exception."""
+    import torch
+    from selective_state_space_scan_amd import _block
+    from selective_state_space_scan_amd import build as B
+    import os
+    assert os.path.exists(B.TORCH_LIB_PATH), "run __graft_entry__.build() first"
+    n = _block._native
+    with pytest.raises(TypeError):
+        n.scan_step()
+    with pytest.raises(TypeError):
+        n.conv_step(1, 2, 3, None, True, None, None, None)
+    with pytest.raises(ValueError):
+        n.conv_step(torch.zeros(2, 16), torch.zeros(2, 3, 16), torch.zeros(16, 4), None, True, None, None, None)
+    with pytest.raises(TypeError):
+        n.bind(1, 2)
+
+
+def test_marshalling_module_is_host_code():
+    """Compiled by the host compiler against torch's headers; no GPU source in it."""
+    from selective_state_space_scan_amd import build as B
+    cmd = B.torch_command("/tmp/x.so")
+    assert cmd[0] == "g++" and cmd[cmd.index("-o") + 1] == "/tmp/x.so" and B.TORCH_SRC in cmd
+    assert "-lc10_hip" in cmd and "-ltorch_python" in cmd and not any("offload-arch" in a for a in cmd)
