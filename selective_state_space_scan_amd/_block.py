@@ -39,7 +39,10 @@ def _on(stream, x):
     orders with them."""
     if not torch.is_tensor(x) or x.device.type != "cuda":
         raise ValueError("tensors must be on a GPU device")
-    return torch.cuda.stream(_b._stream_for(stream, x.device))
+    stream = _b._stream_for(stream, x.device)
+    if stream.device != x.device:
+        raise ValueError(f"the stream belongs to {stream.device}, the tensors to {x.device}")
+    return torch.cuda.stream(stream)
 
 
 # ---- single tokens ---------------------------------------------------------

@@ -96,7 +96,7 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void norm_fwd_kernel(const N
   constexpr int V = VecIO<IO>::kWide, BLOCK = TPR > 256 ? TPR : 256, RPB = BLOCK / TPR;
   __shared__ float lds[BLOCK / 64 * 2];
   const int lane = threadIdx.x % TPR;
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * RPB + threadIdx.x / TPR;
+  const int64_t row = (static_cast<int64_t>(blockIdx.y) * gridDim.x + blockIdx.x) * RPB + threadIdx.x / TPR;
   const bool valid = row_valid(prm.valid_len, row, prm.rows, prm.L);
   const int64_t at = row * prm.nd;
   float v[NV][V];
@@ -139,7 +139,9 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void norm_fwd_kernel(const N
     }
   row_sums<TPR>(s, lds);
   const float off = prm.rms ? 0.0f : s[0] * prm.inv_n;
-  const float var = __builtin_fmaf(-off, off, s[1] * prm.inv_n);
+  // far from zero a constant row's two terms agree but for their rounding
+  float var = __builtin_fmaf(-off, off, s[1] * prm.inv_n);
+  var = var < 0.0f ? 0.0f : var;
   const float rstd = 1.0f / __builtin_sqrtf(var + prm.eps);
   if (row >= prm.rows) return;
   if (lane == 0) {
@@ -366,10 +368,13 @@ int ssm_layer_norm_fwd(ssm_scan_t handle, const ssm_norm_dims* dims, const ssm_n
   bool fits = true;
   for_norm(dims, [&]<typename IO, typename RT, int TPR, int NV>() {
     constexpr int BLOCK = block_of<TPR>, RPB = BLOCK / TPR;
-    const int64_t blocks = (rows + RPB - 1) / RPB;
-    fits = grid_fits(blocks, BLOCK);
+    // a grid's side holds fewer than 2^32 lanes: more rows take another side
+    const int64_t blocks = (rows + RPB - 1) / RPB, wide = blocks < (1 << 21) ? blocks : 1 << 21;
+    const int64_t high = (blocks + wide - 1) / wide;
+    fits = high <= 65535;
     if (fits)
-      hipLaunchKernelGGL((norm_fwd_kernel<IO, RT, TPR, NV>), dim3(static_cast<unsigned>(blocks)), dim3(BLOCK), 0,
+      hipLaunchKernelGGL((norm_fwd_kernel<IO, RT, TPR, NV>),
+                         dim3(static_cast<unsigned>(wide), static_cast<unsigned>(high)), dim3(BLOCK), 0,
                          static_cast<hipStream_t>(stream), p);
   });
   return fits ? launched() : SSM_ERR_UNSUPPORTED;

@@ -65,6 +65,10 @@ CONV = [
     ("f32", 2, 260, 33, 2, [-4, 999]),
     ("bf16", 2, 600, 24, 4, [513, 600]),
     ("f32", 5, 64, 520, 4, [64, 63, 32, 31, 33]),
+    ("bf16", 2, 40, 3, 4, [40, 5]),
+    ("bf16", 1, 70, 2, 3, None),
+    ("f32", 1, 20, 5, 4, None),
+    ("bf16", 2, 16, 1, 2, [16, 13]),
 ]
 
 
@@ -110,6 +114,28 @@ def test_conv_bwd(io, B, L, D, W, lens, carry, wide, silu):
         assert not bits(g["dx"])[b, n:].any()
     if wide:
         assert (dx[..., D:] == 7).all()   # the other half of the buffer is left alone
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+def test_conv_large(io):
+    """Work enough for the forward's long chunks and for several runs a workgroup in the backward, rows of every kind
+    of length, an odd width."""
+    import selective_state_space_scan_amd as ssm
+    B, L, D, W = 5, 3500, 1001, 4
+    lens = [3500, 3487, 12, 0, 1777]
+    c = conv_inputs(io, B, L, D, W, 18)
+    y, last = ssm.causal_conv_fwd(c["x"], c["w"], c["b"], i32(lens), conv0=c["c0"])
+    g = ssm.causal_conv_bwd(c["x"], c["w"], c["b"], i32(lens), c["dy"], conv0=c["c0"], dconv_last=c["dl"])
+    sync()
+    a = (n64(c["x"]), n64(c["w"]), n64(c["b"]), lens)
+    ry, rl, tol = R.conv_fwd(*a, n64(c["c0"]), True, io)
+    R.check("y", n64(y), ry, tol)
+    assert np.array_equal(n64(last), rl)
+    ref, tol = R.conv_bwd(*a, n64(c["dy"]), n64(c["c0"]), n64(c["dl"]), True, io)
+    for k in ref:
+        R.check(k, n64(g[k]), ref[k], tol[k])
+    again = ssm.causal_conv_bwd(c["x"], c["w"], c["b"], i32(lens), c["dy"], conv0=c["c0"], dconv_last=c["dl"])
+    assert all(np.array_equal(bits(g[k]), bits(again[k])) for k in g)   # run to run
 
 
 @pytest.mark.parametrize("io", ["f32", "bf16"])
@@ -361,16 +387,18 @@ def test_idle_rows_read_nothing():
     assert ssm.causal_conv_step(x[:0], c, w, slots=slots[:0]).shape == (0, D)
 
 
-def test_many_rows_with_repeated_slots():
-    """More rows than lanes of a workgroup, every slot named three times: the first of each takes the step."""
+@pytest.mark.parametrize("D", [24, 330])
+def test_many_rows_with_repeated_slots(D):
+    """More rows than a wave's lanes, every slot named three times and one a fourth: the first of each takes the step.
+    The wider one runs two rows a workgroup, the last alone."""
     import torch
     import selective_state_space_scan_amd as ssm
-    B, D, N, W = 900, 24, 16, 4
+    B, N, W = 901, 16, 4
     g = Gen(24, "f32")
     x, dl, bm, cm = g.normal(B, D), g.normal(B, D), g.normal(B, N), g.normal(B, N)
     A, w = g.normal(D, N, io="f32"), g.normal(D, W, io="f32")
     h, c = g.normal(300, D, N), g.normal(300, W - 1, D)
-    order = torch.cat([torch.randperm(300, generator=g.g) for _ in range(3)]).to(DEV, torch.int32)
+    order = torch.cat([torch.randperm(300, generator=g.g) for _ in range(3)] + [torch.tensor([7])]).to(DEV, torch.int32)
     first = 300   # each permutation names every slot once
     h1, c1 = h.clone(), c.clone()
     y = ssm.selective_scan_step(x, dl, A, bm, cm, None, h1, slots=order)
@@ -493,6 +521,21 @@ def test_norm_rows_far_from_zero_and_constant_rows():
     R.check("mean", n64(mean), rm, tm)
     R.check("rstd", n64(rstd), rr, tr)
     assert torch.equal(y[3], b) and torch.equal(y[4], b)
+
+
+@pytest.mark.parametrize("D", [7, 700, 5001])
+def test_norm_constant_rows_far_from_zero(D):
+    """The variance of a constant row is what rounding leaves of zero: it must not come out negative."""
+    import torch
+    import selective_state_space_scan_amd as ssm
+    x = torch.tensor([1e9, -3.3e9, 7.7e10, 1.1e12, 3e5, 123456.7], device=DEV)[:, None].expand(6, D).contiguous()
+    w = torch.ones(D, device=DEV)
+    y, _, mean, rstd = ssm.layer_norm_fwd(x, w, return_stats=True)
+    sync()
+    (ry, _, rm, _), (ty, _, tm, _) = R.norm_fwd(n64(x), n64(w), None)
+    R.check("y", n64(y), ry, ty)
+    R.check("mean", n64(mean), rm, tm)
+    assert torch.isfinite(rstd).all() and (rstd > 0).all()
 
 
 def test_norm_bad_rows_stay_alone():
@@ -779,6 +822,10 @@ def test_refusals():
         lambda: ssm.layer_norm_bwd(x.float(), x, nw, None, torch.zeros((2, 8), device=DEV)),
         lambda: ssm.layer_norm_bwd(x, x, nw, None, torch.zeros(16, device=DEV)),
     ]
+    for k in (1.5, "x", None):
+        bad.append(lambda k=k: ssm.causal_conv_fwd(k, w))
+    bad.append(lambda: ssm.selective_scan_step(t, t, A, bm, bm, None, h, delta_clamp=(0.1,)))
+    bad.append(lambda: ssm.selective_scan_step(t, t, A, bm, bm, None, h, delta_clamp=0.1))
     for i, f in enumerate(bad):
         with pytest.raises((ValueError, TypeError)):
             f()
