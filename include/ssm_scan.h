@@ -66,10 +66,11 @@ enum ssm_io_dtype { SSM_IO_F32 = 0, SSM_IO_BF16 = 1 };
 enum ssm_status {
   SSM_OK = 0,
   SSM_ERR_INVALID_ARG = -1,     /* NULL required pointer or handle, negative dim, bad flag or clip bounds */
-  SSM_ERR_UNSUPPORTED = -2,     /* dstate not 16/32/64, dim not a multiple of 16, misaligned pointer, wrong GPU,
-                                   one batch row of x, delta, B or C spanning 2 GiB or more, or a grid too
-                                   large */
-  SSM_ERR_ALIAS = -3,           /* y or h_last overlaps an input, or y overlaps h_last */
+  SSM_ERR_UNSUPPORTED = -2,     /* dstate not 16/32/64, dim not a multiple of 16 (scan) or above its limit (norm),
+                                   width not 2 to 4, misaligned pointer, wrong GPU, one batch row of x, delta, B
+                                   or C spanning 2 GiB or more (scan), or a grid too large */
+  SSM_ERR_ALIAS = -3,           /* an output overlaps an input or another output; strided tensors are compared
+                                   as the ranges from their first byte to their last */
   SSM_ERR_HIP = -4,             /* a HIP runtime or launch error */
   SSM_ERR_NO_DEVICE = -5,       /* no usable GPU at the requested ordinal */
   SSM_ERR_DEVICE_MISMATCH = -6, /* the calling thread's current device is not the handle's device */
@@ -368,7 +369,8 @@ int ssm_selective_scan_step(ssm_scan_t handle, const ssm_scan_dims* dims, const 
  *  conv0        [batch, width - 1, dim] io dtype or NULL, oldest first.
  *  conv_last    like conv0, or NULL: the last width - 1 inputs of every row
  *               (its conv0's for the part that a short row does not fill),
- *               exact copies.
+ *               exact copies.  Not conv0's buffer: a row of many lanes reads
+ *               the one while it writes the other.
  *
  * dim may be any number.  Sizes are below 2^31 (SSM_ERR_UNSUPPORTED).  The
  * conventions are the scan's: host-side checks first, asynchronous, nothing
@@ -513,7 +515,8 @@ int ssm_layer_norm_fwd(ssm_scan_t handle, const ssm_norm_dims* dims, const ssm_n
  *               two types (x and the residual enter v alike).
  *  dweight      [dim] fp32;  dbias [dim] fp32 or NULL.
  *  workspace    at least ssm_layer_norm_bwd_workspace_bytes(dims) bytes of
- *               device scratch (4-byte aligned), overwritten. */
+ *               device scratch (4-byte aligned), overwritten.
+ * Rows past valid_len give +0 in dx and dresidual and add nothing. */
 typedef struct ssm_norm_bwd_io {
   const void* dy;
   const void* v;

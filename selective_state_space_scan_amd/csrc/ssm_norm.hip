@@ -15,6 +15,11 @@
 // a lane, 64 to 1024 lanes a row (dim <= 16384).  The mean is subtracted before
 // squares are summed, and the small sum of the differences corrects both it and
 // the variance, so rows whose mean is far from zero lose nothing.
+//
+// Measured, 32768 rows x 1024 in bf16 with the residual stream in fp32 (a copy of
+// 1 GiB: 5.3 TB/s): forward 77 us, 5.2 TB/s; backward 97 us and 4 for the second
+// pass, 5.3 TB/s.  24 rows x 1000 fp32 forward 3.3 us, 1021 x 600 backward 8.9 us
+// (two dependent launches).
 
 #include <hip/hip_runtime.h>
 
@@ -113,8 +118,11 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void norm_fwd_kernel(const N
 #pragma unroll
       for (int i = 0; i < V; ++i) v[k][i] += r[i];
     }
-    if (prm.residual_out != nullptr && row < prm.rows)
-      store_n<RT, V>(static_cast<RT*>(prm.residual_out) + at + d, n[k], v[k]);
+  }
+  if (prm.residual_out != nullptr && row < prm.rows) {
+#pragma unroll
+    for (int k = 0; k < NV; ++k)
+      store_n<RT, V>(static_cast<RT*>(prm.residual_out) + at + (k * TPR + lane) * V, n[k], v[k]);
   }
   float mean = 0.0f;
   if (!prm.rms) {

@@ -1047,9 +1047,10 @@ const char* ssm_scan_error_string(int code) {
     case SSM_ERR_INVALID_ARG:
       return "invalid argument (null pointer or handle, negative size, bad flag or clip bounds)";
     case SSM_ERR_UNSUPPORTED:
-      return "unsupported (dstate not 16/32/64, dim not a multiple of 16, misaligned pointer, or not gfx950)";
+      return "unsupported (dstate not 16/32/64, dim not a multiple of 16 (scan) or above 16384 (norm), width not 2 to 4, "
+             "a size above its limit, misaligned pointer, or not gfx950)";
     case SSM_ERR_ALIAS:
-      return "an output overlaps an input or the other output";
+      return "an output overlaps an input or another output";
     case SSM_ERR_HIP:
       return "HIP runtime or launch error";
     case SSM_ERR_NO_DEVICE:

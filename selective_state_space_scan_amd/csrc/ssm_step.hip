@@ -14,6 +14,11 @@
 // Layout: a lane owns four adjacent states of one channel (16 bytes), so a
 // wave reads 1 KB of one cache row; a channel's dstate / 4 lanes are adjacent
 // and add their parts of C.h' by DPP within a row of 16 lanes.
+//
+// Measured: 256 rows x 2048 channels x 16 states in bf16, 69 MB: 15.3 us without
+// slots, 17.0 us on 256 of 512 slots (4.0 TB/s; a copy of 1 GiB runs at 5.3): a
+// row's slot has to be there before its states can be asked for.  One row:
+// 2.4 us, the latency of two dependent reads.
 
 #include <hip/hip_runtime.h>
 
