@@ -56,6 +56,13 @@ struct VecIO<float> {
       }
     }
   }
+  // a store past the caches, for what is not read again soon
+  static __device__ __forceinline__ void stream(float* p, const float (&o)[4]) {
+    vec4 v;
+    v.x = o[0], v.y = o[1], v.z = o[2], v.w = o[3];
+    __builtin_nontemporal_store(v, reinterpret_cast<vec4*>(p));
+  }
+  static __device__ __forceinline__ void stream(float* p, const float (&o)[1]) { *p = o[0]; }
   static __device__ __forceinline__ float get(const float* p) { return *p; }
   static __device__ __forceinline__ void put(float* p, float v) { *p = v; }
 };
@@ -120,6 +127,12 @@ struct VecIO<uint16_t> {
       }
     }
   }
+  static __device__ __forceinline__ void stream(uint16_t* p, const float (&o)[4]) {
+    vec2 v;
+    v.x = pack(o[0], o[1]), v.y = pack(o[2], o[3]);
+    __builtin_nontemporal_store(v, reinterpret_cast<vec2*>(p));
+  }
+  static __device__ __forceinline__ void stream(uint16_t* p, const float (&o)[1]) { put(p, o[0]); }
   static __device__ __forceinline__ float get(const uint16_t* p) {
     return __builtin_bit_cast(float, static_cast<uint32_t>(*p) << 16);
   }

@@ -22,8 +22,8 @@
 // the sizes below, the backward fetching 16 % over its inputs (now 4 %).
 //
 // Measured (copy of 1 GiB: 5.3 TB/s): forward of 16 rows of up to 8192 steps x
-// 512 channels, bf16, lengths uniform: 36.3 us, 5.5 TB/s of what it has to
-// move.  Backward of 8 x 4096 x 1024 bf16, W = 4, silu: 46 us and 4 for the
+// 512 channels, bf16, lengths uniform: 29.6 us, 6.8 TB/s of what it has to move
+// (the inputs partly from the 256 MiB cache).  Backward of 8 x 4096 x 1024 bf16, W = 4, silu: 46 us and 4 for the
 // second pass, 4.0 TB/s: the vector units are busy two thirds of it (26
 // operations a step and channel, 16/13 of the g's), fp32 of half the elements
 // moves 4.6 TB/s.  2 x 256 x 64 fp32: 3.8 us forward; 3 x 1021 x 200: 8.9 us
@@ -159,6 +159,11 @@ __device__ __forceinline__ void input_at(const IO* x, const IO* conv0, int64_t t
 
 // One lane: T steps of V channels.  Chunks, not channels, run over the grid's
 // slow index, so that a workgroup's lanes cover whole rows where dim allows.
+// y is stored past the caches, which leaves them to the inputs: 36.4 -> 29.7 us
+// for 16 x 8192 x 512 ragged bf16, and with the copy that writes x and the
+// operator that reads y around it 205 -> 195 us (full rows; 8 x 4096 x 1024: 99.4
+// -> 97.2).  The same in the backward and the norms was no gain, or a loss with
+// what reads their outputs (norm and reader at 32768 x 2048: 192 -> 206 us).
 template <typename IO, int V, int W, bool SILU, int T>
 __global__ __launch_bounds__(256) void conv_fwd_kernel(const ConvParams prm) {
   // a launch has fewer than 2^32 work-items
@@ -197,7 +202,7 @@ __global__ __launch_bounds__(256) void conv_fwd_kernel(const ConvParams prm) {
 #pragma unroll
         for (int i = 0; i < V; ++i) p[i] *= sigmoid_for<IO>(p[i]);
       }
-      VecIO<IO>::store(yp + u * prm.y_ts, p);
+      VecIO<IO>::stream(yp + u * prm.y_ts, p);
       shift<W, V>(xs);
     };
     if (valid == T) {
@@ -210,7 +215,7 @@ __global__ __launch_bounds__(256) void conv_fwd_kernel(const ConvParams prm) {
     }
   }
   const float zero[V] = {};
-  for (int64_t t = v1 > c0 ? v1 : c0; t < c1; ++t) VecIO<IO>::store(y + t * prm.y_ts, zero);
+  for (int64_t t = v1 > c0 ? v1 : c0; t < c1; ++t) VecIO<IO>::stream(y + t * prm.y_ts, zero);
 
   // The row's last W-1 inputs, by the lanes of its first chunk.
   if (c0 == 0 && prm.conv_last != nullptr) {

@@ -118,11 +118,8 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void norm_fwd_kernel(const N
 #pragma unroll
       for (int i = 0; i < V; ++i) v[k][i] += r[i];
     }
-  }
-  if (prm.residual_out != nullptr && row < prm.rows) {
-#pragma unroll
-    for (int k = 0; k < NV; ++k)
-      store_n<RT, V>(static_cast<RT*>(prm.residual_out) + at + (k * TPR + lane) * V, n[k], v[k]);
+    if (prm.residual_out != nullptr && row < prm.rows)
+      store_n<RT, V>(static_cast<RT*>(prm.residual_out) + at + d, n[k], v[k]);
   }
   float mean = 0.0f;
   if (!prm.rms) {

@@ -15,10 +15,11 @@
 // wave reads 1 KB of one cache row; a channel's dstate / 4 lanes are adjacent
 // and add their parts of C.h' by DPP within a row of 16 lanes.
 //
-// Measured: 256 rows x 2048 channels x 16 states in bf16, 69 MB: 15.3 us without
-// slots, 17.0 us on 256 of 512 slots (4.0 TB/s; a copy of 1 GiB runs at 5.3): a
+// Measured: 256 rows x 2048 channels x 16 states in bf16, 69 MB: 15.4 us from 256
+// of 512 slots into another cache (4.5 TB/s; a copy of 1 GiB runs at 5.3); in
+// place, eight such caches in turn, 18.1 us a step and 16.7 without slots: a
 // row's slot has to be there before its states can be asked for.  One row:
-// 2.4 us, the latency of two dependent reads.
+// 2.6 us, the latency of two dependent reads.
 
 #include <hip/hip_runtime.h>
 
@@ -102,7 +103,9 @@ __global__ __launch_bounds__(256) void scan_step_kernel(const StepParams prm) {
       h[r][i] = __builtin_fmaf(fast_exp2(delta * a[i]), h[r][i], u * Bv[r][i]);
       sum = __builtin_fmaf(Cv[r][i], h[r][i], sum);
     }
-    VecIO<float>::store(prm.h_last + (slot[r] * static_cast<int64_t>(prm.nd) + d) * N + n0, h[r]);
+    // past the caches: next read a token and all other layers' states later
+    // (into another cache 17.7 -> 15.4 us; in place no difference)
+    VecIO<float>::stream(prm.h_last + (slot[r] * static_cast<int64_t>(prm.nd) + d) * N + n0, h[r]);
     sum = group_sum<LPC>(sum);
     if (n0 == 0) {
       if (prm.D != nullptr) sum = __builtin_fmaf(skip, x[r], sum);
@@ -115,7 +118,8 @@ __global__ __launch_bounds__(256) void scan_step_kernel(const StepParams prm) {
 // Rows of a workgroup where there are slots and kSeveral workgroups of one row:
 // they share the look through the slots and its latency.  us at 1 / 2 / 4 rows,
 // 2048 channels, dstate 16: 64 rows 6.3 / 6.4 / 7.5, 128 rows 10.4 / 10.2 / 10.6,
-// 256 rows 18.0 / 17.5 / 18.6, 1024 rows x 1024 channels 44.7 / 39.8 / 42.5.
+// 256 rows 18.0 / 17.5 / 18.6, 1024 rows x 1024 channels 44.7 / 39.8 / 42.5 (with
+// cached stores).
 // Without slots one row is the faster (256 rows 15.3 / 15.9).
 constexpr int kStepRows = 2;
 constexpr int64_t kSeveral = 4096;
