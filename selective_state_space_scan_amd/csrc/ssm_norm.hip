@@ -11,15 +11,15 @@
 //     dw = sum over rows of dy xh,  db = sum over rows of dy
 //
 // About ten operations an element on 4 to 16 bytes: bound by memory.  A row is
-// held in registers between its one read and its one write: up to 16 elements
-// a lane, 64 to 1024 lanes a row (dim <= 16384).  The mean is subtracted before
+// held in registers between its one read and its one write: eight elements a
+// lane (16 beyond dim 8192), 64 to 1024 lanes a row (dim <= 16384).  The mean is subtracted before
 // squares are summed, and the small sum of the differences corrects both it and
 // the variance, so rows whose mean is far from zero lose nothing.
 //
 // Measured, 32768 rows x 1024 in bf16 with the residual stream in fp32 (a copy of
-// 1 GiB: 5.3 TB/s): forward 77 us, 5.2 TB/s; backward 97 us and 4 for the second
-// pass, 5.3 TB/s.  24 rows x 1000 fp32 forward 3.3 us, 1021 x 600 backward 8.9 us
-// (two dependent launches).
+// 1 GiB: 5.3 TB/s): forward 74.6 us, 5.4 TB/s; backward 96 us and 4 for the
+// second pass, 5.4 TB/s.  24 rows x 1000 fp32 forward 2.8 us, 1021 x 600 backward
+// 8.3 us (two dependent launches).
 
 #include <hip/hip_runtime.h>
 
@@ -282,53 +282,73 @@ int check_norm_dims(const ssm_norm_dims* dims) {
 }
 
 // Calls f.template operator()<IO, RT, TPR, NV>(): the fewest lanes a row that
-// hold it at kLaneElems each, then the fewest pieces.
-template <typename IO, typename RT, typename F>
+// hold it at E elements each (16 where 1024 lanes would not), one piece a lane
+// where a wave holds it so.
+template <int E, typename IO, typename RT, typename F>
 void for_row(int64_t nd, const F& f) {
   constexpr int V = VecIO<IO>::kWide;
   if (nd <= 64 * V)
     f.template operator()<IO, RT, 64, 1>();
-  else if (nd <= 64 * kLaneElems / 2)
-    f.template operator()<IO, RT, 64, kLaneElems / 2 / V>();
-  else if (nd <= 64 * kLaneElems)
-    f.template operator()<IO, RT, 64, kLaneElems / V>();
-  else if (nd <= 128 * kLaneElems)
-    f.template operator()<IO, RT, 128, kLaneElems / V>();
-  else if (nd <= 256 * kLaneElems)
-    f.template operator()<IO, RT, 256, kLaneElems / V>();
-  else if (nd <= 512 * kLaneElems)
-    f.template operator()<IO, RT, 512, kLaneElems / V>();
+  else if (nd <= 64 * 8)
+    f.template operator()<IO, RT, 64, 8 / V>();
+  else if (nd <= 64 * E)
+    f.template operator()<IO, RT, 64, E / V>();
+  else if (nd <= 128 * E)
+    f.template operator()<IO, RT, 128, E / V>();
+  else if (nd <= 256 * E)
+    f.template operator()<IO, RT, 256, E / V>();
+  else if (nd <= 512 * E)
+    f.template operator()<IO, RT, 512, E / V>();
+  else if (nd <= 1024 * E)
+    f.template operator()<IO, RT, 1024, E / V>();
   else
     f.template operator()<IO, RT, 1024, kLaneElems / V>();
 }
 
+// Eight elements a lane: more waves of fewer registers than with sixteen (us
+// forward / backward, 32768 x 1024 bf16 with an fp32 stream 74.6 / 100.2 against
+// 80.1 / 100.9; 16384 x 2048 fp32 96.6 against 101.6 forward; 24 x 1000 2.8 against
+// 3.3).  Rows of bf16 alone, 4 bytes an element, want the sixteen forward (24.3
+// against 27.5 us).
+constexpr int kShortElems = 8;
+
 template <typename F>
-void for_norm(const ssm_norm_dims* dims, const F& f) {
+void for_norm_fwd(const ssm_norm_dims* dims, bool residual, const F& f) {
   if (dims->io_dtype == SSM_IO_F32)
-    for_row<float, float>(dims->dim, f);
+    for_row<kShortElems, float, float>(dims->dim, f);
   else if (dims->residual_dtype == SSM_IO_F32)
-    for_row<uint16_t, float>(dims->dim, f);
+    for_row<kShortElems, uint16_t, float>(dims->dim, f);
+  else if (residual)
+    for_row<kShortElems, uint16_t, uint16_t>(dims->dim, f);
   else
-    for_row<uint16_t, uint16_t>(dims->dim, f);
+    for_row<kLaneElems, uint16_t, uint16_t>(dims->dim, f);
+}
+
+template <typename F>
+void for_norm_bwd(const ssm_norm_dims* dims, const F& f) {
+  if (dims->io_dtype == SSM_IO_F32)
+    for_row<kShortElems, float, float>(dims->dim, f);
+  else if (dims->residual_dtype == SSM_IO_F32)
+    for_row<kShortElems, uint16_t, float>(dims->dim, f);
+  else
+    for_row<kShortElems, uint16_t, uint16_t>(dims->dim, f);
 }
 
 template <int TPR>
 constexpr int block_of = TPR > 256 ? TPR : 256;
 
-int64_t lanes_per_row(int64_t nd) {
-  int64_t t = 64;
-  while (t < 1024 && nd > t * kLaneElems) t *= 2;
-  return t;
-}
-
-// Workgroups of the backward, each walking several rows: as many as 256 CUs
-// hold at once (three of 256 lanes by their registers, one of 512 or 1024), so
-// that none waits for another's end.  us at three / four a CU: 32768 x 1024 bf16
-// without residual 47.3 / 62.3, 16384 x 2048 with 105 / 122; at one / two of 512
-// lanes, 4096 x 8192 106 / 110.
-int64_t bwd_groups(int64_t rows, int64_t nd) {
-  const int64_t tpr = lanes_per_row(nd), rpb = tpr > 256 ? 1 : 256 / tpr;
-  const int64_t all = (rows + rpb - 1) / rpb, most = tpr > 256 ? 256 : 3 * 256;
+// Workgroups of the backward, each walking several rows, all on the GPU at
+// once (256 CUs), so that none waits for another's end.  Three a CU keep the
+// memory busy where a row has fp32 in it, five where all is bf16 (us at 3 / 4 / 5:
+// 32768 x 1024 with an fp32 stream 100.2 / 102.6 / 105.3, in bf16 63.4 / 56.9 / 53.0;
+// 16384 x 1024 fp32 49.7 / 51.7 / 53.2); one where a row takes more than 256 lanes
+// (4096 x 8192, one / two: 101.7 / 106.2).
+int64_t bwd_groups(const ssm_norm_dims* dims) {
+  int64_t tpr = 64;
+  while (tpr < 1024 && dims->dim > tpr * kShortElems) tpr *= 2;
+  const int64_t rows = dims->batch * dims->seqlen, rpb = tpr > 256 ? 1 : 256 / tpr;
+  const bool short_rows = dims->io_dtype == SSM_IO_BF16 && dims->residual_dtype == SSM_IO_BF16;
+  const int64_t all = (rows + rpb - 1) / rpb, most = 256 * (tpr > 256 ? 1 : short_rows ? 5 : 3);
   return all < most ? all : most;
 }
 
@@ -371,7 +391,7 @@ int ssm_layer_norm_fwd(ssm_scan_t handle, const ssm_norm_dims* dims, const ssm_n
   p.rows = rows, p.L = dims->seqlen, p.nd = static_cast<int32_t>(nd), p.rms = dims->rms;
   p.eps = dims->eps, p.inv_n = 1.0f / static_cast<float>(nd);
   bool fits = true;
-  for_norm(dims, [&]<typename IO, typename RT, int TPR, int NV>() {
+  for_norm_fwd(dims, io->residual != nullptr, [&]<typename IO, typename RT, int TPR, int NV>() {
     constexpr int BLOCK = block_of<TPR>, RPB = BLOCK / TPR;
     // a grid's side holds fewer than 2^32 lanes: more rows take another side
     const int64_t blocks = (rows + RPB - 1) / RPB, wide = blocks < (1 << 21) ? blocks : 1 << 21;
@@ -387,7 +407,7 @@ int ssm_layer_norm_fwd(ssm_scan_t handle, const ssm_norm_dims* dims, const ssm_n
 
 int64_t ssm_layer_norm_bwd_workspace_bytes(const ssm_norm_dims* dims) {
   if (check_norm_dims(dims) != SSM_OK) return -1;
-  return bwd_groups(dims->batch * dims->seqlen, dims->dim) * 2 * dims->dim * 4;
+  return bwd_groups(dims) * 2 * dims->dim * 4;
 }
 
 int ssm_layer_norm_bwd(ssm_scan_t handle, const ssm_norm_dims* dims, const ssm_norm_bwd_io* io, void* stream) {
@@ -429,8 +449,8 @@ int ssm_layer_norm_bwd(ssm_scan_t handle, const ssm_norm_dims* dims, const ssm_n
   p.ws = static_cast<float*>(io->workspace);
   p.rows = rows, p.L = dims->seqlen, p.nd = static_cast<int32_t>(nd), p.rms = dims->rms;
   p.with_bias = io->dbias != nullptr, p.inv_n = 1.0f / static_cast<float>(nd);
-  const int64_t groups = bwd_groups(rows, nd);
-  for_norm(dims, [&]<typename IO, typename RT, int TPR, int NV>() {
+  const int64_t groups = bwd_groups(dims);
+  for_norm_bwd(dims, [&]<typename IO, typename RT, int TPR, int NV>() {
     const auto kernel = p.with_bias ? norm_bwd_kernel<IO, RT, TPR, NV, true> : norm_bwd_kernel<IO, RT, TPR, NV, false>;
     hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>(groups)), dim3(block_of<TPR>), 0, s, p);
   });
