@@ -372,8 +372,8 @@ int ssm_selective_scan_step(ssm_scan_t handle, const ssm_scan_dims* dims, const 
  *               exact copies.  Not conv0's buffer: a row of many lanes reads
  *               the one while it writes the other.
  *
- * dim may be any number.  Sizes are below 2^31 (SSM_ERR_UNSUPPORTED).  The
- * conventions are the scan's: host-side checks first, asynchronous, nothing
+ * dim may be any number below 2^29, the other sizes below 2^31
+ * (SSM_ERR_UNSUPPORTED).  The conventions are the scan's: host-side checks first, asynchronous, nothing
  * allocated, bitwise reproducible, fp32 arithmetic rounded once to the io
  * dtype. */
 typedef struct ssm_conv_dims {

@@ -31,7 +31,16 @@ def _load():
     return _ssm_torch
 
 
-_native = _load()
+class _Unloaded:
+    """Stands for the module until its first use, so that importing the package needs no built library."""
+
+    def __getattr__(self, name):
+        global _native
+        _native = _load()
+        return getattr(_native, name)
+
+
+_native = _Unloaded()
 
 
 def _on(stream, x):

@@ -51,6 +51,9 @@ __device__ __forceinline__ int64_t first_channel(int64_t vec, int64_t nd) {
   return d < last ? d : last;
 }
 
+// The carried inputs of a row, (W-1) * dim, are counted in 32 bits.
+constexpr int64_t kMaxConvDim = 1 << 29;
+
 struct ConvParams {
   const void* x;
   const float* w;
@@ -486,7 +489,7 @@ int check_conv_dims(const ssm_conv_dims* dims) {
   if (dims->io_dtype != SSM_IO_F32 && dims->io_dtype != SSM_IO_BF16) return SSM_ERR_INVALID_ARG;
   if (dims->silu != 0 && dims->silu != 1) return SSM_ERR_INVALID_ARG;
   if (dims->width < 2 || dims->width > 4) return SSM_ERR_UNSUPPORTED;
-  if (dims->batch > kMaxSize || dims->seqlen > kMaxSize || dims->dim > kMaxSize) return SSM_ERR_UNSUPPORTED;
+  if (dims->batch > kMaxSize || dims->seqlen > kMaxSize || dims->dim >= kMaxConvDim) return SSM_ERR_UNSUPPORTED;
   return SSM_OK;
 }
 

@@ -207,7 +207,7 @@ def test_required_and_optional_pointers(op):
 @pytest.mark.parametrize("op", ["conv_fwd", "conv_bwd", "conv_step"])
 @pytest.mark.parametrize("kw,code", [
     (dict(batch=-1), INVALID), (dict(dim=-1), INVALID), (dict(io_dtype=2), INVALID), (dict(silu=2), INVALID),
-    (dict(width=1), UNSUPPORTED), (dict(width=5), UNSUPPORTED), (dict(dim=2**31), UNSUPPORTED),
+    (dict(width=1), UNSUPPORTED), (dict(width=5), UNSUPPORTED), (dict(dim=2**29), UNSUPPORTED),
     (dict(batch=2**31), UNSUPPORTED)])
 def test_conv_dims(op, kw, code):
     base = dict(seqlen=1) if op == "conv_step" else {}
@@ -335,7 +335,7 @@ def test_marshalling_module_is_built_and_refuses_plainly():
     from selective_state_space_scan_amd import build as B
     import os
     assert os.path.exists(B.TORCH_LIB_PATH), "run __graft_entry__.build() first"
-    n = _block._native
+    n = _block._load()
     with pytest.raises(TypeError):
         n.scan_step()
     with pytest.raises(TypeError):

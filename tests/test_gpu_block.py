@@ -789,6 +789,73 @@ def test_offsets_past_32_bits():
     assert torch.equal(g["dx"][L - 50:], gt["dx"])
 
 
+def test_given_outputs_and_scratch():
+    """Outputs and scratch that the caller owns are the ones written and returned."""
+    import torch
+    import selective_state_space_scan_amd as ssm
+    c = conv_inputs("bf16", 2, 60, 24, 4, 62)
+    y0, l0 = ssm.causal_conv_fwd(c["x"], c["w"], c["b"], conv0=c["c0"])
+    y, last = torch.zeros_like(y0), torch.zeros_like(l0)
+    r = ssm.causal_conv_fwd(c["x"], c["w"], c["b"], conv0=c["c0"], y=y, conv_last=last, return_conv_last=False)
+    assert r[0] is y and r[1] is last and torch.equal(y, y0) and torch.equal(last, l0)
+    y1, none = ssm.causal_conv_fwd(c["x"], c["w"], c["b"], conv0=c["c0"], return_conv_last=False)
+    assert none is None and torch.equal(y1, y0)
+    ws = torch.full((1 << 20,), 255, dtype=torch.uint8, device=DEV)   # NaN where read before written
+    g0 = ssm.causal_conv_bwd(c["x"], c["w"], c["b"], None, c["dy"])
+    g1 = ssm.causal_conv_bwd(c["x"], c["w"], c["b"], None, c["dy"], dx=y, workspace=ws)
+    assert g1["dx"] is y and all(torch.equal(g0[k], g1[k]) for k in ("dx", "dweight", "dbias"))
+    g = Gen(63, "bf16")
+    x, res, w = g.normal(70, 48), g.normal(70, 48, io="f32"), g.normal(48, io="f32")
+    a0, v0, m, s = ssm.layer_norm_fwd(x, w, residual=res, return_stats=True)
+    a, v = torch.zeros_like(a0), torch.zeros_like(v0)
+    r = ssm.layer_norm_fwd(x, w, residual=res, y=a, residual_out=v)
+    assert r[0] is a and r[1] is v and torch.equal(a, a0) and torch.equal(v, v0)
+    n0 = ssm.layer_norm_bwd(x, v0, w, m, s, dresidual_out=res)
+    ws.fill_(255)
+    n1 = ssm.layer_norm_bwd(x, v0, w, m, s, dresidual_out=res, workspace=ws)
+    assert all(torch.equal(n0[k], n1[k]) for k in n0)
+    n2 = ssm.layer_norm_bwd(x, v0, w, m, s, with_residual=True)   # the stream ends here: no gradient comes in
+    n3 = ssm.layer_norm_bwd(x, v0, w, m, s, dresidual_out=torch.zeros_like(res))
+    assert n2["dresidual"].dtype == torch.float32 and all(torch.equal(n2[k], n3[k]) for k in n2)
+    assert ssm.layer_norm_bwd(x, v0, w, m, s, dresidual_out=res, with_residual=False)["dresidual"] is None
+
+
+def test_most_rows():
+    """The largest batch of a step, one row more, and more rows of a norm than a grid's side takes."""
+    import torch
+    import selective_state_space_scan_amd as ssm
+    B, D, N, W = 65535, 8, 16, 4
+    g = Gen(64, "f32")
+    x, dl, bm = g.normal(B + 1, D), g.normal(B + 1, D), g.normal(B + 1, N)
+    A, w = g.normal(D, N), g.normal(D, W)
+    h, cache = g.normal(B + 1, D, N), g.normal(B + 1, W - 1, D)
+    sl = torch.randperm(B, generator=g.g).to(DEV, torch.int32)
+    h0, c0 = h.clone(), cache.clone()
+    y = ssm.selective_scan_step(x[:B], dl[:B], A, bm[:B], bm[:B], None, h, slots=sl)
+    yc = ssm.causal_conv_step(x[:B], cache, w, slots=sl)
+    at = sl.long()
+    hs, cs = h0[at], c0[at]
+    half = B // 2
+    for part in (slice(0, half), slice(half, B)):
+        hp, cp = hs[part].clone(), cs[part].clone()
+        assert torch.equal(y[part], ssm.selective_scan_step(x[:B][part], dl[:B][part], A, bm[:B][part], bm[:B][part], None, hp))
+        assert torch.equal(yc[part], ssm.causal_conv_step(x[:B][part], cp, w))
+        assert torch.equal(h[at[part]], hp) and torch.equal(cache[at[part]], cp)
+    for f in (lambda: ssm.selective_scan_step(x, dl, A, bm, bm, None, h), lambda: ssm.causal_conv_step(x, cache, w)):
+        with pytest.raises(ssm.SsmScanError) as e:
+            f()
+        assert e.value.code == ssm.SSM_ERR_UNSUPPORTED
+    rows = (1 << 23) + 5
+    v, nw = torch.randn((rows, 4), device=DEV), torch.ones(4, device=DEV)
+    y, _, m, r = ssm.layer_norm_fwd(v, nw, return_stats=True)
+    for part in (slice(0, 50), slice((1 << 23) - 9, rows)):
+        yp, _, mp, rp = ssm.layer_norm_fwd(v[part], nw, return_stats=True)
+        assert torch.equal(y[part], yp) and torch.equal(m[part], mp) and torch.equal(r[part], rp)
+    g = ssm.layer_norm_bwd(y, v, nw, m, r)
+    gp = ssm.layer_norm_bwd(y[-40:], v[-40:], nw, m[-40:], r[-40:])
+    assert torch.equal(g["dx"][-40:], gp["dx"])
+
+
 def test_refusals():
     import torch
     import selective_state_space_scan_amd as ssm
