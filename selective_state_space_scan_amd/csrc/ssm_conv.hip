@@ -26,7 +26,7 @@
 // (the inputs partly from the 256 MiB cache).  Backward of 8 x 4096 x 1024 bf16, W = 4, silu: 46 us and 4 for the
 // second pass, 4.0 TB/s: the vector units are busy two thirds of it (26
 // operations a step and channel, 16/13 of the g's), fp32 of half the elements
-// moves 4.6 TB/s.  2 x 256 x 64 fp32: 3.8 us forward; 3 x 1021 x 200: 8.9 us
+// moves 4.6 TB/s.  2 x 256 x 64 fp32: 3.8 us forward; 3 x 1021 x 200: 9.2 us
 // backward.  One token of 256 rows x 2048: 4.2 us, of one row 2.8.
 
 #include <hip/hip_runtime.h>
@@ -323,7 +323,8 @@ __global__ __launch_bounds__(256) void conv_bwd_kernel(const ConvBwdParams prm) 
             for (int i = 0; i < V; ++i) g[H][i] = 0.0f;
           }
         }
-        if (j < T) {
+        // past the row's end g = 0, but xs may still hold an infinity or NaN
+        if (j < T && (!EDGE || c0 + j < len)) {
 #pragma unroll
           for (int i = 0; i < V; ++i) {
 #pragma unroll

@@ -139,6 +139,30 @@ def test_conv_large(io):
 
 
 @pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("lens", [[37, 20, 52], None])
+def test_conv_bwd_last_input_not_finite(io, lens):
+    """An infinity or NaN as a row's last input meets one tap only: the steps behind it, which would bring it to the
+    others, are not the row's."""
+    import selective_state_space_scan_amd as ssm
+    B, L, D, W = 3, 52, 70, 4
+    c = conv_inputs(io, B, L, D, W, 19)
+    ends = R.lengths(lens, B, L)
+    bad, zero = c["x"].clone(), c["x"].clone()
+    for b, v in enumerate((float("inf"), float("nan"), -float("inf"))):
+        bad[b, ends[b] - 1, 4 + b], zero[b, ends[b] - 1, 4 + b] = v, 0.0
+    g, ref = (ssm.causal_conv_bwd(x, c["w"], c["b"], i32(lens), c["dy"], silu=False, conv0=c["c0"])
+              for x in (bad, zero))
+    sync()
+    for k in ("dx", "dbias", "dconv0"):   # without silu the inputs only reach the taps
+        assert np.array_equal(bits(g[k]), bits(ref[k])), k
+    got, want = n64(g["dweight"]), n64(ref["dweight"])
+    dy = n64(c["dy"])
+    for b, v in enumerate((np.inf, np.nan, -np.inf)):
+        want[4 + b, W - 1] = v * dy[b, ends[b] - 1, 4 + b]
+    assert np.array_equal(got, want, equal_nan=True)
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
 def test_conv_padding_reaches_nothing(io):
     """NaN, infinities and the type's lowest value past a row's end change no bit."""
     import torch
