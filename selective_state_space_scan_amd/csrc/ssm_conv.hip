@@ -26,7 +26,7 @@
 // (the inputs partly from the 256 MiB cache).  Backward of 8 x 4096 x 1024 bf16, W = 4, silu: 46 us and 4 for the
 // second pass, 4.0 TB/s: the vector units are busy two thirds of it (26
 // operations a step and channel, 16/13 of the g's), fp32 of half the elements
-// moves 4.6 TB/s.  2 x 256 x 64 fp32: 3.8 us forward; 3 x 1021 x 200: 9.2 us
+// moves 4.6 TB/s.  2 x 256 x 64 fp32: 3.8 us forward; 3 x 1021 x 200: 9.0 us
 // backward.  One token of 256 rows x 2048: 4.2 us, of one row 2.8.
 
 #include <hip/hip_runtime.h>
@@ -323,12 +323,17 @@ __global__ __launch_bounds__(256) void conv_bwd_kernel(const ConvBwdParams prm) 
             for (int i = 0; i < V; ++i) g[H][i] = 0.0f;
           }
         }
-        // past the row's end g = 0, but xs may still hold an infinity or NaN
-        if (j < T && (!EDGE || c0 + j < len)) {
+        if (j < T) {
 #pragma unroll
           for (int i = 0; i < V; ++i) {
 #pragma unroll
-            for (int k = 0; k < W; ++k) dw[k][i] = __builtin_fmaf(g[H][i], xs[k][i], dw[k][i]);
+            for (int k = 0; k < W; ++k) {
+              // past the row's end g = 0, but xs may still hold an infinity or NaN (a
+              // select: with a branch around the sums the registers fall to four
+              // waves' and full rows take 55.2 us for 53.3, ragged ones 65 for 69)
+              const float in = EDGE && c0 + j >= len ? 0.0f : xs[k][i];
+              dw[k][i] = __builtin_fmaf(g[H][i], in, dw[k][i]);
+            }
             dw[W][i] += g[H][i];
           }
         }
