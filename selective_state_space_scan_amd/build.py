@@ -14,6 +14,7 @@ import shutil
 import subprocess
 import sys
 import tempfile
+import warnings
 
 PKG_DIR = os.path.dirname(os.path.abspath(__file__))
 REPO_DIR = os.path.dirname(PKG_DIR)
@@ -119,12 +120,23 @@ def _compile(out: str, srcs: list[str], verbose: bool) -> str:
 
 
 def build(verbose: bool = False) -> str:
-    """Compile ``libssmscan.so`` (with the torch marshalling module and the
-    benchmark's ``libssmpeaks.so``) next to this file and return the scan
-    library's path."""
+    """Compile ``libssmscan.so`` (with the benchmark's ``libssmpeaks.so`` and
+    the torch marshalling module) next to this file and return the scan
+    library's path.
+
+    The libraries need hipcc alone.  The module comes last: where torch or g++
+    is missing it is left out with a warning, an older one of it removed (its
+    structs might no longer be the library's), and the C ABI is whole."""
     _compile(PEAKS_LIB_PATH, [PEAKS_SRC], verbose)
-    _compile_torch(TORCH_LIB_PATH, verbose)
-    return _compile(LIB_PATH, SRCS, verbose)
+    _compile(LIB_PATH, SRCS, verbose)
+    try:
+        _compile_torch(TORCH_LIB_PATH, verbose)
+    except (ImportError, FileNotFoundError) as e:
+        if os.path.exists(TORCH_LIB_PATH):
+            os.remove(TORCH_LIB_PATH)
+        warnings.warn(f"the torch marshalling module was not built ({e}); the C ABI and the scan's binding do not need it",
+                      RuntimeWarning, stacklevel=2)
+    return LIB_PATH
 
 
 if __name__ == "__main__":
