@@ -23,7 +23,7 @@ _BLOCK = ("causal_conv_bwd", "causal_conv_fwd", "causal_conv_step", "layer_norm_
 
 
 def __getattr__(name):
-    # these import torch with their module, so they load on first use: the
+    # their module loads on first use, and torch with their first call: the
     # package's import stays light
     if name in _BLOCK:
         from . import _block

@@ -10,13 +10,12 @@ from __future__ import annotations
 
 import ctypes
 
-import torch
-
 from . import _binding as _b
 
 
 def _load():
     """The marshalling module, with the HIP library's entry points bound to it."""
+    import torch  # noqa: F401  the module links its libraries
     lib = _b.lib()
     try:
         from . import _ssm_torch
@@ -46,6 +45,7 @@ _native = _Unloaded()
 def _on(stream, x):
     """The context of a call on ``stream``: its kernels and the memory it allocates, which the caching allocator then
     orders with them."""
+    import torch
     if not torch.is_tensor(x) or x.device.type != "cuda":
         raise ValueError("tensors must be on a GPU device")
     stream = _b._stream_for(stream, x.device)

@@ -344,3 +344,14 @@ def test_missing_library_fails_loudly(monkeypatch, tmp_path):
                   lambda: B.ssm_scan_create(0)):
         with pytest.raises(ImportError):
             call_()
+
+
+def test_package_and_its_names_import_without_torch():
+    """The raw calls need no torch: neither the package's import nor that of all its names loads it."""
+    import subprocess
+    import sys
+    code = ("import sys; sys.modules['torch'] = None\n"
+            "from selective_state_space_scan_amd import *\n"
+            "assert callable(ssm_selective_scan_fwd) and callable(causal_conv_fwd)\n")
+    r = subprocess.run([sys.executable, "-c", code], cwd=REPO, capture_output=True, text=True, timeout=120)
+    assert r.returncode == 0, r.stderr
