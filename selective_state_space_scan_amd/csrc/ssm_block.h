@@ -183,15 +183,15 @@ struct RawVec<uint16_t, 1> {
   __device__ __forceinline__ void unpack(float (&o)[1]) const { o[0] = VecIO<uint16_t>::lo(v); }
 };
 
-// The first n (0 <= n <= V) of V elements; the others read as zero and are not
+// The first n (0 <= n <= V) of V elements; the others read as `rest` and are not
 // written.
 template <typename IO, int V>
-__device__ __forceinline__ void load_n(const IO* p, int n, float (&o)[V]) {
+__device__ __forceinline__ void load_n(const IO* p, int n, float (&o)[V], float rest = 0.0f) {
   if (n == V) {
     VecIO<IO>::load(p, o);
   } else {
 #pragma unroll
-    for (int i = 0; i < V; ++i) o[i] = i < n ? VecIO<IO>::get(p + i) : 0.0f;
+    for (int i = 0; i < V; ++i) o[i] = i < n ? VecIO<IO>::get(p + i) : rest;
   }
 }
 template <typename IO, int V>

@@ -194,15 +194,17 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void norm_bwd_kernel(const N
     for (int k = 0; k < NV; ++k) {
       const int d = (k * TPR + lane) * V;
       const int m = valid ? n[k] : 0;
-      load_n<RT, V>(static_cast<const RT*>(prm.v) + at + d, m, xh[k]);
+      // past the row's end v = mean, so that h there is 0: from 0 it would be
+      // -mean * rstd, which may leave fp32's range, and g h is then no number
+      load_n<RT, V>(static_cast<const RT*>(prm.v) + at + d, m, xh[k], mean);
       load_n<IO, V>(static_cast<const IO*>(prm.dy) + at + d, m, g[k]);
     }
 #pragma unroll
     for (int k = 0; k < NV; ++k)
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        // an element past the row's end has g = 0, and a row that is not
-        // valid has rstd = 0 on zeros: both add nothing
+        // an element past the row's end has g = 0 and h = 0, and a row that is
+        // not valid has rstd = 0 on zeros: both add nothing
         const float h = (xh[k][i] - mean) * rstd;
         xh[k][i] = h;
         dw[k][i] = __builtin_fmaf(g[k][i], h, dw[k][i]);

@@ -588,6 +588,24 @@ def test_norm_bad_rows_stay_alone():
         assert all(np.array_equal(bits(p), bits(q)) for p, q in zip(outs, want))
 
 
+@pytest.mark.parametrize("io,rio", [("f32", "f32"), ("bf16", "f32"), ("bf16", "bf16")])
+@pytest.mark.parametrize("D", [7, 200, 1001, 2050, 9001])
+def test_norm_bwd_of_large_means(D, io, rio):
+    """Rows that are constant and so large that mean * rstd leaves fp32's range: v - mean is 0 in every element, and
+    the places past a row's end that widths leave in the last lanes have no say."""
+    import torch
+    import selective_state_space_scan_amd as ssm
+    g = Gen(37, io)
+    v = torch.tensor([3e36, -1e37, 2.5], device=DEV).to(_dt(rio))[:, None].expand(3, D).contiguous()
+    mean, rstd = v[:, 0].float().contiguous(), torch.full((3,), 1e-5 ** -0.5, device=DEV)
+    dy, w, dr = g.normal(3, D), g.normal(D, io="f32"), g.normal(3, D, io=rio)
+    out = ssm.layer_norm_bwd(dy, v, w, mean, rstd, dresidual_out=dr)
+    sync()
+    ref, tol = R.norm_bwd(n64(dy), n64(v), n64(w), n64(mean), n64(rstd), n64(dr), io, rio)
+    for k in ("dx", "dresidual", "dweight", "dbias"):
+        R.check(k, n64(out[k]), ref[k], tol[k])
+
+
 def test_norm_empty():
     import torch
     import selective_state_space_scan_amd as ssm
