@@ -223,7 +223,9 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void norm_bwd_kernel(const N
         if (prm.dresidual_out != nullptr)
           load_n<RT, V>(static_cast<const RT*>(prm.dresidual_out) + at + d, valid ? n[k] : 0, o);
 #pragma unroll
-        for (int i = 0; i < V; ++i) o[i] = __builtin_fmaf(g[k][i] - off - xh[k][i] * along, rstd, o[i]);
+        for (int i = 0; i < V; ++i)
+          // a padded row is +0 whatever the weight (its g is 0 w: NaN for an infinite one)
+          o[i] = valid ? __builtin_fmaf(g[k][i] - off - xh[k][i] * along, rstd, o[i]) : 0.0f;
         store_n<IO, V>(static_cast<IO*>(prm.dx) + at + d, n[k], o);
         if (prm.dresidual != nullptr) store_n<RT, V>(static_cast<RT*>(prm.dresidual) + at + d, n[k], o);
       }

@@ -606,6 +606,25 @@ def test_norm_bwd_of_large_means(D, io, rio):
         R.check(k, n64(out[k]), ref[k], tol[k])
 
 
+@pytest.mark.parametrize("io,rio", [("f32", "f32"), ("bf16", "f32"), ("bf16", "bf16")])
+@pytest.mark.parametrize("D", [40, 1030])
+def test_norm_padding_with_infinite_weights(D, io, rio):
+    """Rows past the valid length give +0 in every output, an infinity or NaN in weight or bias notwithstanding."""
+    import selective_state_space_scan_amd as ssm
+    g = Gen(38, io)
+    B, L = 3, 5
+    lens = [2, 0, 4]
+    x, res, w, b = g.normal(B, L, D), g.normal(B, L, D, io=rio), g.normal(D, io="f32"), g.normal(D, io="f32")
+    w[3], w[-1], b[5] = float("inf"), float("nan"), float("-inf")
+    y, v, mean, rstd = ssm.layer_norm_fwd(x, w, b, i32(lens), residual=res, return_stats=True)
+    out = ssm.layer_norm_bwd(x, v, w, mean, rstd, i32(lens), dresidual_out=res)
+    sync()
+    for t in (y, v, mean, rstd, out["dx"], out["dresidual"]):
+        for i, n in enumerate(lens):
+            assert not bits(t)[i, n:].any()
+    assert np.isfinite(n64(out["dweight"])).all() and np.isfinite(n64(out["dbias"])).all()
+
+
 def test_norm_empty():
     import torch
     import selective_state_space_scan_amd as ssm
