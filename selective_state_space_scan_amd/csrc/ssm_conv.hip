@@ -355,7 +355,7 @@ __global__ __launch_bounds__(256) void conv_bwd_kernel(const ConvBwdParams prm) 
             }
             if (o < 0) {
               if (d0 != nullptr) VecIO<IO>::store(d0 + (o + H) * prm.nd, v);
-            } else if (o < prm.L) {
+            } else if (o < len) {
               VecIO<IO>::store(op + (j - H) * prm.dx_ts, v);
             }
           } else {
@@ -370,12 +370,12 @@ __global__ __launch_bounds__(256) void conv_bwd_kernel(const ConvBwdParams prm) 
       const int64_t c0 = ((static_cast<int64_t>(group) * prm.M + m) * ty + sub) * T;
       if (c0 > 0 && c0 + T + H <= len) {
         chunk.template operator()<false>(c0);
-      } else if (c0 == 0 || c0 < len) {
-        chunk.template operator()<true>(c0);
       } else {
+        if (c0 == 0 || c0 < len) chunk.template operator()<true>(c0);
+        // +0 past the row's end (a sum of taps times g = 0 would be NaN for an infinite one)
         const float zero[V] = {};
         const int64_t c1 = c0 + T < prm.L ? c0 + T : prm.L;
-        for (int64_t t = c0; t < c1; ++t) VecIO<IO>::store(dx + t * prm.dx_ts, zero);
+        for (int64_t t = c0 < len ? len : c0; t < c1; ++t) VecIO<IO>::store(dx + t * prm.dx_ts, zero);
       }
     }
   }

@@ -187,6 +187,30 @@ def test_conv_padding_reaches_nothing(io):
             assert np.array_equal(a, b)
 
 
+@pytest.mark.parametrize("silu", [True, False])
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+def test_conv_padding_with_infinite_weights(io, silu):
+    """Steps past a row's end give +0, an infinity or NaN in taps or bias notwithstanding, in every chunk that a row's
+    end may fall into."""
+    import selective_state_space_scan_amd as ssm
+    B, L, D, W = 6, 75, 40, 4
+    lens = [75, 40, 13, 38, 1, 0]
+    c = conv_inputs(io, B, L, D, W, 20)
+    c["w"][3, 0], c["w"][7, 3], c["b"][9] = float("inf"), float("nan"), float("-inf")
+    y, last = ssm.causal_conv_fwd(c["x"], c["w"], c["b"], i32(lens), silu=silu, conv0=c["c0"])
+    g = ssm.causal_conv_bwd(c["x"], c["w"], c["b"], i32(lens), c["dy"], silu=silu, conv0=c["c0"], dconv_last=c["dl"])
+    sync()
+    for t in (y, g["dx"]):
+        for b, n in enumerate(lens):
+            assert not bits(t)[b, n:].any()
+    # the other channels are those of finite weights
+    ok = [d for d in range(D) if d not in (3, 7, 9)]
+    f = conv_inputs(io, B, L, D, W, 20)
+    r = ssm.causal_conv_bwd(f["x"], f["w"], f["b"], i32(lens), f["dy"], silu=silu, conv0=f["c0"], dconv_last=f["dl"])
+    assert np.array_equal(bits(g["dx"])[..., ok], bits(r["dx"])[..., ok])
+    assert np.array_equal(bits(g["dweight"])[ok], bits(r["dweight"])[ok])
+
+
 def test_conv_infinite_and_nan_inputs_follow_the_formula():
     """Inside a row they spread over the W steps that see them and no further."""
     import torch
