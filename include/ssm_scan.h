@@ -475,7 +475,8 @@ int ssm_causal_conv_step(ssm_scan_t handle, const ssm_conv_dims* dims, const ssm
  *  weight, bias [dim] fp32; bias may be NULL.
  *  valid_len    [batch] int32 or NULL: rows past it give +0 in every output,
  *               and their inputs are not read.
- *  mean, rstd   [batch, seqlen] fp32 or NULL: m and r, for the backward.
+ *  mean, rstd   [batch, seqlen] fp32 or NULL: m and r, for the backward (of a
+ *               row of no elements, dim 0: 0 and 1 / sqrt(eps)).
  *
  * dim is at most 16384, eps positive.  Conventions as above. */
 typedef struct ssm_norm_dims {

@@ -371,9 +371,10 @@ int ssm_layer_norm_fwd(ssm_scan_t handle, const ssm_norm_dims* dims, const ssm_n
   if (io == nullptr) return SSM_ERR_INVALID_ARG;
   const int64_t rows = dims->batch * dims->seqlen, nd = dims->dim;
   const int64_t e = dims->io_dtype == SSM_IO_BF16 ? 2 : 4, r = dims->residual_dtype == SSM_IO_BF16 ? 2 : 4;
-  const bool empty = rows == 0 || nd == 0;
+  // rows of no elements still have statistics
+  const bool empty = rows == 0 || (nd == 0 && io->mean == nullptr && io->rstd == nullptr);
   if (!empty) {
-    if (io->x == nullptr || io->weight == nullptr || io->y == nullptr) return SSM_ERR_INVALID_ARG;
+    if (nd > 0 && (io->x == nullptr || io->weight == nullptr || io->y == nullptr)) return SSM_ERR_INVALID_ARG;
     if (!aligned(io->x, e) || !aligned(io->y, e) || !aligned(io->residual, r) || !aligned(io->residual_out, r) ||
         !aligned(io->weight, 4) || !aligned(io->bias, 4) || !aligned(io->valid_len, 4) || !aligned(io->mean, 4) ||
         !aligned(io->rstd, 4))
@@ -393,7 +394,7 @@ int ssm_layer_norm_fwd(ssm_scan_t handle, const ssm_norm_dims* dims, const ssm_n
   p.x = io->x, p.residual = io->residual, p.w = io->weight, p.bias = io->bias, p.valid_len = io->valid_len;
   p.y = io->y, p.residual_out = io->residual_out, p.mean = io->mean, p.rstd = io->rstd;
   p.rows = rows, p.L = dims->seqlen, p.nd = static_cast<int32_t>(nd), p.rms = dims->rms;
-  p.eps = dims->eps, p.inv_n = 1.0f / static_cast<float>(nd);
+  p.eps = dims->eps, p.inv_n = nd > 0 ? 1.0f / static_cast<float>(nd) : 0.0f;
   bool fits = true;
   for_norm_fwd(dims, io->residual != nullptr, [&]<typename IO, typename RT, int TPR, int NV>() {
     constexpr int BLOCK = block_of<TPR>, RPB = BLOCK / TPR;

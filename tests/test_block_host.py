@@ -315,6 +315,14 @@ def test_empty_batches_need_only_the_handle():
     assert norm_fwd(norm_dims(batch=0), **none) == INVALID
 
 
+def test_norm_rows_of_no_elements():
+    """dim 0 needs no rows and no weight; misaligned statistics are looked at all the same, so they are not skipped."""
+    none = {k: None for k in OPTIONAL["norm_fwd"] + REQUIRED["norm_fwd"]}
+    assert norm_fwd(norm_dims(dim=0), **none) == INVALID   # the handle
+    assert norm_fwd(norm_dims(dim=0), **{**none, "rstd": 9 * MB + 2}) == UNSUPPORTED
+    assert norm_fwd(norm_dims(dim=0), **{**none, "mean": 9 * MB, "rstd": 9 * MB}) == ALIAS
+
+
 def test_binding_rejects_cpu_tensors():
     import torch
     x = torch.zeros(2, 16)

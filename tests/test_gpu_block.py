@@ -663,6 +663,20 @@ def test_norm_empty():
     assert y.shape == (4, 0)
 
 
+def test_norm_statistics_of_no_elements():
+    """Rows of no elements: mean 0 and rstd 1 / sqrt(eps), padded rows 0, all written."""
+    import torch
+    import selective_state_space_scan_amd as ssm
+    keep = [torch.full((3, 4), 7.0, device=DEV) for _ in range(2)]
+    del keep   # what the allocator hands out next holds something
+    x, w = torch.empty((3, 4, 0), device=DEV), torch.empty(0, device=DEV)
+    y, _, mean, rstd = ssm.layer_norm_fwd(x, w, None, i32([4, 0, 2]), eps=0.25, return_stats=True)
+    assert y.shape == (3, 4, 0) and not mean.any()
+    assert rstd.tolist() == [[2.0] * 4, [0.0] * 4, [2.0] * 2 + [0.0] * 2]
+    _, _, none, rstd = ssm.layer_norm_fwd(x, w, None, i32([4, 0, 2]), eps=0.25, rms=True, return_stats=True)
+    assert none is None and rstd.tolist() == [[2.0] * 4, [0.0] * 4, [2.0] * 2 + [0.0] * 2]
+
+
 def test_norm_starts_a_residual_stream():
     """residual_out without residual: x itself, in the stream's own type."""
     import torch
