@@ -7,7 +7,8 @@
 // Host code only.  The entry points of the HIP library come in as addresses
 // (bind), so this module loads no library by itself, and a missing library is
 // reported where it always was.  Errors are Python exceptions: TypeError and
-// ValueError for what a tensor is, the package's own error for a status code.
+// ValueError for what a tensor is, the package's own error for a status code,
+// torch's own for what torch reports.
 
 #include <Python.h>
 
@@ -16,9 +17,11 @@
 #include <c10/core/DeviceGuard.h>
 #include <c10/hip/HIPFunctions.h>
 #include <c10/hip/HIPStream.h>
+#include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <array>
+#include <exception>
 #include <sstream>
 #include <stdexcept>
 #include <string>
@@ -217,12 +220,8 @@ PyObject* guarded(Py_ssize_t got, Py_ssize_t want, const F& body) {
     PyErr_SetString(PyExc_TypeError, e.what());
   } catch (const ValueRefused& e) {
     PyErr_SetString(PyExc_ValueError, e.what());
-  } catch (python_error& e) {  // raised by Python code under torch
-    e.restore();
-  } catch (const std::bad_alloc&) {
-    PyErr_NoMemory();
-  } catch (const std::exception& e) {
-    PyErr_SetString(PyExc_RuntimeError, e.what());
+  } catch (...) {  // torch's own, as torch reports them (an allocation that fails is its OutOfMemoryError)
+    torch::translate_exception_to_python(std::current_exception());
   }
   return nullptr;
 }

@@ -955,6 +955,19 @@ def test_most_rows():
     assert torch.equal(g["dx"][-40:], gp["dx"])
 
 
+def test_outputs_that_do_not_fit_are_torch_s_out_of_memory():
+    """As where torch allocates itself (and in the scan's calls): one exception type to catch, and the next call runs."""
+    import torch
+    import selective_state_space_scan_amd as ssm
+    x, w = torch.ones((1, 1, 1024), dtype=torch.bfloat16, device=DEV), torch.ones((1024, 4), device=DEV)
+    big = x.expand(1 << 10, 1 << 20, 1024)   # 2 TiB of output
+    for f in (lambda: ssm.causal_conv_fwd(big, w), lambda: ssm.causal_conv_bwd(big, w, None, None, big)):
+        with pytest.raises(torch.OutOfMemoryError):
+            f()
+    y, _ = ssm.causal_conv_fwd(x, w, silu=False)
+    assert (y == 1).all()
+
+
 def test_refusals():
     import torch
     import selective_state_space_scan_amd as ssm
