@@ -5,6 +5,11 @@ As for the scan, every step runs in the HIP library.  Shapes, dtypes and
 devices are checked, outputs and scratch allocated and the C ABI called by the
 CPython module ``_ssm_torch`` (``csrc/ssm_torch.cpp``): done here, that took up
 to 8 us of a single-token call whose launch takes 4.  There is no fallback.
+
+Like the scan's, these calls record no autograd graph: inputs that require
+gradients give outputs that do not, and the ``_bwd`` calls are what a custom
+``torch.autograd.Function`` is made of.  Tensors of the caller's that a call
+writes (caches in place, given outputs) count as modified in place.
 """
 from __future__ import annotations
 

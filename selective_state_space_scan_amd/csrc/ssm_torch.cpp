@@ -184,6 +184,13 @@ void call(const char* name, F fn, const at::Device& dev, const D& dims, const I&
   throw Raised();
 }
 
+// The caller's own tensors that a call wrote, for torch's version counters: an
+// autograd graph that saved one for its backward refuses to run, as after any
+// operation in place.  (Inference tensors have no counter.)
+void written(PyObject* o, const Tensor& t) {
+  if (o != Py_None && t.defined() && !t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+}
+
 PyObject* wrap(const Tensor& t) {
   if (!t.defined()) Py_RETURN_NONE;
   PyObject* o = THPVariable_Wrap(t);
@@ -297,6 +304,7 @@ PyObject* scan_step(PyObject*, PyObject* const* a, Py_ssize_t n) {
     s.x_row_stride = x.stride(0), s.delta_row_stride = delta.stride(0), s.B_row_stride = B.stride(0);
     s.C_row_stride = C.stride(0), s.y_row_stride = y.stride(0), s.n_slots = c.rows;
     call("ssm_selective_scan_step", entry.scan_step, dev, dims, s);
+    written(a[6], c.to), written(a[13], y);
     return wrap(y);
   });
 }
@@ -323,6 +331,7 @@ PyObject* conv_step(PyObject*, PyObject* const* a, Py_ssize_t n) {
     s.conv0 = c.from.data_ptr(), s.conv_last = c.to.data_ptr(), s.y = y.data_ptr();
     s.x_row_stride = x.stride(0), s.y_row_stride = y.stride(0), s.n_slots = c.rows;
     call("ssm_causal_conv_step", entry.conv_step, dev, dims, s);
+    written(a[1], c.to), written(a[7], y);
     return wrap(y);
   });
 }
@@ -371,6 +380,7 @@ PyObject* conv_fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
     s.x_batch_stride = c.x.stride(0), s.x_time_stride = c.x.stride(1);
     s.y_batch_stride = y.stride(0), s.y_time_stride = y.stride(1);
     call("ssm_causal_conv_fwd", entry.conv_fwd, c.dev, c.dims, s);
+    written(a[6], y), written(a[7], last);
     return pack<2>({y, last});
   });
 }
@@ -398,6 +408,7 @@ PyObject* conv_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
     s.dy_batch_stride = dy.stride(0), s.dy_time_stride = dy.stride(1);
     s.dx_batch_stride = dx.stride(0), s.dx_time_stride = dx.stride(1);
     call("ssm_causal_conv_bwd", entry.conv_bwd, c.dev, c.dims, s);
+    written(a[8], dx);
     return pack<4>({dx, dw, db, d0});
   });
 }
@@ -465,6 +476,7 @@ PyObject* norm_fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
     s.x = x.const_data_ptr(), s.weight = m.w, s.valid_len = m.valid_len, s.y = y.data_ptr();
     s.residual_out = at_ptr<void>(out), s.mean = at_ptr<float>(mean), s.rstd = at_ptr<float>(rstd);
     call("ssm_layer_norm_fwd", entry.norm_fwd, m.dev, m.dims, s);
+    written(a[7], y), written(a[8], out);
     return stats ? pack<4>({y, out, mean, rstd}) : pack<2>({y, out});
   });
 }

@@ -968,6 +968,44 @@ def test_outputs_that_do_not_fit_are_torch_s_out_of_memory():
     assert (y == 1).all()
 
 
+def test_written_tensors_count_as_modified():
+    """torch's version counters see what a call writes, so a graph that saved such a tensor refuses its backward;
+    inputs, and tensors without a counter, are left alone."""
+    import torch
+    import selective_state_space_scan_amd as ssm
+    g = Gen(65, "f32")
+    B, L, D, N, W = 2, 9, 16, 16, 4
+    x, x3, bm = g.normal(B, D), g.normal(B, L, D), g.normal(B, N)
+    A, w, nw = g.normal(D, N), g.normal(D, W), g.normal(D)
+    h, h2, c, c2 = g.normal(B, D, N), g.normal(B, D, N), g.normal(B, W - 1, D), g.normal(B, W - 1, D)
+    y, y3, y4, c3, r = (torch.zeros_like(t) for t in (x, x3, x3, c, x3))
+    ins = [x, x3, bm, A, w, nw]
+
+    def bumped(f, *outs, kept=()):
+        old, still = [t._version for t in outs], [t._version for t in (*ins, *kept)]
+        f()
+        assert all(t._version > v for t, v in zip(outs, old))
+        assert [t._version for t in (*ins, *kept)] == still
+
+    bumped(lambda: ssm.selective_scan_step(x, x, A, bm, bm, None, h, y=y), h, y)
+    bumped(lambda: ssm.selective_scan_step(x, x, A, bm, bm, None, h, h_last=h2), h2, kept=(h,))
+    bumped(lambda: ssm.causal_conv_step(x, c, w, y=y), c, y)
+    bumped(lambda: ssm.causal_conv_step(x, c, w, conv_last=c2), c2, kept=(c,))
+    bumped(lambda: ssm.causal_conv_fwd(x3, w, y=y3, conv_last=c3), y3, c3)
+    bumped(lambda: ssm.causal_conv_bwd(x3, w, None, None, y3, dx=y4), y4, kept=(y3,))
+    bumped(lambda: ssm.layer_norm_fwd(x3, nw, y=y3, residual=r, residual_out=r), y3, r)
+    bumped(lambda: ssm.layer_norm_fwd(x3, nw, residual=r), kept=(r,))
+    p = torch.ones_like(h, requires_grad=True)
+    loss = (p * h).sum()   # saves h
+    ssm.selective_scan_step(x, x, A, bm, bm, None, h)
+    with pytest.raises(RuntimeError, match="inplace"):
+        loss.backward()
+    with torch.inference_mode():
+        hi = torch.zeros_like(h)
+        ssm.selective_scan_step(x, x, A, bm, bm, None, hi)
+    assert ssm.selective_scan_step(x, x, A, bm, bm, None, hi).shape == (B, D)
+
+
 def test_refusals():
     import torch
     import selective_state_space_scan_amd as ssm
