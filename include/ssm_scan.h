@@ -89,7 +89,7 @@ typedef struct ssm_scan_dims {
   int64_t dstate;         /* N states per channel: 16, 32 or 64 */
   int32_t io_dtype;       /* enum ssm_io_dtype for x, delta, B, C and y */
   int32_t delta_softplus; /* 1: delta = softplus(delta_raw); 0: delta is used as given */
-  int32_t delta_clamp;    /* 1: delta = min(max(delta, delta_min), delta_max) after softplus */
+  int32_t delta_clamp;    /* 1: delta = min(max(delta, delta_min), delta_max) after softplus; NaN gives delta_min */
   float delta_min;        /* used when delta_clamp = 1; must satisfy 0 <= delta_min <= delta_max */
   float delta_max;
 } ssm_scan_dims;
@@ -305,7 +305,8 @@ int ssm_selective_scan_bwd(ssm_scan_t handle, const void* x, const void* delta, 
  *
  *     h' = exp(delta * A) h + delta * B x,   y = (C . h' + D x) (* silu(z))
  *
- * dims is the forward's, with seqlen = 1; dim may be any number here.
+ * dims is the forward's, with seqlen = 1; dim may be any number here.  As in
+ * the forward, the clip takes a NaN delta to delta_min.
  *
  *  x, delta, z, y  [batch, dim] io dtype, rows x_row_stride (...) elements
  *               apart, dim fastest; z may be NULL (no gate).

@@ -69,7 +69,8 @@ def selective_scan_step(x, delta, A_log, B, C, D, h, *, slots=None, h_last=None,
     (torch.float32 or torch.bfloat16), rows anywhere (any row stride, last
     dimension dense).  A_log [dim, dstate], D [dim] or None and delta_bias
     [dim] or None: float32.  z like x or None: output gate y * silu(z).
-    delta_softplus and delta_clamp as in ``selective_scan_fwd``.
+    delta_softplus and delta_clamp as in ``selective_scan_fwd`` (the clip
+    takes a NaN to its lower bound, as there).
 
     h: the states, float32, [batch, dim, dstate], or with ``slots`` a cache
     [n_slots, dim, dstate] of which batch row b uses row slots[b] (int32).  A

@@ -412,6 +412,30 @@ def test_scan_step(io, B, D, N, slots, gate, skip, bias, clamp, softplus):
     assert torch.equal(y, y2) and torch.equal(inplace[at], new[at]) and torch.equal(inplace[rest], h[rest])
 
 
+@pytest.mark.parametrize("softplus", [True, False])
+def test_clip_of_a_delta_that_is_not_finite(softplus):
+    """The step's clip is the scan's: NaN becomes the lower bound, infinities the bounds; without a clip NaN spreads."""
+    import torch
+    import selective_state_space_scan_amd as ssm
+    B, D, N = 3, 32, 16
+    lo, hi = 0.125, 0.5
+    g = Gen(25, "f32")
+    x, bm, cm, A, h = g.normal(B, D), g.normal(B, N), g.normal(B, N), g.normal(D, N), g.normal(B, D, N)
+    bad = torch.tensor([float("nan"), float("inf"), -float("inf")], device=DEV)[:, None].expand(B, D).contiguous()
+    bound = torch.tensor([lo, hi, lo], device=DEV)[:, None].expand(B, D).contiguous()
+    want_h, got_h = h.clone(), h.clone()
+    want = ssm.selective_scan_step(x, bound, A, bm, cm, None, want_h, delta_softplus=False)
+    got = ssm.selective_scan_step(x, bad, A, bm, cm, None, got_h, delta_softplus=softplus, delta_clamp=(lo, hi))
+    assert torch.equal(got, want) and torch.equal(got_h, want_h)
+    seq = [t[:, None].contiguous() for t in (x, bad, bound, bm, cm)]
+    y0, h0 = ssm.selective_scan_fwd(seq[0], seq[2], A, seq[3], seq[4], h0=h, delta_softplus=False)
+    y1, h1 = ssm.selective_scan_fwd(seq[0], seq[1], A, seq[3], seq[4], h0=h, delta_softplus=softplus,
+                                    delta_clamp=(lo, hi))
+    assert torch.equal(y1, y0) and torch.equal(h1, h0)
+    y = ssm.selective_scan_step(x, bad, A, bm, cm, None, got_h, delta_softplus=softplus)
+    assert torch.isnan(y[0]).all() and torch.isnan(got_h[0]).all()
+
+
 def test_idle_rows_read_nothing():
     """What an idle row's inputs hold, NaN included, reaches no output; an empty cache leaves every row idle."""
     import torch
