@@ -559,6 +559,56 @@ def test_norm_bwd(io, rio, B, L, D, lens, rms):
         R.check("dresidual", flat(out["dresidual"]), ref["dresidual"], tol["dresidual"])
 
 
+NORM_TYPES = [("f32", None), ("f32", "f32"), ("bf16", None), ("bf16", "bf16"), ("bf16", "f32")]
+
+
+@pytest.mark.parametrize("rms", [False, True])
+@pytest.mark.parametrize("D", [300, 600, 1024, 1500, 3000, 6000, 12000])
+@pytest.mark.parametrize("io,rio", NORM_TYPES)
+def test_norm_every_row_width(io, rio, D, rms):
+    """64 to 1024 lanes a row, 8 and 16 elements a lane, each with rows past the valid length."""
+    test_norm_fwd(io, rio, 2, 5, D, [5, 3], rms)
+    test_norm_bwd(io, rio, 2, 5, D, [5, 3], rms)
+
+
+@pytest.mark.parametrize("rms", [False, True])
+@pytest.mark.parametrize("D,L", [(40, 4001), (700, 2001), (1500, 1001), (3000, 251), (6000, 251), (9000, 251)])
+@pytest.mark.parametrize("io,rio", NORM_TYPES)
+def test_norm_many_rows_of_every_width(io, rio, D, L, rms):
+    """Several rows a workgroup of the backward (at most 1280 of them, 256 where a row takes more than 256 lanes, of
+    256 lanes): sums over rows in registers and over a row in LDS, one row after the other, some past their valid
+    length.  The weight gradients' sums: at most 4 rows a lane, 4 lanes of a workgroup, 20 workgroups a lane of the
+    second pass, its 8 exchanges; the row's: 16 elements, 6 exchanges, 16 waves."""
+    import torch
+    import selective_state_space_scan_amd as ssm
+    g = Gen(39, io)
+    B, lens = 3, [L, L // 2, L - 1]
+    x, dy = g.normal(B, L, D, shift=0.5), g.normal(B, L, D)
+    w, b = g.normal(D, io="f32", scale=0.2, shift=1.0), g.normal(D, io="f32")
+    res = None if rio is None else g.normal(B, L, D, io=rio)
+    y, v, mean, rstd = ssm.layer_norm_fwd(x, w, b, i32(lens), residual=res, rms=rms, return_stats=True)
+    out = ssm.layer_norm_bwd(dy, x if v is None else v, w, mean, rstd, i32(lens), dresidual_out=res)
+    sync()
+    live = np.concatenate([np.arange(L) < n for n in lens])
+    flat = lambda t: None if t is None else n64(t).reshape(-1, D)[live]  # noqa: E731
+    per_row = lambda t: None if t is None else n64(t).ravel()[live]  # noqa: E731
+    (ry, rv, rm, rr), (ty, tv, tm, tr) = R.norm_fwd(flat(x), n64(w), n64(b), flat(res), 1e-5, rms, io, rio or io)
+    R.check("y", flat(y), ry, ty)
+    R.check("rstd", per_row(rstd), rr, tr)
+    if v is not None:
+        R.check("residual_out", flat(v), rv, tv)
+    ref, tol = R.norm_bwd(flat(dy), flat(x if v is None else v), n64(w), per_row(mean), per_row(rstd), flat(res), io,
+                          rio or io)
+    for k in ("dx", "dweight", "dbias"):
+        R.check(k, flat(out[k]) if k == "dx" else n64(out[k]), ref[k], tol[k])
+    if res is not None:
+        R.check("dresidual", flat(out["dresidual"]), ref["dresidual"], tol["dresidual"])
+    for t in (y, out["dx"]) + (() if v is None else (v, out["dresidual"])):
+        assert not bits(t).reshape(-1, D)[~live].any()
+    again = ssm.layer_norm_bwd(dy, x if v is None else v, w, mean, rstd, i32(lens), dresidual_out=res)
+    assert all(torch.equal(out[k], again[k]) for k in ("dx", "dweight", "dbias"))
+
+
 def test_norm_many_rows():
     """More rows than the backward has workgroups: the weights' sums over several rows a lane."""
     import selective_state_space_scan_amd as ssm
