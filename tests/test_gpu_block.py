@@ -138,6 +138,33 @@ def test_conv_large(io):
     assert all(np.array_equal(bits(g[k]), bits(again[k])) for k in g)   # run to run
 
 
+@pytest.mark.parametrize("silu", [True, False])
+@pytest.mark.parametrize("W", [2, 3, 4])
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+def test_conv_every_form(io, W, silu):
+    """Each number of taps with and without silu: the forward's long chunks and the backward's several runs a workgroup
+    at an odd width, rows of every kind of length (2 runs of 13 steps a lane, 4 lanes, 3 workgroups a lane of
+    the second pass and its exchanges, behind one another in a weight's sum), and one channel."""
+    import selective_state_space_scan_amd as ssm
+    B, L, D = 5, 3300, 1001
+    lens = [3300, 3287, 12, 0, 1777]
+    c = conv_inputs(io, B, L, D, W, 27, wide=True, bias=silu)
+    y, last = ssm.causal_conv_fwd(c["x"], c["w"], c["b"], i32(lens), silu=silu, conv0=c["c0"])
+    g = ssm.causal_conv_bwd(c["x"], c["w"], c["b"], i32(lens), c["dy"], silu=silu, conv0=c["c0"], dconv_last=c["dl"])
+    sync()
+    a = (n64(c["x"]), n64(c["w"]), n64(c["b"]), lens)
+    ry, rl, tol = R.conv_fwd(*a, n64(c["c0"]), silu, io)
+    R.check("y", n64(y), ry, tol)
+    assert np.array_equal(n64(last), rl)
+    ref, tol = R.conv_bwd(*a, n64(c["dy"]), n64(c["c0"]), n64(c["dl"]), silu, io)
+    for k in ("dx", "dweight", "dconv0") + (("dbias",) if silu else ()):
+        R.check(k, n64(g[k]), ref[k], tol[k])
+    for b, n in enumerate(lens):
+        assert not bits(y)[b, n:].any() and not bits(g["dx"])[b, n:].any()
+    test_conv_fwd(io, 2, 30, 1, W, [30, 11], True, False, silu)
+    test_conv_bwd(io, 2, 30, 1, W, [30, 11], True, False, silu)
+
+
 @pytest.mark.parametrize("io", ["f32", "bf16"])
 @pytest.mark.parametrize("lens", [[37, 20, 52], None])
 def test_conv_bwd_last_input_not_finite(io, lens):
@@ -434,6 +461,54 @@ def test_clip_of_a_delta_that_is_not_finite(softplus):
     assert torch.equal(y1, y0) and torch.equal(h1, h0)
     y = ssm.selective_scan_step(x, bad, A, bm, cm, None, got_h, delta_softplus=softplus)
     assert torch.isnan(y[0]).all() and torch.isnan(got_h[0]).all()
+
+
+@pytest.mark.parametrize("gate,skip,bias,clamp", [(True, True, True, (0.01, 0.5)), (False, False, True, None),
+                                                  (True, False, False, (0.05, 0.4))])
+@pytest.mark.parametrize("N", [16, 32, 64])
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+def test_scan_step_two_rows_a_workgroup(io, N, gate, skip, bias, clamp):
+    """257 rows of 16 workgroups each with slots take two rows a workgroup, the last alone: idle rows first and second
+    of a pair, slots repeated within a pair, in a later one and by the last row."""
+    import torch
+    import selective_state_space_scan_amd as ssm
+    B, D, n = 257, 15 * (1024 // N) + 7, 300
+    g = Gen(26, io)
+    h = g.normal(n, D, N, io="f32")
+    x, delta, z = g.normal(B, 2 * D)[:, D:], g.normal(B, D, scale=0.5), g.normal(B, D) if gate else None
+    bc = g.normal(B, 2 * N)
+    Bm, Cm, A_log = bc[:, :N], bc[:, N:], g.normal(D, N, io="f32", shift=1.0)
+    Dk, db = g.normal(D, io="f32") if skip else None, g.normal(D, io="f32") if bias else None
+    slots = torch.randperm(n, generator=g.g)[:B].tolist()
+    slots[2], slots[101], slots[150] = -1, n, -2**31
+    slots[5], slots[20], slots[77], slots[256] = slots[4], slots[7], slots[30], slots[0]
+    new = torch.full_like(h, 9.0)
+    kw = dict(slots=i32(slots), delta_clamp=clamp, delta_bias=db, z=z)
+    y = ssm.selective_scan_step(x, delta, A_log, Bm, Cm, Dk, h, h_last=new, **kw)
+    inplace = h.clone()
+    y2 = ssm.selective_scan_step(x, delta, A_log, Bm, Cm, Dk, inplace, **kw)
+    sync()
+    idle = [2, 101, 150, 5, 20, 77, 256]
+    rows = [b for b in range(B) if b not in idle]
+    at = [slots[b] for b in rows]
+    rest = [s for s in range(n) if s not in at]
+    clamp64 = None if clamp is None else tuple(float(np.float32(v)) for v in clamp)
+    ry, rh, ty, th = R.scan_step(n64(x)[rows], n64(delta)[rows], n64(A_log), n64(Bm)[rows], n64(Cm)[rows], n64(Dk),
+                                 n64(h)[at], n64(db), None if z is None else n64(z)[rows], True, clamp64, io)
+    R.check("h_last", n64(new)[at], rh, th)
+    R.check("y", n64(y)[rows], ry, ty)
+    assert not bits(y)[idle].any() and (n64(new)[rest] == 9).all()
+    assert torch.equal(y, y2) and torch.equal(inplace[at], new[at]) and torch.equal(inplace[rest], h[rest])
+
+
+@pytest.mark.parametrize("silu", [True, False])
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+def test_every_form_of_a_step(io, silu):
+    """The taps and state counts that the lists above leave out for a type."""
+    for W in (2, 3, 4):
+        test_conv_step(io, 3, 24, W, [1, -1, 4], silu)
+    for N in (16, 32, 64):
+        test_scan_step(io, 2, 24, N, None, silu, True, True, None, True)
 
 
 def test_idle_rows_read_nothing():
