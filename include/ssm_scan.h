@@ -435,7 +435,9 @@ typedef struct ssm_conv_bwd_io {
   int64_t dx_time_stride;
 } ssm_conv_bwd_io;
 
-/* Workspace bytes of ssm_causal_conv_bwd; -1 for NULL or invalid dims. */
+/* Workspace bytes of ssm_causal_conv_bwd; -1 for NULL or invalid dims.  A
+ * multiple of batch * (width + 1) * dim * 4: every row has sums of its own, so
+ * for many rows of a few steps the scratch passes x itself in size. */
 int64_t ssm_causal_conv_bwd_workspace_bytes(const ssm_conv_dims* dims);
 
 int ssm_causal_conv_bwd(ssm_scan_t handle, const ssm_conv_dims* dims, const ssm_conv_bwd_io* io, void* stream);

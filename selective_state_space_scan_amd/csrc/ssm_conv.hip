@@ -526,11 +526,13 @@ BwdTiling bwd_tiling(const ssm_conv_dims* dims) {
   t.n_tiles = (t.n_vec + cx - 1) / cx;
   const int64_t run = kBwdChunk * t.ty, runs = dims->seqlen > 0 ? (dims->seqlen + run - 1) / run : 1;
   // Fewer, longer workgroups leave fewer sums; at least kBwdBlocks of them
-  // fill the GPU (us, M = 1 or 2 / 4: bf16 8 x 4096 x 1024 50.0 / 47.8, fp32 8 x 2048
+  // fill the GPU.  A workgroup stays within one batch row, so there is one set
+  // of sums a row at least, however short the rows are, and M ends at a row's
+  // runs (GPU time with the second pass, us, M = 1 or 2 / 4: bf16 8 x 4096 x 1024 50.0 / 47.8, fp32 8 x 2048
   // x 1024 43.1 / 46.0).
   const __int128 all = static_cast<__int128>(dims->batch) * runs * t.n_tiles;
   t.M = 1;
-  while (t.M < 8 && all >= (t.M + 1) * kBwdBlocks) ++t.M;
+  while (t.M < 8 && t.M < runs && all >= (t.M + 1) * kBwdBlocks) ++t.M;
   t.n_groups = (runs + t.M - 1) / t.M;
   t.parts = dims->batch * t.n_groups;
   return t;

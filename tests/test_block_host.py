@@ -264,6 +264,14 @@ def test_workspaces():
     assert norm_bwd(workspace_bytes=-1, **ODD["norm_bwd"]) == INVALID
 
 
+@pytest.mark.parametrize("batch,seqlen,dim,width", [(4096, 8, 2048, 4), (65536, 2, 1024, 4), (3, 0, 24, 2),
+                                                    (512, 52, 1024, 3)])
+def test_conv_workspace_of_short_rows(batch, seqlen, dim, width):
+    """One set of sums a row where a row's steps are one workgroup's, as the header says."""
+    d = conv_dims(batch=batch, seqlen=seqlen, dim=dim, width=width)
+    assert ssm.lib().ssm_causal_conv_bwd_workspace_bytes(ctypes.byref(d)) == batch * (width + 1) * dim * 4
+
+
 def test_strides():
     bad = ODD["conv_fwd"]
     assert conv_fwd(x_time_stride=-24, **bad) == INVALID and conv_fwd(y_batch_stride=-1, **bad) == INVALID
