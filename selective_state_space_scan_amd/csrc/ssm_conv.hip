@@ -22,12 +22,15 @@
 // the sizes below, the backward fetching 16 % over its inputs (now 4 %).
 //
 // Measured (copy of 1 GiB: 5.3 TB/s): forward of 16 rows of up to 8192 steps x
-// 512 channels, bf16, lengths uniform: 29.6 us, 6.8 TB/s of what it has to move
-// (the inputs partly from the 256 MiB cache).  Backward of 8 x 4096 x 1024 bf16, W = 4, silu: 46 us and 4 for the
-// second pass, 4.0 TB/s: the vector units are busy two thirds of it (26
-// operations a step and channel, 16/13 of the g's), fp32 of half the elements
-// moves 4.6 TB/s.  2 x 256 x 64 fp32: 3.8 us forward; 3 x 1021 x 200: 9.0 us
-// backward.  One token of 256 rows x 2048: 4.2 us, of one row 2.8.
+// 512 channels, bf16, lengths uniform: 29.7 us, 6.8 TB/s of what it has to move
+// (the inputs partly from the 256 MiB cache).  Backward of 8 x 4096 x 1024 bf16,
+// W = 4, silu: 49.6 us, 4.1 TB/s (in a kernel trace 46.1 and 4.7 for the second
+// pass): the vector units are busy two thirds of it (26 operations a step and
+// channel, 16/13 of the g's), and 16 rows of lengths uniform up to 4096 take
+// 70.5; fp32 of half the elements moves 4.6 TB/s.  2 x 256 x 64 fp32: 3.8 us
+// forward; 3 x 1021 x 200: 8.8 us backward.  One token of 256 of 512 slots x
+// 2048: 4.1 us into another cache, 4.6 in place with eight caches in turn; of
+// one row 2.6.
 
 #include <hip/hip_runtime.h>
 
@@ -241,9 +244,9 @@ __global__ __launch_bounds__(256) void conv_fwd_kernel(const ConvParams prm) {
 // the same time.  The weights' sums join in LDS at the end; each workgroup
 // leaves W+1 rows of sums.
 //
-// 13 steps, us for 8 x 4096 x 1024 bf16 / 3 x 1021 x 200 fp32: 50.5 / 8.9; 9 steps
-// 51.9 / 8.2, 16 steps 51.9 / 9.5, 21 steps 56.7 / 12.2.  Two channels a lane:
-// with four, 56.4 (half the waves at 1.6 times the registers).
+// 13 steps, us for 8 x 4096 x 1024 bf16 / 16 ragged rows of them / 3 x 1021 x 200
+// fp32: 49.9 / 70.7 / 8.6; 9 steps 51.3 / 66.2 / 7.8, 16 steps 52.4 / 66.1 / 9.2, 21
+// steps 53.0 / 70.6 / 10.1.  Two channels a lane: with four, 71.8 / 87.6 / 9.6.
 constexpr int kBwdChunk = 13;
 constexpr int kBwdVec = 2;
 
@@ -330,7 +333,8 @@ __global__ __launch_bounds__(256) void conv_bwd_kernel(const ConvBwdParams prm) 
             for (int k = 0; k < W; ++k) {
               // past the row's end g = 0, but xs may still hold an infinity or NaN (a
               // select: with a branch around the sums the registers fall to four
-              // waves' and full rows take 55.2 us for 53.3, ragged ones 65 for 69)
+              // waves' and whole calls, CPU time included, of full rows take 55.2 us
+              // for 53.3, of ragged ones 65 for 69)
               const float in = EDGE && c0 + j >= len ? 0.0f : xs[k][i];
               dw[k][i] = __builtin_fmaf(g[H][i], in, dw[k][i]);
             }
@@ -500,9 +504,10 @@ int check_conv_dims(const ssm_conv_dims* dims) {
 }
 
 // Steps a lane of the forward walks: long chunks read fewer of the inputs in
-// front of them twice, short ones fill the GPU sooner and answer sooner.  bf16,
-// us at 4 / 12 steps: 2 x 1000 steps x 512 channels 4.0 / 5.5, 2 x 2000 x 1024
-// 7.0 / 8.0, 4 x 2000 x 1024 11.3 / 10.7, 8 x 4096 x 1024 35.7 / 26.9.
+// front of them twice, short ones fill the GPU sooner and answer sooner.  us at
+// 4 / 12 steps: fp32 2 x 256 steps x 64 channels 3.3 / 5.0, bf16 2 x 1000 x 512 3.7 /
+// 4.5, 2 x 2000 x 1024 6.4 / 6.4, 4 x 2000 x 1024 10.1 / 8.7, 8 x 4096 x 1024 30.7 /
+// 23.9.
 constexpr int kShortChunk = 4, kLongChunk = 12;
 constexpr int64_t kShortWork = 3 << 19;  // (step, lane) pairs
 
@@ -526,10 +531,11 @@ BwdTiling bwd_tiling(const ssm_conv_dims* dims) {
   t.n_tiles = (t.n_vec + cx - 1) / cx;
   const int64_t run = kBwdChunk * t.ty, runs = dims->seqlen > 0 ? (dims->seqlen + run - 1) / run : 1;
   // Fewer, longer workgroups leave fewer sums; at least kBwdBlocks of them
-  // fill the GPU.  A workgroup stays within one batch row, so there is one set
-  // of sums a row at least, however short the rows are, and M ends at a row's
-  // runs (GPU time with the second pass, us, M = 1 or 2 / 4: bf16 8 x 4096 x 1024 50.0 / 47.8, fp32 8 x 2048
-  // x 1024 43.1 / 46.0).
+  // fill the GPU.  us at M = 1 / 2 / 4 / 8: bf16 8 x 4096 x 1024 - / 51.6 / 49.9 /
+  // 55.6, fp32 8 x 2048 x 1024 44.4 / 44.3 / 46.7 / -, and against the rule bf16 16
+  // ragged rows of 4096 x 1024 - / - / 65.5 / 70.7.  A workgroup stays within one
+  // batch row, so there is one set of sums a row at least, however short the
+  // rows are, and M ends at a row's runs.
   const __int128 all = static_cast<__int128>(dims->batch) * runs * t.n_tiles;
   t.M = 1;
   while (t.M < 8 && t.M < runs && all >= (t.M + 1) * kBwdBlocks) ++t.M;

@@ -12,14 +12,21 @@
 //
 // About ten operations an element on 4 to 16 bytes: bound by memory.  A row is
 // held in registers between its one read and its one write: eight elements a
-// lane (16 beyond dim 8192), 64 to 1024 lanes a row (dim <= 16384).  The mean is subtracted before
+// lane (16 beyond dim 8192, and forward for rows of bf16 without a residual
+// stream), 64 to 1024 lanes a row (dim <= 16384).  The mean is subtracted before
 // squares are summed, and the small sum of the differences corrects both it and
 // the variance, so rows whose mean is far from zero lose nothing.
 //
 // Measured, 32768 rows x 1024 in bf16 with the residual stream in fp32 (a copy of
-// 1 GiB: 5.3 TB/s): forward 74.6 us, 5.4 TB/s; backward 96 us and 4 for the
-// second pass, 5.4 TB/s.  24 rows x 1000 fp32 forward 2.8 us, 1021 x 600 backward
-// 8.3 us (two dependent launches).
+// 1 GiB: 5.3 TB/s): forward 74.7 us, 5.4 TB/s; backward 100.1 us, 5.4 TB/s (in a
+// kernel trace 95.6 and 4.6 for the second pass).  24 rows x 1000 fp32 forward
+// 2.8 us, 1021 x 600 backward 8.4 us (two dependent launches).
+//
+// Further from the bytes: narrow rows, which leave most of a wave's lanes idle
+// (524288 x 64 bf16 forward, stream in bf16: 248 us, 1.1 TB/s); rows that end
+// within a lane's elements, moved one by one there (32768 x 1001 bf16 forward 27.8
+// us, x 1024 23.5); and the backward beyond dim 8192, whose 16 elements a lane
+// spill 36 to 92 bytes of scratch a lane (2048 x 12288 bf16 66.4 us, 3.0 TB/s).
 
 #include <hip/hip_runtime.h>
 
@@ -310,10 +317,10 @@ void for_row(int64_t nd, const F& f) {
 }
 
 // Eight elements a lane: more waves of fewer registers than with sixteen (us
-// forward / backward, 32768 x 1024 bf16 with an fp32 stream 74.6 / 100.2 against
-// 80.1 / 100.9; 16384 x 2048 fp32 96.6 against 101.6 forward; 24 x 1000 2.8 against
-// 3.3).  Rows of bf16 alone, 4 bytes an element, want the sixteen forward (24.3
-// against 27.5 us).
+// forward / backward, 32768 x 1024 bf16 with an fp32 stream 74.4 / 100.0 against
+// 79.8 / 102.2; 16384 x 2048 fp32 97.6 against 103.0 forward; 24 x 1000 3.1 against
+// 3.7).  Rows of bf16 alone, 4 bytes an element, want the sixteen forward (32768
+// x 1024: 23.5 against 26.5 us).
 constexpr int kShortElems = 8;
 
 template <typename F>
@@ -344,9 +351,9 @@ constexpr int block_of = TPR > 256 ? TPR : 256;
 // Workgroups of the backward, each walking several rows, all on the GPU at
 // once (256 CUs), so that none waits for another's end.  Three a CU keep the
 // memory busy where a row has fp32 in it, five where all is bf16 (us at 3 / 4 / 5:
-// 32768 x 1024 with an fp32 stream 100.2 / 102.6 / 105.3, in bf16 63.4 / 56.9 / 53.0;
-// 16384 x 1024 fp32 49.7 / 51.7 / 53.2); one where a row takes more than 256 lanes
-// (4096 x 8192, one / two: 101.7 / 106.2).
+// 32768 x 1024 with an fp32 stream 100.0 / 102.3 / 105.5, in bf16 62.1 / 55.0 / 50.8;
+// 16384 x 1024 fp32 51.5 / 50.7 / 51.4); one where a row takes more than 256 lanes
+// (4096 x 8192, one / two: 101.3 / 105.5).
 int64_t bwd_groups(const ssm_norm_dims* dims) {
   int64_t tpr = 64;
   while (tpr < 1024 && dims->dim > tpr * kShortElems) tpr *= 2;

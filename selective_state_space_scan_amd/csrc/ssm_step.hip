@@ -15,11 +15,11 @@
 // wave reads 1 KB of one cache row; a channel's dstate / 4 lanes are adjacent
 // and add their parts of C.h' by DPP within a row of 16 lanes.
 //
-// Measured: 256 rows x 2048 channels x 16 states in bf16, 69 MB: 15.4 us from 256
-// of 512 slots into another cache (4.5 TB/s; a copy of 1 GiB runs at 5.3); in
-// place, eight such caches in turn, 18.1 us a step and 16.7 without slots: a
-// row's slot has to be there before its states can be asked for.  One row:
-// 2.6 us, the latency of two dependent reads.
+// Measured: 256 rows x 2048 channels x 16 states in bf16, 71 MB: 15.2 us from 256
+// of 512 slots into another cache (4.7 TB/s; a copy of 1 GiB runs at 5.3, and the
+// states of three input sets stay in the 256 MiB cache in part); in place, eight
+// such caches in turn, 19.4 us a step (3.7 TB/s), and 19.5 without slots.  One
+// row: 2.6 us, the latency of two dependent reads.
 
 #include <hip/hip_runtime.h>
 
@@ -117,9 +117,9 @@ __global__ __launch_bounds__(256) void scan_step_kernel(const StepParams prm) {
 
 // Rows of a workgroup where there are slots and kSeveral workgroups of one row:
 // they share the look through the slots and its latency.  us at 1 / 2 / 4 rows,
-// 2048 channels, dstate 16: 64 rows 6.3 / 6.4 / 7.5, 128 rows 10.4 / 10.2 / 10.6,
-// 256 rows 18.0 / 17.5 / 18.6, 1024 rows x 1024 channels 44.7 / 39.8 / 42.5 (with
-// cached stores).
+// 2048 channels, dstate 16, in place with eight caches in turn: 128 rows 10.9 /
+// 10.1 / 10.5, 256 rows 21.6 / 19.5 / 21.7, 1024 rows x 1024 channels 45.5 / 40.4 /
+// 42.5; at 1 / 2, 64 rows into another cache 5.4 / 5.5 (in place 6.8 both).
 // Without slots one row is the faster (256 rows 15.3 / 15.9).
 constexpr int kStepRows = 2;
 constexpr int64_t kSeveral = 4096;
