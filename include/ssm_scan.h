@@ -2,7 +2,9 @@
  * ssm_scan.h -- C ABI of the MI355X (gfx950) fused selective scan: the
  * forward and its backward (ssm_selective_scan_bwd, further below), its form
  * for single tokens on a cache of states, and the operators beside it in the
- * block: the short causal convolution and the layer or RMS norm.
+ * block: the short causal convolution, the layer or RMS norm, the gated
+ * recurrence (the scan's sibling with one state a channel) and the group norm
+ * with an activation or a gate behind either.
  *
  * The operation (Mamba's selective state-space scan).  For every
  * batch row b, channel d and state n, with A = -exp(A_log[d,n]):
@@ -66,11 +68,13 @@ enum ssm_io_dtype { SSM_IO_F32 = 0, SSM_IO_BF16 = 1 };
 enum ssm_status {
   SSM_OK = 0,
   SSM_ERR_INVALID_ARG = -1,     /* NULL required pointer or handle, negative dim, bad flag or clip bounds */
-  SSM_ERR_UNSUPPORTED = -2,     /* dstate not 16/32/64, dim not a multiple of 16 (scan) or above its limit (norm),
+  SSM_ERR_UNSUPPORTED = -2,     /* dstate not 16/32/64, dim not a multiple of 16 (scan) or above its limit (norms),
                                    width not 2 to 4, misaligned pointer, wrong GPU, one batch row of x, delta, B
                                    or C spanning 2 GiB or more (scan), or a grid too large */
   SSM_ERR_ALIAS = -3,           /* an output overlaps an input or another output; strided tensors are compared
-                                   as the ranges from their first byte to their last */
+                                   as the ranges from their first byte to their last (gated recurrence and
+                                   group norm: columns of one buffer, whose strides are multiples of one
+                                   another and whose columns are apart, do not overlap) */
   SSM_ERR_HIP = -4,             /* a HIP runtime or launch error */
   SSM_ERR_NO_DEVICE = -5,       /* no usable GPU at the requested ordinal */
   SSM_ERR_DEVICE_MISMATCH = -6, /* the calling thread's current device is not the handle's device */
@@ -541,6 +545,250 @@ typedef struct ssm_norm_bwd_io {
 int64_t ssm_layer_norm_bwd_workspace_bytes(const ssm_norm_dims* dims);
 
 int ssm_layer_norm_bwd(ssm_scan_t handle, const ssm_norm_dims* dims, const ssm_norm_bwd_io* io, void* stream);
+
+/* ---- gated recurrence --------------------------------------------------
+ *
+ * The diagonal recurrence of a block whose decay and input are gated by the
+ * data, with one state per channel.  For every row b, channel d and step
+ * t < valid_len[b], with r = sigmoid(a_gate), i = sigmoid(x_gate):
+ *
+ *     a[t] = exp(-exp(A_log[d]) r[t]),   h[t] = a[t] h[t-1] + sqrt(1 - a[t]^2) i[t] x[t],   y[t] = h[t]
+ *
+ *  x, a_gate, x_gate, y [batch, seqlen, dim] io dtype, dim fastest, rows and
+ *               steps x_batch_stride and x_time_stride (...) elements apart
+ *               (both gates are often the halves of one projection's output).
+ *               Strides of inputs must not be negative; outputs must not
+ *               overlap themselves.
+ *  A_log        [dim] fp32.
+ *  valid_len    [batch] int32 or NULL, as for the scan: y is +0 past it,
+ *               nothing there is read and the state stays as it is.
+ *  h0, h_last   [batch, dim] fp32 or NULL: the state before the first step
+ *               (zeros when NULL) and after the last valid one.  They may be
+ *               one buffer (update in place); no other overlap.
+ *  chunk_states [batch, ceil(seqlen / chunk), dim] fp32 or NULL, chunk =
+ *               ssm_gated_recurrence_chunk_len(): the state after the last
+ *               step of every chunk (the last one may be shorter; past
+ *               valid_len the state no longer changes), for the backward.
+ *  workspace    at least ssm_gated_recurrence_fwd_workspace_bytes(dims) bytes
+ *               of device scratch (8-byte aligned), overwritten; nothing in it
+ *               need hold anything before the call.  NULL allowed where that
+ *               is 0.  Calls that may run at the same time must not share it.
+ *
+ * Sizes are below 2^31, dim below 2^29 (SSM_ERR_UNSUPPORTED).  The conventions
+ * are the scan's: host-side checks first, asynchronous, nothing allocated,
+ * bitwise reproducible, fp32 arithmetic rounded once to the io dtype. */
+typedef struct ssm_gated_dims {
+  int64_t batch;
+  int64_t seqlen;
+  int64_t dim;
+  int32_t io_dtype;
+} ssm_gated_dims;
+
+typedef struct ssm_gated_fwd_io {
+  const void* x;
+  const void* a_gate;
+  const void* x_gate;
+  const float* A_log;
+  const int32_t* valid_len;
+  const float* h0;
+  void* y;
+  float* h_last;
+  float* chunk_states;
+  void* workspace;
+  int64_t workspace_bytes;
+  int64_t x_batch_stride;
+  int64_t x_time_stride;
+  int64_t a_gate_batch_stride;
+  int64_t a_gate_time_stride;
+  int64_t x_gate_batch_stride;
+  int64_t x_gate_time_stride;
+  int64_t y_batch_stride;
+  int64_t y_time_stride;
+} ssm_gated_fwd_io;
+
+/* Steps between the states that the forward keeps for the backward: 64. */
+int64_t ssm_gated_recurrence_chunk_len(void);
+
+/* Workspace bytes of ssm_gated_recurrence_fwd; -1 for NULL or invalid dims. */
+int64_t ssm_gated_recurrence_fwd_workspace_bytes(const ssm_gated_dims* dims);
+
+int ssm_gated_recurrence_fwd(ssm_scan_t handle, const ssm_gated_dims* dims, const ssm_gated_fwd_io* io, void* stream);
+
+/* Gradients of the recurrence for the loss sum(dy * y) + sum(dh_last *
+ * h_last); gates and states are recomputed from the inputs and chunk_states.
+ *
+ *  x, a_gate, x_gate, A_log, valid_len, h0: the forward's, again.
+ *  dy           like y;  dx, da_gate, dx_gate like x and the gates, with
+ *               strides of their own; the gradients are +0 past valid_len.
+ *               da_gate and dx_gate are those of the gates before their
+ *               sigmoid.  Where s = exp(A_log) r underflows to 0 the decay's
+ *               gradient is its limit 0.
+ *  dh_last      [batch, dim] fp32 or NULL (zero).
+ *  chunk_states the forward's (only the first ceil(seqlen / chunk) - 1 of a
+ *               row are read; NULL allowed when seqlen <= chunk).
+ *  dA_log       [dim] fp32;  dh0 [batch, dim] fp32 or NULL.
+ *  workspace    at least ssm_gated_recurrence_bwd_workspace_bytes(dims) bytes
+ *               of device scratch (8-byte aligned), as for the forward. */
+typedef struct ssm_gated_bwd_io {
+  const void* x;
+  const void* a_gate;
+  const void* x_gate;
+  const float* A_log;
+  const int32_t* valid_len;
+  const float* h0;
+  const void* dy;
+  const float* dh_last;
+  const float* chunk_states;
+  void* dx;
+  void* da_gate;
+  void* dx_gate;
+  float* dA_log;
+  float* dh0;
+  void* workspace;
+  int64_t workspace_bytes;
+  int64_t x_batch_stride;
+  int64_t x_time_stride;
+  int64_t a_gate_batch_stride;
+  int64_t a_gate_time_stride;
+  int64_t x_gate_batch_stride;
+  int64_t x_gate_time_stride;
+  int64_t dy_batch_stride;
+  int64_t dy_time_stride;
+  int64_t dx_batch_stride;
+  int64_t dx_time_stride;
+  int64_t da_gate_batch_stride;
+  int64_t da_gate_time_stride;
+  int64_t dx_gate_batch_stride;
+  int64_t dx_gate_time_stride;
+} ssm_gated_bwd_io;
+
+/* Workspace bytes of ssm_gated_recurrence_bwd; -1 for NULL or invalid dims. */
+int64_t ssm_gated_recurrence_bwd_workspace_bytes(const ssm_gated_dims* dims);
+
+int ssm_gated_recurrence_bwd(ssm_scan_t handle, const ssm_gated_dims* dims, const ssm_gated_bwd_io* io, void* stream);
+
+/* The recurrence for single tokens, on a cache of states.  dims has seqlen =
+ * 1.  x, a_gate, x_gate, y [batch, dim] with row strides; h0 and h_last
+ * [n_slots, dim] fp32 (or [batch, dim] without slots), the same buffer for an
+ * update in place; slots, idle rows and the limit on batch as in
+ * ssm_selective_scan_step. */
+typedef struct ssm_gated_step_io {
+  const void* x;
+  const void* a_gate;
+  const void* x_gate;
+  const float* A_log;
+  const int32_t* slots;
+  const float* h0;
+  float* h_last;
+  void* y;
+  int64_t x_row_stride;
+  int64_t a_gate_row_stride;
+  int64_t x_gate_row_stride;
+  int64_t y_row_stride;
+  int64_t n_slots;
+} ssm_gated_step_io;
+
+int ssm_gated_recurrence_step(ssm_scan_t handle, const ssm_gated_dims* dims, const ssm_gated_step_io* io, void* stream);
+
+/* ---- group norm --------------------------------------------------------
+ *
+ * The norm behind a recurrence, with its activation or gate: every step's
+ * channels are normalised group by group (`groups` groups of n = dim / groups
+ * adjacent channels), each step by itself, so that no step sees a later one.
+ * With act(u) = u sigmoid(u) (silu 1) or u (silu 0), for every row (b, t) with
+ * t < valid_len[b] and every group:
+ *
+ *     v = x, or x act(z) with gate SSM_GATE_BEFORE
+ *     m = mean(v) (rms: 0),  r = 1 / sqrt(mean((v - m)^2) + eps),  p = (v - m) r weight + bias
+ *     y = act(p) without a gate, p act(z) with SSM_GATE_AFTER, p with SSM_GATE_BEFORE
+ *
+ *  x, z, y      [batch, seqlen, dim] io dtype, dim fastest, rows and steps
+ *               x_batch_stride and x_time_stride (...) elements apart; z is
+ *               given with a gate (required) and NULL without.
+ *  weight, bias [dim] fp32; bias may be NULL.
+ *  valid_len    [batch] int32 or NULL: rows past it give +0 in every output,
+ *               and their inputs are not read.
+ *  mean, rstd   [batch, seqlen, groups] fp32 or NULL: m and r, for the
+ *               backward.
+ *
+ * groups divides dim (SSM_ERR_INVALID_ARG); a group has at most 8192
+ * channels, batch * seqlen is below 2^31 and dim below 2^29
+ * (SSM_ERR_UNSUPPORTED); eps is positive.  Conventions as above. */
+enum ssm_gate { SSM_GATE_NONE = 0, SSM_GATE_AFTER = 1, SSM_GATE_BEFORE = 2 };
+
+typedef struct ssm_group_norm_dims {
+  int64_t batch;
+  int64_t seqlen;
+  int64_t dim;
+  int64_t groups;
+  int32_t io_dtype;
+  int32_t rms;  /* 1: no mean is subtracted */
+  int32_t silu; /* 1: act(u) = u * sigmoid(u); 0: act(u) = u */
+  int32_t gate; /* enum ssm_gate */
+  float eps;
+} ssm_group_norm_dims;
+
+typedef struct ssm_group_norm_fwd_io {
+  const void* x;
+  const void* z;
+  const float* weight;
+  const float* bias;
+  const int32_t* valid_len;
+  void* y;
+  float* mean;
+  float* rstd;
+  int64_t x_batch_stride;
+  int64_t x_time_stride;
+  int64_t z_batch_stride;
+  int64_t z_time_stride;
+  int64_t y_batch_stride;
+  int64_t y_time_stride;
+} ssm_group_norm_fwd_io;
+
+int ssm_group_norm_fwd(ssm_scan_t handle, const ssm_group_norm_dims* dims, const ssm_group_norm_fwd_io* io,
+                       void* stream);
+
+/* Gradients of the group norm for the loss sum(dy * y).
+ *
+ *  x, z, weight, bias, valid_len, dims: the forward's; mean (may be NULL for
+ *               rms) and rstd as it returned them.
+ *  dy           like y;  dx, dz like x and z with strides of their own (dz
+ *               with a gate, required, and NULL without): +0 past valid_len.
+ *  dweight      [dim] fp32;  dbias [dim] fp32 or NULL.
+ *  workspace    at least ssm_group_norm_bwd_workspace_bytes(dims) bytes of
+ *               device scratch (4-byte aligned), overwritten. */
+typedef struct ssm_group_norm_bwd_io {
+  const void* dy;
+  const void* x;
+  const void* z;
+  const float* weight;
+  const float* bias;
+  const float* mean;
+  const float* rstd;
+  const int32_t* valid_len;
+  void* dx;
+  void* dz;
+  float* dweight;
+  float* dbias;
+  void* workspace;
+  int64_t workspace_bytes;
+  int64_t dy_batch_stride;
+  int64_t dy_time_stride;
+  int64_t x_batch_stride;
+  int64_t x_time_stride;
+  int64_t z_batch_stride;
+  int64_t z_time_stride;
+  int64_t dx_batch_stride;
+  int64_t dx_time_stride;
+  int64_t dz_batch_stride;
+  int64_t dz_time_stride;
+} ssm_group_norm_bwd_io;
+
+/* Workspace bytes of ssm_group_norm_bwd; -1 for NULL or invalid dims. */
+int64_t ssm_group_norm_bwd_workspace_bytes(const ssm_group_norm_dims* dims);
+
+int ssm_group_norm_bwd(ssm_scan_t handle, const ssm_group_norm_dims* dims, const ssm_group_norm_bwd_io* io,
+                       void* stream);
 
 /* Release the handle.  NULL is accepted.  The caller must ensure no work
  * enqueued with the handle is still to be launched. */

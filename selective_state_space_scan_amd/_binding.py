@@ -27,6 +27,10 @@ SSM_SCAN_NOALLOC_SCRATCH_BYTES = 16 << 20
 SSM_IO_F32 = 0
 SSM_IO_BF16 = 1
 
+SSM_GATE_NONE = 0
+SSM_GATE_AFTER = 1
+SSM_GATE_BEFORE = 2
+
 SSM_COMBINE_WALK = 0
 SSM_COMBINE_WAVE_SCAN = 1
 
@@ -36,7 +40,10 @@ EXPORTED = ("ssm_scan_create", "ssm_selective_scan_fwd", "ssm_selective_scan_fwd
             "ssm_scan_bwd_workspace_bytes", "ssm_selective_scan_bwd", "ssm_scan_destroy", "ssm_scan_error_string",
             "ssm_selective_scan_fwd_noalloc", "ssm_selective_scan_step", "ssm_causal_conv_fwd",
             "ssm_causal_conv_bwd_workspace_bytes", "ssm_causal_conv_bwd", "ssm_causal_conv_step", "ssm_layer_norm_fwd",
-            "ssm_layer_norm_bwd_workspace_bytes", "ssm_layer_norm_bwd")
+            "ssm_layer_norm_bwd_workspace_bytes", "ssm_layer_norm_bwd", "ssm_gated_recurrence_chunk_len",
+            "ssm_gated_recurrence_fwd_workspace_bytes", "ssm_gated_recurrence_fwd",
+            "ssm_gated_recurrence_bwd_workspace_bytes", "ssm_gated_recurrence_bwd", "ssm_gated_recurrence_step",
+            "ssm_group_norm_fwd", "ssm_group_norm_bwd_workspace_bytes", "ssm_group_norm_bwd")
 
 
 class SsmScanError(RuntimeError):
@@ -226,6 +233,154 @@ class ssm_norm_bwd_io(ctypes.Structure):
     ]
 
 
+class ssm_gated_dims(ctypes.Structure):
+    _fields_ = [
+        ("batch", ctypes.c_int64),
+        ("seqlen", ctypes.c_int64),
+        ("dim", ctypes.c_int64),
+        ("io_dtype", ctypes.c_int32),
+    ]
+
+
+class ssm_gated_fwd_io(ctypes.Structure):
+    _fields_ = [
+        ("x", ctypes.c_void_p),
+        ("a_gate", ctypes.c_void_p),
+        ("x_gate", ctypes.c_void_p),
+        ("A_log", ctypes.c_void_p),
+        ("valid_len", ctypes.c_void_p),
+        ("h0", ctypes.c_void_p),
+        ("y", ctypes.c_void_p),
+        ("h_last", ctypes.c_void_p),
+        ("chunk_states", ctypes.c_void_p),
+        ("workspace", ctypes.c_void_p),
+        ("workspace_bytes", ctypes.c_int64),
+        ("x_batch_stride", ctypes.c_int64),
+        ("x_time_stride", ctypes.c_int64),
+        ("a_gate_batch_stride", ctypes.c_int64),
+        ("a_gate_time_stride", ctypes.c_int64),
+        ("x_gate_batch_stride", ctypes.c_int64),
+        ("x_gate_time_stride", ctypes.c_int64),
+        ("y_batch_stride", ctypes.c_int64),
+        ("y_time_stride", ctypes.c_int64),
+    ]
+
+
+class ssm_gated_bwd_io(ctypes.Structure):
+    _fields_ = [
+        ("x", ctypes.c_void_p),
+        ("a_gate", ctypes.c_void_p),
+        ("x_gate", ctypes.c_void_p),
+        ("A_log", ctypes.c_void_p),
+        ("valid_len", ctypes.c_void_p),
+        ("h0", ctypes.c_void_p),
+        ("dy", ctypes.c_void_p),
+        ("dh_last", ctypes.c_void_p),
+        ("chunk_states", ctypes.c_void_p),
+        ("dx", ctypes.c_void_p),
+        ("da_gate", ctypes.c_void_p),
+        ("dx_gate", ctypes.c_void_p),
+        ("dA_log", ctypes.c_void_p),
+        ("dh0", ctypes.c_void_p),
+        ("workspace", ctypes.c_void_p),
+        ("workspace_bytes", ctypes.c_int64),
+        ("x_batch_stride", ctypes.c_int64),
+        ("x_time_stride", ctypes.c_int64),
+        ("a_gate_batch_stride", ctypes.c_int64),
+        ("a_gate_time_stride", ctypes.c_int64),
+        ("x_gate_batch_stride", ctypes.c_int64),
+        ("x_gate_time_stride", ctypes.c_int64),
+        ("dy_batch_stride", ctypes.c_int64),
+        ("dy_time_stride", ctypes.c_int64),
+        ("dx_batch_stride", ctypes.c_int64),
+        ("dx_time_stride", ctypes.c_int64),
+        ("da_gate_batch_stride", ctypes.c_int64),
+        ("da_gate_time_stride", ctypes.c_int64),
+        ("dx_gate_batch_stride", ctypes.c_int64),
+        ("dx_gate_time_stride", ctypes.c_int64),
+    ]
+
+
+class ssm_gated_step_io(ctypes.Structure):
+    _fields_ = [
+        ("x", ctypes.c_void_p),
+        ("a_gate", ctypes.c_void_p),
+        ("x_gate", ctypes.c_void_p),
+        ("A_log", ctypes.c_void_p),
+        ("slots", ctypes.c_void_p),
+        ("h0", ctypes.c_void_p),
+        ("h_last", ctypes.c_void_p),
+        ("y", ctypes.c_void_p),
+        ("x_row_stride", ctypes.c_int64),
+        ("a_gate_row_stride", ctypes.c_int64),
+        ("x_gate_row_stride", ctypes.c_int64),
+        ("y_row_stride", ctypes.c_int64),
+        ("n_slots", ctypes.c_int64),
+    ]
+
+
+class ssm_group_norm_dims(ctypes.Structure):
+    _fields_ = [
+        ("batch", ctypes.c_int64),
+        ("seqlen", ctypes.c_int64),
+        ("dim", ctypes.c_int64),
+        ("groups", ctypes.c_int64),
+        ("io_dtype", ctypes.c_int32),
+        ("rms", ctypes.c_int32),
+        ("silu", ctypes.c_int32),
+        ("gate", ctypes.c_int32),
+        ("eps", ctypes.c_float),
+    ]
+
+
+class ssm_group_norm_fwd_io(ctypes.Structure):
+    _fields_ = [
+        ("x", ctypes.c_void_p),
+        ("z", ctypes.c_void_p),
+        ("weight", ctypes.c_void_p),
+        ("bias", ctypes.c_void_p),
+        ("valid_len", ctypes.c_void_p),
+        ("y", ctypes.c_void_p),
+        ("mean", ctypes.c_void_p),
+        ("rstd", ctypes.c_void_p),
+        ("x_batch_stride", ctypes.c_int64),
+        ("x_time_stride", ctypes.c_int64),
+        ("z_batch_stride", ctypes.c_int64),
+        ("z_time_stride", ctypes.c_int64),
+        ("y_batch_stride", ctypes.c_int64),
+        ("y_time_stride", ctypes.c_int64),
+    ]
+
+
+class ssm_group_norm_bwd_io(ctypes.Structure):
+    _fields_ = [
+        ("dy", ctypes.c_void_p),
+        ("x", ctypes.c_void_p),
+        ("z", ctypes.c_void_p),
+        ("weight", ctypes.c_void_p),
+        ("bias", ctypes.c_void_p),
+        ("mean", ctypes.c_void_p),
+        ("rstd", ctypes.c_void_p),
+        ("valid_len", ctypes.c_void_p),
+        ("dx", ctypes.c_void_p),
+        ("dz", ctypes.c_void_p),
+        ("dweight", ctypes.c_void_p),
+        ("dbias", ctypes.c_void_p),
+        ("workspace", ctypes.c_void_p),
+        ("workspace_bytes", ctypes.c_int64),
+        ("dy_batch_stride", ctypes.c_int64),
+        ("dy_time_stride", ctypes.c_int64),
+        ("x_batch_stride", ctypes.c_int64),
+        ("x_time_stride", ctypes.c_int64),
+        ("z_batch_stride", ctypes.c_int64),
+        ("z_time_stride", ctypes.c_int64),
+        ("dx_batch_stride", ctypes.c_int64),
+        ("dx_time_stride", ctypes.c_int64),
+        ("dz_batch_stride", ctypes.c_int64),
+        ("dz_time_stride", ctypes.c_int64),
+    ]
+
+
 _lib = None
 _lib_lock = threading.Lock()
 
@@ -283,14 +438,23 @@ def lib() -> ctypes.CDLL:
                                ("causal_conv_bwd", ssm_conv_dims, ssm_conv_bwd_io),
                                ("causal_conv_step", ssm_conv_dims, ssm_conv_step_io),
                                ("layer_norm_fwd", ssm_norm_dims, ssm_norm_fwd_io),
-                               ("layer_norm_bwd", ssm_norm_dims, ssm_norm_bwd_io)):
+                               ("layer_norm_bwd", ssm_norm_dims, ssm_norm_bwd_io),
+                               ("gated_recurrence_fwd", ssm_gated_dims, ssm_gated_fwd_io),
+                               ("gated_recurrence_bwd", ssm_gated_dims, ssm_gated_bwd_io),
+                               ("gated_recurrence_step", ssm_gated_dims, ssm_gated_step_io),
+                               ("group_norm_fwd", ssm_group_norm_dims, ssm_group_norm_fwd_io),
+                               ("group_norm_bwd", ssm_group_norm_dims, ssm_group_norm_bwd_io)):
             f = getattr(L, "ssm_" + name)
             f.argtypes = [vp, ctypes.POINTER(dims), ctypes.POINTER(io), vp]
             f.restype = ctypes.c_int
-        for name, dims in (("causal_conv", ssm_conv_dims), ("layer_norm", ssm_norm_dims)):
-            f = getattr(L, f"ssm_{name}_bwd_workspace_bytes")
+        for name, dims in (("causal_conv_bwd", ssm_conv_dims), ("layer_norm_bwd", ssm_norm_dims),
+                           ("gated_recurrence_fwd", ssm_gated_dims), ("gated_recurrence_bwd", ssm_gated_dims),
+                           ("group_norm_bwd", ssm_group_norm_dims)):
+            f = getattr(L, f"ssm_{name}_workspace_bytes")
             f.argtypes = [ctypes.POINTER(dims)]
             f.restype = ctypes.c_int64
+        L.ssm_gated_recurrence_chunk_len.argtypes = []
+        L.ssm_gated_recurrence_chunk_len.restype = ctypes.c_int64
         _lib = L
         return L
 
@@ -350,6 +514,11 @@ _default_chunk_len = chunk_len  # the parameter of selective_scan_fwd shadows th
 def bwd_chunk_len(dstate: int) -> int:
     """The chunk length the forward must save chunk states at for the backward."""
     return int(lib().ssm_scan_bwd_chunk_len(int(dstate)))
+
+
+def gated_chunk_len() -> int:
+    """Steps between the states that ``gated_recurrence_fwd`` keeps for its backward."""
+    return int(lib().ssm_gated_recurrence_chunk_len())
 
 
 def bwd_workspace_bytes(dims: ssm_scan_dims) -> int:

@@ -1,5 +1,6 @@
 """torch front end of the operators beside the scan in its block: the scan for
-single tokens, the short causal convolution and the layer or RMS norm.
+single tokens, the short causal convolution, the layer or RMS norm, the gated
+recurrence and the group norm.
 
 As for the scan, every step runs in the HIP library.  Shapes, dtypes and
 devices are checked, outputs and scratch allocated and the C ABI called by the
@@ -29,7 +30,11 @@ def _load():
                           "`python -m selective_state_space_scan_amd.build` (or __graft_entry__.build())") from e
     entries = ("ssm_selective_scan_step", "ssm_causal_conv_step", "ssm_causal_conv_fwd", "ssm_causal_conv_bwd",
                "ssm_causal_conv_bwd_workspace_bytes", "ssm_layer_norm_fwd", "ssm_layer_norm_bwd",
-               "ssm_layer_norm_bwd_workspace_bytes")
+               "ssm_layer_norm_bwd_workspace_bytes", "ssm_gated_recurrence_fwd",
+               "ssm_gated_recurrence_fwd_workspace_bytes", "ssm_gated_recurrence_bwd",
+               "ssm_gated_recurrence_bwd_workspace_bytes", "ssm_gated_recurrence_chunk_len",
+               "ssm_gated_recurrence_step", "ssm_group_norm_fwd", "ssm_group_norm_bwd",
+               "ssm_group_norm_bwd_workspace_bytes")
     _ssm_torch.bind(*(ctypes.cast(getattr(lib, name), ctypes.c_void_p).value for name in entries), _b.handle_for,
                     _b.SsmScanError)
     return _ssm_torch
@@ -189,3 +194,109 @@ def layer_norm_bwd(dy, v, weight, mean, rstd, valid_len=None, *, dresidual_out=N
     dx, dresidual, dweight, dbias = _native.norm_bwd(dy, v, weight, mean, rstd, valid_len, dresidual_out, with_bias,
                                                      with_residual, workspace)
     return dict(dx=dx, dresidual=dresidual, dweight=dweight, dbias=dbias)
+
+
+# ---- gated recurrence ------------------------------------------------------
+
+def gated_recurrence_fwd(x, a_gate, x_gate, A_log, valid_len=None, *, h0=None, y=None, h_last=None,
+                         return_chunk_states: bool = False, workspace=None, stream=None):
+    """The gated recurrence over whole sequences; returns ``(y, h_last)``, or ``(y, h_last, chunk_states)``.
+
+    With r = sigmoid(a_gate), i = sigmoid(x_gate) and a = exp(-exp(A_log) r), every
+    channel's state is h = a h + sqrt(1 - a^2) i x, and y = h.
+
+    x, a_gate, x_gate: [batch, L, dim] of one dtype (torch.float32 or
+    torch.bfloat16), last dimension dense, other strides any (both gates may be
+    halves of one projection's output).  A_log [dim] float32.  valid_len [batch]
+    int32 or None: y is 0 past it, nothing there is read and the state stays.
+    h0 [batch, dim] float32: the state before the first step (zeros if None);
+    h_last, likewise: the state after the last valid one.  Outputs are allocated
+    unless given; y may be strided like x, and h_last may be h0 itself.
+    chunk_states [batch, ceil(L / gated_chunk_len()), dim] float32, what the
+    backward takes: the state after every chunk.  workspace: a uint8 tensor as
+    long as the library asks for (allocated if None; never shared by calls that
+    may run at the same time).  Asynchronous on ``stream``.
+    """
+    if stream is not None:
+        with _on(stream, x):
+            return gated_recurrence_fwd(x, a_gate, x_gate, A_log, valid_len, h0=h0, y=y, h_last=h_last,
+                                        return_chunk_states=return_chunk_states, workspace=workspace)
+    return _native.gated_fwd(x, a_gate, x_gate, A_log, valid_len, h0, y, h_last, return_chunk_states, workspace)
+
+
+def gated_recurrence_bwd(x, a_gate, x_gate, A_log, valid_len, dy, chunk_states, *, h0=None, dh_last=None, dx=None,
+                         da_gate=None, dx_gate=None, workspace=None, stream=None) -> dict:
+    """Gradients of ``gated_recurrence_fwd`` for the loss sum(dy * y) + sum(dh_last * h_last).
+
+    The forward's inputs must be given again, with its chunk_states (None where L
+    is at most ``gated_chunk_len()``).  dy like y (any strides, last dimension
+    dense); dh_last like h_last or None.  Returns a dict: dx, da_gate, dx_gate like
+    their inputs (contiguous unless given, strided like x then: the gates' may be
+    the halves of one tensor), dA_log [dim] and dh0 like h0 (None without h0), both
+    float32.
+    """
+    if stream is not None:
+        with _on(stream, x):
+            return gated_recurrence_bwd(x, a_gate, x_gate, A_log, valid_len, dy, chunk_states, h0=h0, dh_last=dh_last,
+                                        dx=dx, da_gate=da_gate, dx_gate=dx_gate, workspace=workspace)
+    dx, da_gate, dx_gate, dA_log, dh0 = _native.gated_bwd(x, a_gate, x_gate, A_log, valid_len, h0, dy, dh_last,
+                                                          chunk_states, dx, da_gate, dx_gate, workspace)
+    return dict(dx=dx, da_gate=da_gate, dx_gate=dx_gate, dA_log=dA_log, dh0=dh0)
+
+
+def gated_recurrence_step(x, a_gate, x_gate, A_log, h, *, slots=None, h_last=None, y=None, stream=None):
+    """One step of the gated recurrence for every row of a batch; returns y.
+
+    x, a_gate, x_gate: [batch, dim] of one dtype, any row stride.  A_log [dim]
+    float32.  h: the states, float32, [batch, dim], or with ``slots`` a cache
+    [n_slots, dim]; updated in place, or with ``h_last`` (like h) written there.
+    slots and idle rows as in ``selective_scan_step``.
+    """
+    if stream is not None:
+        with _on(stream, x):
+            return gated_recurrence_step(x, a_gate, x_gate, A_log, h, slots=slots, h_last=h_last, y=y)
+    return _native.gated_step(x, a_gate, x_gate, A_log, h, slots, h_last, y)
+
+
+# ---- group norm ------------------------------------------------------------
+
+def group_norm_fwd(x, groups: int, weight, bias=None, valid_len=None, *, z=None, silu: bool = True,
+                   gate_first: bool = False, eps: float = 1e-5, rms: bool = False, y=None, return_stats: bool = False,
+                   stream=None):
+    """Norm of every group of a step's channels, with an activation or a gate; returns y.
+
+    With act(u) = u sigmoid(u) (u without ``silu``) and p the layer norm (RMS norm
+    with ``rms``) of each of the ``groups`` groups of adjacent channels, by
+    weight and bias: y = act(p) without z, p * act(z) with z, and with
+    ``gate_first`` p of x * act(z).  Every step is normalised by itself.
+
+    x, z (or None): [rows, dim] or [batch, L, dim], float32 or bfloat16, last
+    dimension dense, other strides any; a group has at most 8192 channels.
+    weight and bias (or None): [dim] float32.  valid_len [batch] int32 or None
+    (for [batch, L, dim]): rows past it give 0 and are not read.  y is allocated
+    unless given (strided like x).  With ``return_stats``: ``(y, mean, rstd)``, the
+    statistics [..., groups] float32 that the backward takes (mean None with rms).
+    """
+    if stream is not None:
+        with _on(stream, x):
+            return group_norm_fwd(x, groups, weight, bias, valid_len, z=z, silu=silu, gate_first=gate_first, eps=eps,
+                                  rms=rms, y=y, return_stats=return_stats)
+    return _native.group_fwd(x, groups, weight, bias, valid_len, z, silu, gate_first, eps, rms, y, return_stats)
+
+
+def group_norm_bwd(dy, x, groups: int, weight, bias, mean, rstd, valid_len=None, *, z=None, silu: bool = True,
+                   gate_first: bool = False, dx=None, dz=None, workspace=None, stream=None) -> dict:
+    """Gradients of ``group_norm_fwd`` for the loss sum(dy * y).
+
+    x, z, weight, bias, valid_len and the flags: the forward's; mean and rstd as
+    it returned them (mean None for RMS norm).  dy like y.  Returns a dict: dx,
+    dz (None without z) like x and z (contiguous unless given, strided like x
+    then); dweight and dbias (None without bias) [dim] float32.
+    """
+    if stream is not None:
+        with _on(stream, dy):
+            return group_norm_bwd(dy, x, groups, weight, bias, mean, rstd, valid_len, z=z, silu=silu,
+                                  gate_first=gate_first, dx=dx, dz=dz, workspace=workspace)
+    dx, dz, dweight, dbias = _native.group_bwd(dy, x, groups, weight, bias, mean, rstd, valid_len, z, silu, gate_first,
+                                               dx, dz, workspace)
+    return dict(dx=dx, dz=dz, dweight=dweight, dbias=dbias)

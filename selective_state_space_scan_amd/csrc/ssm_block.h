@@ -370,6 +370,47 @@ inline bool any_overlap(const Range (&in)[NI], const Range (&out)[NO]) {
   return false;
 }
 
+// A strided [n0, n1, dim] tensor that a call reads or writes (dim fastest,
+// strides in elements of e bytes), or none of one.
+struct Rows {
+  const void* p;
+  int64_t n0, s0, n1, s1, dim, e;
+  int64_t bytes() const { return span_bytes(n0, s0, n1, s1, dim, e); }
+  bool disjoint() const { return rows_disjoint(n0, s0, n1, s1, dim); }
+};
+
+// n bytes in one piece.
+inline Rows flat(const void* p, int64_t n) { return Rows{p, 1, 0, 1, 0, n, 1}; }
+
+// Whether two tensors overlap, as the ranges from their first byte to their
+// last; but the columns of one buffer do not: with strides that are all
+// multiples of one, m, in both, a row's elements keep their places modulo m.
+inline bool rows_overlap(const Rows& a, const Rows& b) {
+  if (!overlaps(a.p, static_cast<size_t>(a.bytes()), b.p, static_cast<size_t>(b.bytes()))) return false;
+  int64_t m = 0;
+  for (const Rows* r : {&a, &b}) {
+    if (r->n0 > 1 && (m == 0 || r->s0 * r->e < m)) m = r->s0 * r->e;
+    if (r->n1 > 1 && (m == 0 || r->s1 * r->e < m)) m = r->s1 * r->e;
+  }
+  if (m == 0) return true;
+  for (const Rows* r : {&a, &b})
+    if ((r->n0 > 1 && r->s0 * r->e % m != 0) || (r->n1 > 1 && r->s1 * r->e % m != 0)) return true;
+  const int64_t wide = reinterpret_cast<intptr_t>(b.p) - reinterpret_cast<intptr_t>(a.p);
+  const int64_t off = (wide % m + m) % m;
+  return off < a.dim * a.e || off + b.dim * b.e > m;
+}
+
+template <int NI, int NO>
+inline bool any_overlap(const Rows (&in)[NI], const Rows (&out)[NO]) {
+  for (int o = 0; o < NO; ++o) {
+    for (int i = 0; i < NI; ++i)
+      if (rows_overlap(out[o], in[i])) return true;
+    for (int k = 0; k < o; ++k)
+      if (rows_overlap(out[o], out[k])) return true;
+  }
+  return false;
+}
+
 // The handle, and that the calling thread's current device is the handle's.
 inline int check_handle(ssm_scan_t handle) {
   if (handle == nullptr) return SSM_ERR_INVALID_ARG;

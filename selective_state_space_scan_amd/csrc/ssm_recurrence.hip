@@ -1,0 +1,643 @@
+// The gated recurrence, for MI355X (gfx950): forward, backward, and one step on
+// a cache of states.
+//
+// For every batch row b, channel d and step t < valid_len[b], with r =
+// sigmoid(a_gate), i = sigmoid(x_gate) and s = exp(A_log[d]) r:
+//
+//     a[t] = exp(-s),  c[t] = sqrt(1 - a[t]^2),  h[t] = a[t] h[t-1] + c[t] i[t] x[t],  y[t] = h[t]
+//
+// Backward, g[t] the gradient of h[t]:
+//
+//     g[t] = dy[t] + a[t+1] g[t+1]  (dh_last behind the last step),
+//     dx = g c i,  dx_gate = g c i x (1 - i),  q = s dL/ds = (s a^2 / c) g i x - s a g h[t-1],
+//     da_gate = q (1 - r),  dA_log = sum over b, t of q,  dh0 = a[0] g[0]
+//
+// (s enters through exp(A_log) and through r, so its own gradient is wanted
+// only as s dL/ds; s a^2 / c goes to 0 with s.)
+//
+// Both recurrences are affine, h -> a h + u, and affine maps compose: (P, S)
+// behind (P', S') is (P P', P S' + S).  A lane folds the steps it holds into
+// one pair, a workgroup's waves join theirs in LDS, and every step is then
+// known from the state in front of its lane.
+
+#include <hip/hip_runtime.h>
+
+#include <cstdint>
+
+#include "ssm_block.h"
+
+namespace {
+
+constexpr int kChunk = 64;  // steps between kept states
+
+struct GatedParams {
+  const void* x;
+  const void* ag;
+  const void* xg;
+  const float* A_log;
+  const int32_t* valid_len;
+  const float* h0;
+  void* y;
+  float* h_last;
+  float* states;
+  int64_t x_bs, x_ts, ag_bs, ag_ts, xg_bs, xg_ts, y_bs, y_ts;
+  int64_t L;
+  int32_t nd, n_cg, n_states;
+};
+
+struct GatedBwdParams {
+  const void* x;
+  const void* ag;
+  const void* xg;
+  const float* A_log;
+  const int32_t* valid_len;
+  const float* h0;
+  const void* dy;
+  const float* dh_last;
+  const float* states;
+  void* dx;
+  void* dag;
+  void* dxg;
+  float* dh0;
+  float* ws;
+  int64_t x_bs, x_ts, ag_bs, ag_ts, xg_bs, xg_ts, dy_bs, dy_ts, dx_bs, dx_ts, dag_bs, dag_ts, dxg_bs, dxg_ts;
+  int64_t L;
+  int32_t nd, n_cg, n_states;
+};
+
+// 1 - a^2 for a = e^(-q/2): near q = 0, where the difference would cancel, the
+// series q - q^2/2! + q^3/3! - ..., whose first term left out is at most
+// q^8/9! = 1e-8 of it at q = 1/2; from there on the difference loses at most 1.5
+// times a^2's own rounding.
+__device__ __forceinline__ float one_minus_square(float a, float q) {
+  float p = __builtin_fmaf(q, -1.0f / 40320, 1.0f / 5040);
+  p = __builtin_fmaf(q, p, -1.0f / 720);
+  p = __builtin_fmaf(q, p, 1.0f / 120);
+  p = __builtin_fmaf(q, p, -1.0f / 24);
+  p = __builtin_fmaf(q, p, 1.0f / 6);
+  p = __builtin_fmaf(q, p, -0.5f);
+  p = __builtin_fmaf(q, p, 1.0f) * q;
+  return q < 0.5f ? p : __builtin_fmaf(-a, a, 1.0f);
+}
+
+// A gate's sigmoid.  sigmoid_exact cuts its argument, and a NaN there comes out as
+// a bound; a gate that is no number has to show in the state.
+template <typename IO>
+__device__ __forceinline__ float gate_sigmoid(float v) {
+  const float s = sigmoid_for<IO>(v);
+  return sizeof(IO) == 2 || v == v ? s : v;
+}
+
+// A step's gates.  rate2 = exp(A_log) log2(e), so that a = 2^(-s2).
+struct Gate {
+  float r, i, s, a, c;
+};
+template <typename IO>
+__device__ __forceinline__ Gate gate_of(float ag, float xg, float rate2) {
+  Gate g;
+  g.r = gate_sigmoid<IO>(ag);
+  g.i = gate_sigmoid<IO>(xg);
+  const float s2 = rate2 * g.r;
+  g.s = s2 * kLn2;
+  g.a = fast_exp2(-s2);
+  g.c = __builtin_amdgcn_sqrtf(one_minus_square(g.a, 2.0f * g.s));
+  return g;
+}
+
+__device__ __forceinline__ int32_t length_of(const int32_t* valid_len, int32_t b, int64_t L) {
+  if (valid_len == nullptr) return static_cast<int32_t>(L);
+  const int32_t n = valid_len[b];
+  return n < 0 ? 0 : (n > L ? static_cast<int32_t>(L) : n);
+}
+
+__device__ __forceinline__ int wave_index() { return __builtin_amdgcn_readfirstlane(threadIdx.x / 64); }
+
+// V channels of T steps as they stand in memory.  Steps past the last one read
+// it again (their values are not used).
+template <typename IO, int V, int T>
+struct Steps {
+  RawVec<IO, V> raw[T];
+  __device__ __forceinline__ void load(const void* base, int64_t ts, int32_t t0, int32_t last, int32_t d) {
+    const IO* p = static_cast<const IO*>(base);
+#pragma unroll
+    for (int t = 0; t < T; ++t) raw[t].load(p + (t0 + t < last ? t0 + t : last) * ts + d);
+  }
+};
+
+// The states of a workgroup's waves in front of their steps: (P, S) of every
+// wave meet in LDS, and each composes those of the waves in front of it behind
+// `h`, the state in front of the workgroup.  `h` becomes the wave's; what the
+// whole workgroup leaves goes to `out`.
+template <int V, int W, bool REVERSE>
+__device__ __forceinline__ void join_waves(float (&lds)[W][2 * V][64], int wave, const float (&P)[V],
+                                           const float (&S)[V], float (&h)[V], float (&out)[V]) {
+  const int lane = threadIdx.x % 64;
+  // the state in front has arrived in every wave before any of them writes the
+  // one behind, which may go to the same place
+#pragma unroll
+  for (int v = 0; v < V; ++v) asm volatile("" : "+v"(h[v]));
+  __syncthreads();  // the last join has been read
+#pragma unroll
+  for (int v = 0; v < V; ++v) lds[wave][v][lane] = P[v], lds[wave][V + v][lane] = S[v];
+  __syncthreads();
+  float mine[V];
+#pragma unroll
+  for (int k = 0; k < W; ++k) {
+    const int w = REVERSE ? W - 1 - k : k;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      if (w == wave) mine[v] = h[v];
+      h[v] = __builtin_fmaf(lds[w][v][lane], h[v], lds[w][V + v][lane]);
+    }
+  }
+#pragma unroll
+  for (int v = 0; v < V; ++v) out[v] = h[v], h[v] = mine[v];
+}
+
+// A workgroup takes 64 V channels of one row and walks their steps, W waves of T
+// steps side by side.  Lanes past the last channel repeat the last V of the row
+// (which a lane whose V would reach past it takes too: both compute and write
+// the same).
+template <typename IO, int V, int T, int W>
+__global__ __launch_bounds__(64 * W) void gated_fwd_kernel(const GatedParams prm) {
+  __shared__ float lds[W][2 * V][64];
+  const int wave = wave_index(), lane = threadIdx.x % 64;
+  const int32_t b = blockIdx.x / prm.n_cg, cg = blockIdx.x % prm.n_cg;
+  const int32_t first = (cg * 64 + lane) * V, d = first < prm.nd - V ? first : prm.nd - V;
+  const bool mine = first < prm.nd;
+  const int32_t n = length_of(prm.valid_len, b, prm.L);
+  const IO* x = static_cast<const IO*>(prm.x) + b * prm.x_bs;
+  const IO* ag = static_cast<const IO*>(prm.ag) + b * prm.ag_bs;
+  const IO* xg = static_cast<const IO*>(prm.xg) + b * prm.xg_bs;
+  IO* y = static_cast<IO*>(prm.y) + b * prm.y_bs;
+  float rate2[V], h[V] = {};
+#pragma unroll
+  for (int v = 0; v < V; ++v) rate2[v] = expf(prm.A_log[d + v]) * kLog2e;
+  if (prm.h0 != nullptr) VecIO<float>::load(prm.h0 + static_cast<int64_t>(b) * prm.nd + d, h);
+  int32_t tile = 0;
+  for (; tile < n; tile += T * W) {
+    const int32_t t0 = tile + wave * T;
+    float a[T][V], u[T][V], P[V], S[V], out[V];
+    Steps<IO, V, T> sx, sa, sg;
+    sx.load(x, prm.x_ts, t0, n - 1, d);
+    sa.load(ag, prm.ag_ts, t0, n - 1, d);
+    sg.load(xg, prm.xg_ts, t0, n - 1, d);
+#pragma unroll
+    for (int v = 0; v < V; ++v) P[v] = 1.0f, S[v] = 0.0f;
+#pragma unroll
+    for (int t = 0; t < T; ++t) {
+      float xv[V], av[V], gv[V];
+      sx.raw[t].unpack(xv);
+      sa.raw[t].unpack(av);
+      sg.raw[t].unpack(gv);
+      const bool valid = t0 + t < n;
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const Gate g = gate_of<IO>(av[v], gv[v], rate2[v]);
+        a[t][v] = valid ? g.a : 1.0f;
+        u[t][v] = valid ? g.c * g.i * xv[v] : 0.0f;
+        P[v] *= a[t][v];
+        S[v] = __builtin_fmaf(a[t][v], S[v], u[t][v]);
+      }
+    }
+    join_waves<V, W, false>(lds, wave, P, S, h, out);
+#pragma unroll
+    for (int t = 0; t < T; ++t) {
+      const bool valid = t0 + t < n;
+      float o[V];
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        h[v] = __builtin_fmaf(a[t][v], h[v], u[t][v]);
+        o[v] = valid ? h[v] : 0.0f;
+      }
+      if (mine && t0 + t < prm.L) VecIO<IO>::store(y + (t0 + t) * prm.y_ts + d, o);
+    }
+    // a chunk ends with a wave's last step
+    static_assert(kChunk % T == 0, "chunks are whole waves");
+    if (prm.states != nullptr && mine && (t0 + T) % kChunk == 0 && (t0 + T) / kChunk <= prm.n_states)
+      VecIO<float>::store(prm.states + (static_cast<int64_t>(b) * prm.n_states + (t0 + T) / kChunk - 1) * prm.nd + d, h);
+#pragma unroll
+    for (int v = 0; v < V; ++v) h[v] = out[v];
+  }
+  if (wave == 0 && mine && prm.h_last != nullptr)
+    VecIO<float>::store(prm.h_last + static_cast<int64_t>(b) * prm.nd + d, h);
+  if (!mine) return;
+  // behind the row's end: steps that are padding, and states that stay
+  for (int64_t t = tile + wave; t < prm.L; t += W) {
+    const float zero[V] = {};
+    VecIO<IO>::store(y + t * prm.y_ts + d, zero);
+  }
+  if (prm.states != nullptr)
+    for (int32_t c = tile / kChunk + wave; c < prm.n_states; c += W)
+      VecIO<float>::store(prm.states + (static_cast<int64_t>(b) * prm.n_states + c) * prm.nd + d, h);
+}
+
+// The same from the row's end.  A tile's states come again from the kept one in
+// front of it; its W T steps are whole chunks.
+template <typename IO, int V, int T, int W>
+__global__ __launch_bounds__(64 * W) void gated_bwd_kernel(const GatedBwdParams prm) {
+  static_assert(T * W % kChunk == 0, "a tile begins behind a kept state");
+  __shared__ float lds[W][2 * V][64];
+  const int wave = wave_index(), lane = threadIdx.x % 64;
+  const int32_t b = blockIdx.x / prm.n_cg, cg = blockIdx.x % prm.n_cg;
+  const int32_t first = (cg * 64 + lane) * V, d = first < prm.nd - V ? first : prm.nd - V;
+  const bool mine = first < prm.nd;
+  const int32_t n = length_of(prm.valid_len, b, prm.L);
+  const int64_t bd = static_cast<int64_t>(b) * prm.nd + d;
+  const IO* x = static_cast<const IO*>(prm.x) + b * prm.x_bs;
+  const IO* ag = static_cast<const IO*>(prm.ag) + b * prm.ag_bs;
+  const IO* xg = static_cast<const IO*>(prm.xg) + b * prm.xg_bs;
+  const IO* dy = static_cast<const IO*>(prm.dy) + b * prm.dy_bs;
+  IO* dx = static_cast<IO*>(prm.dx) + b * prm.dx_bs;
+  IO* dag = static_cast<IO*>(prm.dag) + b * prm.dag_bs;
+  IO* dxg = static_cast<IO*>(prm.dxg) + b * prm.dxg_bs;
+  float rate2[V], g[V] = {}, dA[V] = {};
+#pragma unroll
+  for (int v = 0; v < V; ++v) rate2[v] = expf(prm.A_log[d + v]) * kLog2e;
+  if (prm.dh_last != nullptr) VecIO<float>::load(prm.dh_last + bd, g);
+  const int32_t tiles = (n + T * W - 1) / (T * W);
+  for (int32_t k = tiles - 1; k >= 0; --k) {
+    const int32_t tile = k * T * W, t0 = tile + wave * T;
+    float a[T][V], hp[T][V], P[V], S[V], h[V] = {}, out[V];
+    Steps<IO, V, T> sx, sa, sg, sd;
+    sx.load(x, prm.x_ts, t0, n - 1, d);
+    sa.load(ag, prm.ag_ts, t0, n - 1, d);
+    sg.load(xg, prm.xg_ts, t0, n - 1, d);
+    sd.load(dy, prm.dy_ts, t0, n - 1, d);
+    if (tile > 0)
+      VecIO<float>::load(prm.states + (static_cast<int64_t>(b) * prm.n_states + tile / kChunk - 1) * prm.nd + d, h);
+    else if (prm.h0 != nullptr)
+      VecIO<float>::load(prm.h0 + bd, h);
+#pragma unroll
+    for (int v = 0; v < V; ++v) P[v] = 1.0f, S[v] = 0.0f;
+#pragma unroll
+    for (int t = 0; t < T; ++t) {
+      float xv[V], av[V], gv[V];
+      sx.raw[t].unpack(xv);
+      sa.raw[t].unpack(av);
+      sg.raw[t].unpack(gv);
+      const bool valid = t0 + t < n;
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const Gate q = gate_of<IO>(av[v], gv[v], rate2[v]);
+        a[t][v] = valid ? q.a : 1.0f;
+        hp[t][v] = valid ? q.c * q.i * xv[v] : 0.0f;
+        P[v] *= a[t][v];
+        S[v] = __builtin_fmaf(a[t][v], S[v], hp[t][v]);
+      }
+    }
+    join_waves<V, W, false>(lds, wave, P, S, h, out);
+    // hp becomes the state in front of each step
+#pragma unroll
+    for (int t = 0; t < T; ++t)
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const float u = hp[t][v];
+        hp[t][v] = h[v];
+        h[v] = __builtin_fmaf(a[t][v], h[v], u);
+      }
+    // what comes into a wave from behind leaves it as a (dy + .) of its first step
+#pragma unroll
+    for (int v = 0; v < V; ++v) P[v] = 1.0f, S[v] = 0.0f;
+#pragma unroll
+    for (int t = T - 1; t >= 0; --t) {
+      float dv[V];
+      sd.raw[t].unpack(dv);
+      const bool valid = t0 + t < n;
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        P[v] *= a[t][v];
+        S[v] = a[t][v] * (S[v] + (valid ? dv[v] : 0.0f));
+      }
+    }
+    join_waves<V, W, true>(lds, wave, P, S, g, out);
+#pragma unroll
+    for (int t = T - 1; t >= 0; --t) {
+      float xv[V], av[V], gv[V], dv[V], ox[V], oa[V], og[V];
+      sx.raw[t].unpack(xv);
+      sa.raw[t].unpack(av);
+      sg.raw[t].unpack(gv);
+      sd.raw[t].unpack(dv);
+      const bool valid = t0 + t < n;
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const Gate q = gate_of<IO>(av[v], gv[v], rate2[v]);
+        const float gt = g[v] + dv[v], gi = gt * q.i, gx = gi * xv[v];
+        // s a -> 0 for large s too, where a is 0
+        const float sa = q.a > 0.0f ? q.s * q.a : 0.0f;
+        const float ratio = q.c > 0.0f ? sa * q.a * __builtin_amdgcn_rcpf(q.c) : 0.0f;
+        const float p = ratio * gx - sa * gt * hp[t][v];
+        ox[v] = valid ? gi * q.c : 0.0f;
+        og[v] = valid ? gx * q.c * (1.0f - q.i) : 0.0f;
+        oa[v] = valid ? p * (1.0f - q.r) : 0.0f;
+        dA[v] += valid ? p : 0.0f;
+        g[v] = valid ? gt * a[t][v] : g[v];
+      }
+      if (mine && t0 + t < prm.L) {
+        VecIO<IO>::store(dx + (t0 + t) * prm.dx_ts + d, ox);
+        VecIO<IO>::store(dag + (t0 + t) * prm.dag_ts + d, oa);
+        VecIO<IO>::store(dxg + (t0 + t) * prm.dxg_ts + d, og);
+      }
+    }
+#pragma unroll
+    for (int v = 0; v < V; ++v) g[v] = out[v];
+  }
+  if (wave == 0 && mine && prm.dh0 != nullptr) VecIO<float>::store(prm.dh0 + bd, g);
+  if (mine) {
+    for (int64_t t = static_cast<int64_t>(tiles) * T * W + wave; t < prm.L; t += W) {
+      const float zero[V] = {};
+      VecIO<IO>::store(dx + t * prm.dx_ts + d, zero);
+      VecIO<IO>::store(dag + t * prm.dag_ts + d, zero);
+      VecIO<IO>::store(dxg + t * prm.dxg_ts + d, zero);
+    }
+  }
+  // the waves' sums of q, in order
+  __syncthreads();
+#pragma unroll
+  for (int v = 0; v < V; ++v) lds[wave][v][lane] = dA[v];
+  __syncthreads();
+  if (wave == 0 && mine) {
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+      for (int w = 1; w < W; ++w) dA[v] += lds[w][v][lane];
+    VecIO<float>::store(prm.ws + bd, dA);
+  }
+}
+
+struct GatedGrads {
+  float* dA;
+  __device__ __forceinline__ void operator()(int64_t col, float v) const { dA[col] = v; }
+};
+
+__global__ void gated_copy_kernel(const float* from, float* to, int64_t n) {
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  if (i < n) to[i] = from == nullptr ? 0.0f : from[i];
+}
+
+// ---- single tokens ---------------------------------------------------------
+
+struct GatedStepParams {
+  const void* x;
+  const void* ag;
+  const void* xg;
+  const float* A_log;
+  const int32_t* slots;
+  const float* h0;
+  float* h_last;
+  void* y;
+  int64_t x_rs, ag_rs, xg_rs, y_rs, n_slots;
+  int32_t nb, nd;
+};
+
+// A lane takes V channels of one row: 16 bytes of states.
+template <typename IO, int V>
+__global__ __launch_bounds__(256) void gated_step_kernel(const GatedStepParams prm) {
+  const int32_t b = blockIdx.y;
+  const int64_t d = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * V;
+  const int m = d >= prm.nd ? 0 : (prm.nd - d < V ? static_cast<int>(prm.nd - d) : V);
+  const int32_t slot[1] = {prm.slots == nullptr ? b : prm.slots[b]};
+  const int64_t at = static_cast<int64_t>(slot[0]) * prm.nd + d;
+  float h[V] = {}, x[V] = {}, ag[V] = {}, xg[V] = {}, al[V];
+  // a row that turns out idle is read all the same, inside its bounds
+  const int k = slot[0] >= 0 && slot[0] < prm.n_slots ? m : 0;
+  load_n<float, V>(prm.h0 + at, k, h);
+  load_n<IO, V>(static_cast<const IO*>(prm.x) + b * prm.x_rs + d, k, x);
+  load_n<IO, V>(static_cast<const IO*>(prm.ag) + b * prm.ag_rs + d, k, ag);
+  load_n<IO, V>(static_cast<const IO*>(prm.xg) + b * prm.xg_rs + d, k, xg);
+  load_n<float, V>(prm.A_log + d, m, al);
+  bool active[1];
+  step_rows_active<1>(prm.slots, b, prm.nb, slot, prm.n_slots, active);
+  float o[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    const Gate g = gate_of<IO>(ag[v], xg[v], expf(al[v]) * kLog2e);
+    h[v] = __builtin_fmaf(g.a, h[v], g.c * g.i * x[v]);
+    o[v] = active[0] ? h[v] : 0.0f;
+  }
+  if (active[0]) store_n<float, V>(prm.h_last + at, m, h);
+  store_n<IO, V>(static_cast<IO*>(prm.y) + b * prm.y_rs + d, m, o);
+}
+
+// ---- host ------------------------------------------------------------------
+
+constexpr int64_t kMaxGatedDim = 1 << 29;
+
+int check_gated_dims(const ssm_gated_dims* dims) {
+  if (dims == nullptr || dims->batch < 0 || dims->seqlen < 0 || dims->dim < 0) return SSM_ERR_INVALID_ARG;
+  if (dims->io_dtype != SSM_IO_F32 && dims->io_dtype != SSM_IO_BF16) return SSM_ERR_INVALID_ARG;
+  // a row's steps are counted in 32 bits, a tile's beyond its end among them
+  if (dims->dim >= kMaxGatedDim || dims->batch > kMaxSize || dims->seqlen > kMaxSize - 65536) return SSM_ERR_UNSUPPORTED;
+  if (static_cast<__int128>(dims->batch) * (dims->seqlen + 1) * dims->dim * 4 >= (static_cast<__int128>(1) << 62))
+    return SSM_ERR_UNSUPPORTED;
+  return SSM_OK;
+}
+
+int64_t n_states(const ssm_gated_dims* dims) { return (dims->seqlen + kChunk - 1) / kChunk; }
+
+// Channels of a workgroup: two a lane, one where two would leave half of a wave
+// idle.
+constexpr int64_t kNarrow = 64;
+
+template <typename F>
+void for_gated(const ssm_gated_dims* dims, const F& f) {
+  const bool narrow = dims->dim <= kNarrow;
+  if (dims->io_dtype == SSM_IO_BF16)
+    narrow ? f.template operator()<uint16_t, 1>() : f.template operator()<uint16_t, 2>();
+  else
+    narrow ? f.template operator()<float, 1>() : f.template operator()<float, 2>();
+}
+
+constexpr int kSteps = 8, kWaves = 8;
+
+}  // namespace
+
+extern "C" {
+
+int64_t ssm_gated_recurrence_chunk_len(void) { return kChunk; }
+
+int64_t ssm_gated_recurrence_fwd_workspace_bytes(const ssm_gated_dims* dims) {
+  if (check_gated_dims(dims) != SSM_OK) return -1;
+  return 0;
+}
+
+int ssm_gated_recurrence_fwd(ssm_scan_t handle, const ssm_gated_dims* dims, const ssm_gated_fwd_io* io, void* stream) {
+  const int bad = check_gated_dims(dims);
+  if (bad != SSM_OK) return bad;
+  if (io == nullptr || io->workspace_bytes < 0) return SSM_ERR_INVALID_ARG;
+  const int64_t nb = dims->batch, L = dims->seqlen, nd = dims->dim, ns = n_states(dims);
+  const int64_t e = dims->io_dtype == SSM_IO_BF16 ? 2 : 4;
+  const int64_t need = ssm_gated_recurrence_fwd_workspace_bytes(dims);
+  const bool empty = nb == 0 || nd == 0;
+  if (!empty) {
+    if (L > 0 && (io->x == nullptr || io->a_gate == nullptr || io->x_gate == nullptr || io->A_log == nullptr ||
+                  io->y == nullptr))
+      return SSM_ERR_INVALID_ARG;
+    if (need > 0 && (io->workspace == nullptr || io->workspace_bytes < need)) return SSM_ERR_INVALID_ARG;
+    const Rows x{io->x, nb, io->x_batch_stride, L, io->x_time_stride, nd, e};
+    const Rows ag{io->a_gate, nb, io->a_gate_batch_stride, L, io->a_gate_time_stride, nd, e};
+    const Rows xg{io->x_gate, nb, io->x_gate_batch_stride, L, io->x_gate_time_stride, nd, e};
+    const Rows y{io->y, nb, io->y_batch_stride, L, io->y_time_stride, nd, e};
+    if (x.bytes() < 0 || ag.bytes() < 0 || xg.bytes() < 0 || y.bytes() < 0 || !y.disjoint()) return SSM_ERR_INVALID_ARG;
+    if (!aligned(io->x, e) || !aligned(io->a_gate, e) || !aligned(io->x_gate, e) || !aligned(io->y, e) ||
+        !aligned(io->A_log, 4) || !aligned(io->valid_len, 4) || !aligned(io->h0, 4) || !aligned(io->h_last, 4) ||
+        !aligned(io->chunk_states, 4) || !aligned(io->workspace, 8))
+      return SSM_ERR_UNSUPPORTED;
+    // the state may be updated in place: it is read before it is written
+    const Rows in[] = {x, ag, xg, flat(io->A_log, nd * 4), flat(io->valid_len, nb * 4),
+                       flat(io->h0, io->h0 == io->h_last ? 0 : nb * nd * 4)};
+    const Rows out[] = {y, flat(io->h_last, nb * nd * 4), flat(io->chunk_states, nb * ns * nd * 4),
+                        flat(io->workspace, io->workspace_bytes)};
+    if (any_overlap(in, out)) return SSM_ERR_ALIAS;
+  }
+  const int rc = check_handle(handle);
+  if (rc != SSM_OK || empty) return rc;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  if (L == 0) {
+    if (io->h_last == nullptr || io->h_last == io->h0) return SSM_OK;
+    const int64_t blocks = (nb * nd + 255) / 256;
+    if (!grid_fits(blocks, 256)) return SSM_ERR_UNSUPPORTED;
+    hipLaunchKernelGGL(gated_copy_kernel, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, s, io->h0, io->h_last,
+                       nb * nd);
+    return launched();
+  }
+
+  GatedParams p;
+  p.x = io->x, p.ag = io->a_gate, p.xg = io->x_gate, p.A_log = io->A_log, p.valid_len = io->valid_len, p.h0 = io->h0;
+  p.y = io->y, p.h_last = io->h_last, p.states = io->chunk_states;
+  p.x_bs = io->x_batch_stride, p.x_ts = io->x_time_stride, p.ag_bs = io->a_gate_batch_stride;
+  p.ag_ts = io->a_gate_time_stride, p.xg_bs = io->x_gate_batch_stride, p.xg_ts = io->x_gate_time_stride;
+  p.y_bs = io->y_batch_stride, p.y_ts = io->y_time_stride;
+  p.L = L, p.nd = static_cast<int32_t>(nd), p.n_states = static_cast<int32_t>(ns);
+  bool fits = true;
+  for_gated(dims, [&]<typename IO, int V>() {
+    p.n_cg = static_cast<int32_t>((nd + 64 * V - 1) / (64 * V));
+    fits = grid_fits(nb * p.n_cg, 64 * kWaves);
+    if (fits)
+      hipLaunchKernelGGL((gated_fwd_kernel<IO, V, kSteps, kWaves>), dim3(static_cast<unsigned>(nb * p.n_cg)),
+                         dim3(64 * kWaves), 0, s, p);
+  });
+  return fits ? launched() : SSM_ERR_UNSUPPORTED;
+}
+
+int64_t ssm_gated_recurrence_bwd_workspace_bytes(const ssm_gated_dims* dims) {
+  if (check_gated_dims(dims) != SSM_OK) return -1;
+  return dims->batch * dims->dim * 4;
+}
+
+int ssm_gated_recurrence_bwd(ssm_scan_t handle, const ssm_gated_dims* dims, const ssm_gated_bwd_io* io, void* stream) {
+  const int bad = check_gated_dims(dims);
+  if (bad != SSM_OK) return bad;
+  if (io == nullptr || io->workspace_bytes < 0) return SSM_ERR_INVALID_ARG;
+  const int64_t nb = dims->batch, L = dims->seqlen, nd = dims->dim, ns = n_states(dims);
+  const int64_t e = dims->io_dtype == SSM_IO_BF16 ? 2 : 4;
+  const int64_t need = ssm_gated_recurrence_bwd_workspace_bytes(dims);
+  const bool some = nb > 0 && L > 0;
+  if (nd > 0) {
+    if (io->dA_log == nullptr) return SSM_ERR_INVALID_ARG;
+    if (some && (io->x == nullptr || io->a_gate == nullptr || io->x_gate == nullptr || io->A_log == nullptr ||
+                 io->dy == nullptr || io->dx == nullptr || io->da_gate == nullptr || io->dx_gate == nullptr ||
+                 (io->chunk_states == nullptr && L > kChunk) || io->workspace == nullptr || io->workspace_bytes < need))
+      return SSM_ERR_INVALID_ARG;
+    const Rows x{io->x, nb, io->x_batch_stride, L, io->x_time_stride, nd, e};
+    const Rows ag{io->a_gate, nb, io->a_gate_batch_stride, L, io->a_gate_time_stride, nd, e};
+    const Rows xg{io->x_gate, nb, io->x_gate_batch_stride, L, io->x_gate_time_stride, nd, e};
+    const Rows dy{io->dy, nb, io->dy_batch_stride, L, io->dy_time_stride, nd, e};
+    const Rows dx{io->dx, nb, io->dx_batch_stride, L, io->dx_time_stride, nd, e};
+    const Rows dag{io->da_gate, nb, io->da_gate_batch_stride, L, io->da_gate_time_stride, nd, e};
+    const Rows dxg{io->dx_gate, nb, io->dx_gate_batch_stride, L, io->dx_gate_time_stride, nd, e};
+    for (const Rows* r : {&x, &ag, &xg, &dy, &dx, &dag, &dxg})
+      if (r->bytes() < 0) return SSM_ERR_INVALID_ARG;
+    if (!dx.disjoint() || !dag.disjoint() || !dxg.disjoint()) return SSM_ERR_INVALID_ARG;
+    for (const Rows* r : {&x, &ag, &xg, &dy, &dx, &dag, &dxg})
+      if (!aligned(r->p, e)) return SSM_ERR_UNSUPPORTED;
+    if (!aligned(io->A_log, 4) || !aligned(io->valid_len, 4) || !aligned(io->h0, 4) || !aligned(io->dh_last, 4) ||
+        !aligned(io->chunk_states, 4) || !aligned(io->dA_log, 4) || !aligned(io->dh0, 4) || !aligned(io->workspace, 8))
+      return SSM_ERR_UNSUPPORTED;
+    const Rows in[] = {x, ag, xg, dy, flat(io->A_log, nd * 4), flat(io->valid_len, nb * 4), flat(io->h0, nb * nd * 4),
+                       flat(io->dh_last, nb * nd * 4), flat(io->chunk_states, nb * ns * nd * 4)};
+    const Rows out[] = {dx, dag, dxg, flat(io->dA_log, nd * 4), flat(io->dh0, nb * nd * 4),
+                        flat(io->workspace, io->workspace_bytes)};
+    if (any_overlap(in, out)) return SSM_ERR_ALIAS;
+  }
+  const int rc = check_handle(handle);
+  if (rc != SSM_OK || nd == 0) return rc;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  if (!some) {  // sums over nothing; the state's gradient passes through
+    hipLaunchKernelGGL(gated_copy_kernel, dim3(static_cast<unsigned>((nd + 255) / 256)), dim3(256), 0, s, nullptr,
+                       io->dA_log, nd);
+    if (nb > 0 && io->dh0 != nullptr) {
+      const int64_t blocks = (nb * nd + 255) / 256;
+      if (!grid_fits(blocks, 256)) return SSM_ERR_UNSUPPORTED;
+      hipLaunchKernelGGL(gated_copy_kernel, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, s, io->dh_last, io->dh0,
+                         nb * nd);
+    }
+    return launched();
+  }
+  GatedBwdParams p;
+  p.x = io->x, p.ag = io->a_gate, p.xg = io->x_gate, p.A_log = io->A_log, p.valid_len = io->valid_len, p.h0 = io->h0;
+  p.dy = io->dy, p.dh_last = io->dh_last, p.states = io->chunk_states;
+  p.dx = io->dx, p.dag = io->da_gate, p.dxg = io->dx_gate, p.dh0 = io->dh0, p.ws = static_cast<float*>(io->workspace);
+  p.x_bs = io->x_batch_stride, p.x_ts = io->x_time_stride, p.ag_bs = io->a_gate_batch_stride;
+  p.ag_ts = io->a_gate_time_stride, p.xg_bs = io->x_gate_batch_stride, p.xg_ts = io->x_gate_time_stride;
+  p.dy_bs = io->dy_batch_stride, p.dy_ts = io->dy_time_stride, p.dx_bs = io->dx_batch_stride;
+  p.dx_ts = io->dx_time_stride, p.dag_bs = io->da_gate_batch_stride, p.dag_ts = io->da_gate_time_stride;
+  p.dxg_bs = io->dx_gate_batch_stride, p.dxg_ts = io->dx_gate_time_stride;
+  p.L = L, p.nd = static_cast<int32_t>(nd), p.n_states = static_cast<int32_t>(ns);
+  bool fits = true;
+  for_gated(dims, [&]<typename IO, int V>() {
+    p.n_cg = static_cast<int32_t>((nd + 64 * V - 1) / (64 * V));
+    fits = grid_fits(nb * p.n_cg, 64 * kWaves);
+    if (fits)
+      hipLaunchKernelGGL((gated_bwd_kernel<IO, V, kSteps, kWaves>), dim3(static_cast<unsigned>(nb * p.n_cg)),
+                         dim3(64 * kWaves), 0, s, p);
+  });
+  if (!fits) return SSM_ERR_UNSUPPORTED;
+  if (launched() != SSM_OK) return SSM_ERR_HIP;
+  launch_reduce(p.ws, nb, nd, GatedGrads{io->dA_log}, s);
+  return launched();
+}
+
+int ssm_gated_recurrence_step(ssm_scan_t handle, const ssm_gated_dims* dims, const ssm_gated_step_io* io,
+                              void* stream) {
+  const int bad = check_gated_dims(dims);
+  if (bad != SSM_OK) return bad;
+  if (io == nullptr || dims->seqlen != 1 || io->n_slots < 0) return SSM_ERR_INVALID_ARG;
+  const int64_t nb = dims->batch, nd = dims->dim, rows = io->slots == nullptr ? nb : io->n_slots;
+  if (nb > 65535 || rows > kMaxSize) return SSM_ERR_UNSUPPORTED;
+  const int64_t e = dims->io_dtype == SSM_IO_BF16 ? 2 : 4;
+  const bool empty = nb == 0 || nd == 0;
+  if (!empty) {
+    if (io->x == nullptr || io->a_gate == nullptr || io->x_gate == nullptr || io->A_log == nullptr ||
+        io->y == nullptr || (rows > 0 && (io->h0 == nullptr || io->h_last == nullptr)))
+      return SSM_ERR_INVALID_ARG;
+    const Rows x{io->x, nb, io->x_row_stride, 1, 0, nd, e}, ag{io->a_gate, nb, io->a_gate_row_stride, 1, 0, nd, e};
+    const Rows xg{io->x_gate, nb, io->x_gate_row_stride, 1, 0, nd, e}, y{io->y, nb, io->y_row_stride, 1, 0, nd, e};
+    if (x.bytes() < 0 || ag.bytes() < 0 || xg.bytes() < 0 || y.bytes() < 0 || !y.disjoint()) return SSM_ERR_INVALID_ARG;
+    const int64_t bh = span_bytes(rows, nd, 1, 0, nd, 4);
+    if (bh < 0) return SSM_ERR_UNSUPPORTED;
+    if (!aligned(io->x, e) || !aligned(io->a_gate, e) || !aligned(io->x_gate, e) || !aligned(io->y, e) ||
+        !aligned(io->A_log, 4) || !aligned(io->slots, 4) || !aligned(io->h0, 4) || !aligned(io->h_last, 4))
+      return SSM_ERR_UNSUPPORTED;
+    const Rows in[] = {x, ag, xg, flat(io->A_log, nd * 4), flat(io->slots, nb * 4),
+                       flat(io->h0, io->h0 == io->h_last ? 0 : bh)};
+    const Rows out[] = {y, flat(io->h_last, bh)};
+    if (any_overlap(in, out)) return SSM_ERR_ALIAS;
+  }
+  const int rc = check_handle(handle);
+  if (rc != SSM_OK || empty) return rc;
+  GatedStepParams p;
+  p.x = io->x, p.ag = io->a_gate, p.xg = io->x_gate, p.A_log = io->A_log, p.slots = io->slots, p.h0 = io->h0;
+  p.h_last = io->h_last, p.y = io->y, p.x_rs = io->x_row_stride, p.ag_rs = io->a_gate_row_stride;
+  p.xg_rs = io->x_gate_row_stride, p.y_rs = io->y_row_stride, p.n_slots = rows;
+  p.nb = static_cast<int32_t>(nb), p.nd = static_cast<int32_t>(nd);
+  constexpr int V = 4;
+  const dim3 grid(static_cast<unsigned>((nd + 256 * V - 1) / (256 * V)), static_cast<unsigned>(nb));
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  if (dims->io_dtype == SSM_IO_BF16)
+    hipLaunchKernelGGL((gated_step_kernel<uint16_t, V>), grid, dim3(256), 0, s, p);
+  else
+    hipLaunchKernelGGL((gated_step_kernel<float, V>), grid, dim3(256), 0, s, p);
+  return launched();
+}
+
+}  // extern "C"

@@ -25,6 +25,7 @@
 #include <sstream>
 #include <stdexcept>
 #include <string>
+#include <vector>
 
 #include "ssm_scan.h"
 
@@ -42,6 +43,15 @@ struct Entry {
   decltype(&ssm_layer_norm_fwd) norm_fwd;
   decltype(&ssm_layer_norm_bwd) norm_bwd;
   decltype(&ssm_layer_norm_bwd_workspace_bytes) norm_bwd_bytes;
+  decltype(&ssm_gated_recurrence_fwd) gated_fwd;
+  decltype(&ssm_gated_recurrence_fwd_workspace_bytes) gated_fwd_bytes;
+  decltype(&ssm_gated_recurrence_bwd) gated_bwd;
+  decltype(&ssm_gated_recurrence_bwd_workspace_bytes) gated_bwd_bytes;
+  decltype(&ssm_gated_recurrence_chunk_len) gated_chunk_len;
+  decltype(&ssm_gated_recurrence_step) gated_step;
+  decltype(&ssm_group_norm_fwd) group_fwd;
+  decltype(&ssm_group_norm_bwd) group_bwd;
+  decltype(&ssm_group_norm_bwd_workspace_bytes) group_bwd_bytes;
 };
 
 Entry entry;
@@ -511,11 +521,263 @@ PyObject* norm_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// ---- gated recurrence ------------------------------------------------------
+
+struct Gated {
+  Tensor x, ag, xg, A;
+  at::Device dev{at::kCUDA, 0};
+  at::ScalarType dt;
+  ssm_gated_dims dims;
+  const int32_t* valid_len;
+  const float* h0;
+};
+
+// a: x, a_gate, x_gate, A_log, valid_len, h0
+Gated gated_args(PyObject* const* a) {
+  Gated c;
+  c.x = tensor("x", a[0]), c.ag = tensor("a_gate", a[1]), c.xg = tensor("x_gate", a[2]), c.A = tensor("A_log", a[3]);
+  const int32_t io = io_of("x", c.x);
+  want_dims(c.x, 3, "x must be [batch, L, dim]");
+  c.dev = c.x.device(), c.dt = c.x.scalar_type();
+  const int64_t nb = c.x.size(0), L = c.x.size(1), nd = c.x.size(2);
+  rows("x", c.x, {nb, L, nd}, c.dt, c.dev);
+  rows("a_gate", c.ag, {nb, L, nd}, c.dt, c.dev);
+  rows("x_gate", c.xg, {nb, L, nd}, c.dt, c.dev);
+  dense("A_log", c.A, {nd}, at::kFloat, c.dev);
+  c.valid_len = given<int32_t>("valid_len", a[4], {nb}, at::kInt, c.dev);
+  c.h0 = given<float>("h0", a[5], {nb, nd}, at::kFloat, c.dev);
+  c.dims = ssm_gated_dims{nb, L, nd, io};
+  return c;
+}
+
+template <typename IO>
+void gated_inputs(const Gated& c, IO& s) {
+  s.x = c.x.const_data_ptr(), s.a_gate = c.ag.const_data_ptr(), s.x_gate = c.xg.const_data_ptr();
+  s.A_log = static_cast<const float*>(c.A.const_data_ptr()), s.valid_len = c.valid_len, s.h0 = c.h0;
+  s.x_batch_stride = c.x.stride(0), s.x_time_stride = c.x.stride(1);
+  s.a_gate_batch_stride = c.ag.stride(0), s.a_gate_time_stride = c.ag.stride(1);
+  s.x_gate_batch_stride = c.xg.stride(0), s.x_gate_time_stride = c.xg.stride(1);
+}
+
+int64_t gated_chunks(int64_t L) {
+  const int64_t chunk = entry.gated_chunk_len();
+  return (L + chunk - 1) / chunk;
+}
+
+// x, a_gate, x_gate, A_log, valid_len, h0, y, h_last, return_chunk_states, workspace
+PyObject* gated_fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 10, [&]() -> PyObject* {
+    const Gated c = gated_args(a);
+    const int64_t nb = c.dims.batch, L = c.dims.seqlen, nd = c.dims.dim;
+    const Tensor y = output("y", a[6], {nb, L, nd}, c.dt, c.dev, Layout::kRows);
+    const Tensor last = output("h_last", a[7], {nb, nd}, at::kFloat, c.dev, Layout::kDense);
+    const bool keep = flag(a[8]);
+    Tensor states, ws;
+    if (keep) states = fresh({nb, gated_chunks(L), nd}, at::kFloat, c.dev);
+    const int64_t bytes = entry.gated_fwd_bytes(&c.dims);
+    if (bytes != 0 || a[9] != Py_None) ws = scratch(a[9], bytes, c.dev);
+    ssm_gated_fwd_io s{};
+    gated_inputs(c, s);
+    s.y = y.data_ptr(), s.h_last = at_ptr<float>(last), s.chunk_states = at_ptr<float>(states);
+    s.workspace = at_ptr<void>(ws), s.workspace_bytes = ws.defined() ? ws.numel() : 0;
+    s.y_batch_stride = y.stride(0), s.y_time_stride = y.stride(1);
+    call("ssm_gated_recurrence_fwd", entry.gated_fwd, c.dev, c.dims, s);
+    written(a[6], y), written(a[7], last), written(a[9], ws);
+    return keep ? pack<3>({y, last, states}) : pack<2>({y, last});
+  });
+}
+
+// x, a_gate, x_gate, A_log, valid_len, h0, dy, dh_last, chunk_states, dx, da_gate, dx_gate, workspace
+PyObject* gated_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 13, [&]() -> PyObject* {
+    const Gated c = gated_args(a);
+    const int64_t nb = c.dims.batch, L = c.dims.seqlen, nd = c.dims.dim;
+    const Tensor& dy = tensor("dy", a[6]);
+    rows("dy", dy, {nb, L, nd}, c.dt, c.dev);
+    ssm_gated_bwd_io s{};
+    gated_inputs(c, s);
+    s.dh_last = given<float>("dh_last", a[7], {nb, nd}, at::kFloat, c.dev);
+    s.chunk_states = given<float>("chunk_states", a[8], {nb, gated_chunks(L), nd}, at::kFloat, c.dev);
+    const Tensor dx = output("dx", a[9], {nb, L, nd}, c.dt, c.dev, Layout::kRows);
+    const Tensor dag = output("da_gate", a[10], {nb, L, nd}, c.dt, c.dev, Layout::kRows);
+    const Tensor dxg = output("dx_gate", a[11], {nb, L, nd}, c.dt, c.dev, Layout::kRows);
+    const Tensor dA = fresh({nd}, at::kFloat, c.dev);
+    Tensor d0;
+    if (a[5] != Py_None) d0 = fresh({nb, nd}, at::kFloat, c.dev);
+    const Tensor ws = scratch(a[12], entry.gated_bwd_bytes(&c.dims), c.dev);
+    s.dy = dy.const_data_ptr(), s.dx = dx.data_ptr(), s.da_gate = dag.data_ptr(), s.dx_gate = dxg.data_ptr();
+    s.dA_log = at_ptr<float>(dA), s.dh0 = at_ptr<float>(d0);
+    s.workspace = ws.data_ptr(), s.workspace_bytes = ws.numel();
+    s.dy_batch_stride = dy.stride(0), s.dy_time_stride = dy.stride(1);
+    s.dx_batch_stride = dx.stride(0), s.dx_time_stride = dx.stride(1);
+    s.da_gate_batch_stride = dag.stride(0), s.da_gate_time_stride = dag.stride(1);
+    s.dx_gate_batch_stride = dxg.stride(0), s.dx_gate_time_stride = dxg.stride(1);
+    call("ssm_gated_recurrence_bwd", entry.gated_bwd, c.dev, c.dims, s);
+    written(a[9], dx), written(a[10], dag), written(a[11], dxg), written(a[12], ws);
+    return pack<5>({dx, dag, dxg, dA, d0});
+  });
+}
+
+// x, a_gate, x_gate, A_log, h, slots, h_last, y
+PyObject* gated_step(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 8, [&]() -> PyObject* {
+    const Tensor &x = tensor("x", a[0]), &ag = tensor("a_gate", a[1]), &xg = tensor("x_gate", a[2]),
+                 &A = tensor("A_log", a[3]), &h = tensor("h", a[4]);
+    const int32_t io = io_of("x", x);
+    want_dims(x, 2, "x must be [batch, dim]");
+    want_dims(h, 2, "h must be [rows, dim]");
+    const at::Device dev = x.device();
+    const at::ScalarType dt = x.scalar_type();
+    const int64_t nb = x.size(0), nd = x.size(1);
+    rows("x", x, {nb, nd}, dt, dev);
+    rows("a_gate", ag, {nb, nd}, dt, dev);
+    rows("x_gate", xg, {nb, nd}, dt, dev);
+    dense("A_log", A, {nd}, at::kFloat, dev);
+    Cache c;
+    c.from = h, c.rows = a[5] == Py_None ? nb : h.size(0);
+    dense("h", c.from, {c.rows, nd}, at::kFloat, dev);
+    c.to = a[6] == Py_None ? c.from : tensor("h_last", a[6]);
+    if (!c.to.is_same(c.from)) dense("h's output", c.to, {c.rows, nd}, at::kFloat, dev);
+    c.slots = given<int32_t>("slots", a[5], {nb}, at::kInt, dev);
+    const Tensor y = output("y", a[7], {nb, nd}, dt, dev, Layout::kRows);
+    const ssm_gated_dims dims{nb, 1, nd, io};
+    ssm_gated_step_io s{};
+    s.x = x.const_data_ptr(), s.a_gate = ag.const_data_ptr(), s.x_gate = xg.const_data_ptr();
+    s.A_log = static_cast<const float*>(A.const_data_ptr()), s.slots = c.slots;
+    s.h0 = at_ptr<float>(c.from), s.h_last = at_ptr<float>(c.to), s.y = y.data_ptr();
+    s.x_row_stride = x.stride(0), s.a_gate_row_stride = ag.stride(0), s.x_gate_row_stride = xg.stride(0);
+    s.y_row_stride = y.stride(0), s.n_slots = c.rows;
+    call("ssm_gated_recurrence_step", entry.gated_step, dev, dims, s);
+    written(a[4], c.to), written(a[7], y);
+    return wrap(y);
+  });
+}
+
+// ---- group norm ------------------------------------------------------------
+
+struct Group {
+  at::Device dev{at::kCUDA, 0};
+  at::ScalarType dt;
+  Shape shape;
+  std::vector<int64_t> stats;
+  ssm_group_norm_dims dims;
+  const float *w, *bias;
+  const int32_t* valid_len;
+  Tensor z;
+};
+
+// Batch and time strides of rows; those of [rows, dim] are one batch's.
+void row_strides(const Tensor& t, int64_t& batch, int64_t& time) {
+  batch = t.dim() == 3 ? t.stride(0) : 0;
+  time = t.stride(t.dim() == 3 ? 1 : 0);
+}
+
+// x, groups, weight, bias, valid_len, z, silu, gate_first
+Group group_args(const char* name, const Tensor& x, PyObject* groups, PyObject* weight, PyObject* bias,
+                 PyObject* valid_len, PyObject* z, PyObject* silu, PyObject* gate_first) {
+  Group m;
+  const int32_t io = io_of(name, x);
+  if (x.dim() != 2 && x.dim() != 3) throw ValueRefused("rows must be [rows, dim] or [batch, L, dim]");
+  if (valid_len != Py_None && x.dim() != 3) throw ValueRefused("valid_len needs rows laid out as [batch, L, dim]");
+  m.dev = x.device(), m.dt = x.scalar_type(), m.shape = x.sizes();
+  const int64_t nb = x.dim() == 3 ? x.size(0) : 1, L = x.size(x.dim() - 2), nd = x.size(-1);
+  const long long g = PyLong_AsLongLong(groups);
+  if (g == -1 && PyErr_Occurred()) throw Raised();
+  if (g < 1 || nd % g != 0) throw ValueRefused("groups must divide the last dimension");
+  m.stats.assign(m.shape.begin(), m.shape.end());
+  m.stats.back() = g;
+  rows(name, x, m.shape, m.dt, m.dev);
+  const Tensor& w = tensor("weight", weight);
+  dense("weight", w, {nd}, at::kFloat, m.dev);
+  m.w = static_cast<const float*>(w.const_data_ptr());
+  m.bias = given<float>("bias", bias, {nd}, at::kFloat, m.dev);
+  m.valid_len = given<int32_t>("valid_len", valid_len, {nb}, at::kInt, m.dev);
+  int32_t gate = SSM_GATE_NONE;
+  const bool first = flag(gate_first);
+  if (z != Py_None) {
+    m.z = tensor("z", z);
+    rows("z", m.z, m.shape, m.dt, m.dev);
+    gate = first ? SSM_GATE_BEFORE : SSM_GATE_AFTER;
+  } else if (first) {
+    throw ValueRefused("gate_first needs z");
+  }
+  m.dims = ssm_group_norm_dims{nb, L, nd, g, io, 0, flag(silu) ? 1 : 0, gate, 1.0f};
+  return m;
+}
+
+// x, groups, weight, bias, valid_len, z, silu, gate_first, eps, rms, y, return_stats
+PyObject* group_fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 12, [&]() -> PyObject* {
+    const Tensor& x = tensor("x", a[0]);
+    Group m = group_args("x", x, a[1], a[2], a[3], a[4], a[5], a[6], a[7]);
+    m.dims.eps = number(a[8]);
+    m.dims.rms = flag(a[9]) ? 1 : 0;
+    const Tensor y = output("y", a[10], m.shape, m.dt, m.dev, Layout::kRows);
+    Tensor mean, rstd;
+    const bool stats = flag(a[11]);
+    if (stats) {
+      rstd = fresh(m.stats, at::kFloat, m.dev);
+      if (!m.dims.rms) mean = fresh(m.stats, at::kFloat, m.dev);
+    }
+    ssm_group_norm_fwd_io s{};
+    s.x = x.const_data_ptr(), s.weight = m.w, s.bias = m.bias, s.valid_len = m.valid_len, s.y = y.data_ptr();
+    s.mean = at_ptr<float>(mean), s.rstd = at_ptr<float>(rstd);
+    row_strides(x, s.x_batch_stride, s.x_time_stride);
+    row_strides(y, s.y_batch_stride, s.y_time_stride);
+    if (m.z.defined()) {
+      s.z = m.z.const_data_ptr();
+      row_strides(m.z, s.z_batch_stride, s.z_time_stride);
+    }
+    call("ssm_group_norm_fwd", entry.group_fwd, m.dev, m.dims, s);
+    written(a[10], y);
+    return stats ? pack<3>({y, mean, rstd}) : wrap(y);
+  });
+}
+
+// dy, x, groups, weight, bias, mean, rstd, valid_len, z, silu, gate_first, dx, dz, workspace
+PyObject* group_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 14, [&]() -> PyObject* {
+    const Tensor &dy = tensor("dy", a[0]), &x = tensor("x", a[1]);
+    Group m = group_args("x", x, a[2], a[3], a[4], a[7], a[8], a[9], a[10]);
+    rows("dy", dy, m.shape, m.dt, m.dev);
+    ssm_group_norm_bwd_io s{};
+    s.mean = given<float>("mean", a[5], m.stats, at::kFloat, m.dev);
+    const Tensor& rstd = tensor("rstd", a[6]);
+    dense("rstd", rstd, m.stats, at::kFloat, m.dev);
+    m.dims.rms = a[5] == Py_None ? 1 : 0;
+    const Tensor dx = output("dx", a[11], m.shape, m.dt, m.dev, Layout::kRows);
+    Tensor dz, db;
+    if (m.z.defined())
+      dz = output("dz", a[12], m.shape, m.dt, m.dev, Layout::kRows);
+    else if (a[12] != Py_None)
+      throw ValueRefused("dz needs z");
+    const Tensor dw = fresh({m.dims.dim}, at::kFloat, m.dev);
+    if (m.bias != nullptr || a[4] != Py_None) db = fresh({m.dims.dim}, at::kFloat, m.dev);
+    const Tensor ws = scratch(a[13], entry.group_bwd_bytes(&m.dims), m.dev);
+    s.dy = dy.const_data_ptr(), s.x = x.const_data_ptr(), s.weight = m.w, s.bias = m.bias;
+    s.rstd = static_cast<const float*>(rstd.const_data_ptr()), s.valid_len = m.valid_len;
+    s.dx = dx.data_ptr(), s.dz = at_ptr<void>(dz), s.dweight = at_ptr<float>(dw), s.dbias = at_ptr<float>(db);
+    s.workspace = ws.data_ptr(), s.workspace_bytes = ws.numel();
+    row_strides(dy, s.dy_batch_stride, s.dy_time_stride);
+    row_strides(x, s.x_batch_stride, s.x_time_stride);
+    row_strides(dx, s.dx_batch_stride, s.dx_time_stride);
+    if (m.z.defined()) {
+      s.z = m.z.const_data_ptr();
+      row_strides(m.z, s.z_batch_stride, s.z_time_stride);
+      row_strides(dz, s.dz_batch_stride, s.dz_time_stride);
+    }
+    call("ssm_group_norm_bwd", entry.group_bwd, m.dev, m.dims, s);
+    written(a[11], dx), written(a[12], dz), written(a[13], ws);
+    return pack<4>({dx, dz, dw, db});
+  });
+}
+
 // bind(addresses of Entry's functions in its order, handle_for, error class)
 PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  return guarded(n, 10, [&]() -> PyObject* {
-    void* p[8];
-    for (int i = 0; i < 8; ++i) {
+  constexpr int kEntries = 17;
+  return guarded(n, kEntries + 2, [&]() -> PyObject* {
+    void* p[kEntries];
+    for (int i = 0; i < kEntries; ++i) {
       p[i] = PyLong_AsVoidPtr(a[i]);
       if (p[i] == nullptr) {
         if (PyErr_Occurred()) throw Raised();
@@ -530,17 +792,28 @@ PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
     entry.norm_fwd = reinterpret_cast<decltype(entry.norm_fwd)>(p[5]);
     entry.norm_bwd = reinterpret_cast<decltype(entry.norm_bwd)>(p[6]);
     entry.norm_bwd_bytes = reinterpret_cast<decltype(entry.norm_bwd_bytes)>(p[7]);
-    Py_INCREF(a[8]);
-    Py_XSETREF(handle_for, a[8]);
-    Py_INCREF(a[9]);
-    Py_XSETREF(scan_error, a[9]);
+    entry.gated_fwd = reinterpret_cast<decltype(entry.gated_fwd)>(p[8]);
+    entry.gated_fwd_bytes = reinterpret_cast<decltype(entry.gated_fwd_bytes)>(p[9]);
+    entry.gated_bwd = reinterpret_cast<decltype(entry.gated_bwd)>(p[10]);
+    entry.gated_bwd_bytes = reinterpret_cast<decltype(entry.gated_bwd_bytes)>(p[11]);
+    entry.gated_chunk_len = reinterpret_cast<decltype(entry.gated_chunk_len)>(p[12]);
+    entry.gated_step = reinterpret_cast<decltype(entry.gated_step)>(p[13]);
+    entry.group_fwd = reinterpret_cast<decltype(entry.group_fwd)>(p[14]);
+    entry.group_bwd = reinterpret_cast<decltype(entry.group_bwd)>(p[15]);
+    entry.group_bwd_bytes = reinterpret_cast<decltype(entry.group_bwd_bytes)>(p[16]);
+    Py_INCREF(a[kEntries]);
+    Py_XSETREF(handle_for, a[kEntries]);
+    Py_INCREF(a[kEntries + 1]);
+    Py_XSETREF(scan_error, a[kEntries + 1]);
     Py_RETURN_NONE;
   });
 }
 
 #define FAST(name) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(name)), METH_FASTCALL, nullptr}
-PyMethodDef methods[] = {FAST(bind),     FAST(scan_step), FAST(conv_step), FAST(conv_fwd),
-                         FAST(conv_bwd), FAST(norm_fwd),  FAST(norm_bwd),  {nullptr, nullptr, 0, nullptr}};
+PyMethodDef methods[] = {FAST(bind),      FAST(scan_step),  FAST(conv_step), FAST(conv_fwd),
+                         FAST(conv_bwd),  FAST(norm_fwd),   FAST(norm_bwd),  FAST(gated_fwd),
+                         FAST(gated_bwd), FAST(gated_step), FAST(group_fwd), FAST(group_bwd),
+                         {nullptr, nullptr, 0, nullptr}};
 #undef FAST
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_ssm_torch", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
