@@ -154,6 +154,191 @@ __device__ __forceinline__ void join_waves(float (&lds)[W][2 * V][64], int wave,
   for (int v = 0; v < V; ++v) out[v] = h[v], h[v] = mine[v];
 }
 
+// ---- rows cut into tiles ----------------------------------------------------
+//
+// Where (row, channel) work alone does not fill the GPU, tiles of T W steps of one
+// chain (a row's 64 V channels) run on different workgroups.  A tile folds its
+// steps into one pair per channel, needs the state in front of it, and leaves the
+// one behind.  kSpan tiles make a span.  The state goes from span to span, from
+// the last tile of one to all of the next; within a span every tile publishes its
+// pair as soon as its inputs have come, and composes those of the tiles in front
+// of it, in order, behind the span's state.  What a tile computes does not depend
+// on when the others come, so results are the same bits from run to run, and only
+// every kSpan-th tile is a step of the serial chain.
+//
+// Tiles are dealt by a counter, all chains' first tiles first: a tile waits only for
+// tiles with smaller numbers, a workgroup takes its own in order, so the smallest
+// unfinished one is always at work and never waits for one that is not: every wait ends.
+//
+// Published words tell by themselves that they are there: a fill kernel sets all
+// to kEmpty, a NaN that is never published (it is replaced by another), and words
+// are stored and read whole, relaxed, at agent scope.
+
+constexpr int kSpan = 16;
+constexpr uint32_t kEmpty = 0xffffffffu;
+// Far more polls than any wait takes: should one end here all the same, the
+// states that hang on it become NaN.
+constexpr int kPolls = 1 << 21;
+
+template <int V>
+struct Words;
+template <>
+struct Words<1> {
+  typedef uint32_t type;
+};
+template <>
+struct Words<2> {
+  typedef unsigned long long type;
+};
+
+template <int V>
+__device__ __forceinline__ void publish(float* at, const float (&v)[V]) {
+  typedef typename Words<V>::type W;
+  W w = 0;
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const uint32_t u = __builtin_bit_cast(uint32_t, v[i]);
+    w |= static_cast<W>(u == kEmpty ? 0x7fc00000u : u) << (i * 32 % (8 * sizeof(W)));
+  }
+  __hip_atomic_store(reinterpret_cast<W*>(at), w, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
+// K published vectors, once all of them are there.
+template <int V, int K>
+__device__ __forceinline__ void await(const float* const (&at)[K], float (&v)[K][V]) {
+  typedef typename Words<V>::type W;
+  for (int polls = 0;; ++polls) {
+    bool there = true;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const W w = __hip_atomic_load(reinterpret_cast<const W*>(at[k]), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const uint32_t u = static_cast<uint32_t>(w >> (i * 32 % (8 * sizeof(W))));
+        there = there && u != kEmpty;
+        v[k][i] = __builtin_bit_cast(float, u);
+      }
+    }
+    if (__all(there) || polls == kPolls) return;  // kEmpty itself is a NaN
+    __builtin_amdgcn_s_sleep(1);
+  }
+}
+
+// A product of decays that underflowed would make NaN of an infinite state.
+__device__ __forceinline__ float above_zero(float p) { return __builtin_fmaxf(p, 0x1p-149f); }
+
+// The chains' workspace: a counter, then the tiles' pairs and the spans' states.
+struct ChainSpace {
+  uint32_t* counter;
+  float* pairs;   // [tile][chain][P, S][64 V]
+  float* states;  // [span][chain][64 V]
+  uint32_t chains;
+  template <int V>
+  __device__ __forceinline__ float* pair(uint32_t pos, uint32_t chain) const {
+    return pairs + ((static_cast<int64_t>(pos) * chains + chain) * 2 * 64 + threadIdx.x % 64) * V;
+  }
+  template <int V>
+  __device__ __forceinline__ float* state(uint32_t span, uint32_t chain) const {
+    return states + ((static_cast<int64_t>(span) * chains + chain) * 64 + threadIdx.x % 64) * V;
+  }
+};
+
+// LDS of the waves of a tile, and of the tiles in front of it.
+template <int V, int W>
+struct ChainLds {
+  float waves[2][W][2 * V][64];
+  float front[kSpan][2 * V][64];
+  float state[V][64];
+  uint32_t ticket;
+};
+
+// From a wave's pair (P, S) to the state `h` in front of the wave's steps and `out`,
+// the one behind the tile.  Called with the chain's initial state for its first
+// tile, which takes it into its pair, and zero for the others.  pos: the tile's
+// place in its chain; more: whether another follows.  `next` becomes the ticket
+// that thread 0 drew.
+template <int V, int W, bool REVERSE>
+__device__ __forceinline__ void join_chain(ChainLds<V, W>& lds, const ChainSpace& sp, int buf, int wave, uint32_t pos,
+                                           uint32_t chain, bool more, const float (&P)[V], const float (&S)[V],
+                                           float (&h)[V], float (&out)[V], uint32_t& next) {
+  const int lane = threadIdx.x % 64;
+  auto& mine = lds.waves[buf];
+#pragma unroll
+  for (int v = 0; v < V; ++v) asm volatile("" : "+v"(h[v]));  // the initial state has come before one is written
+#pragma unroll
+  for (int v = 0; v < V; ++v) mine[wave][v][lane] = above_zero(P[v]), mine[wave][V + v][lane] = S[v];
+  __syncthreads();
+  const uint32_t span = pos / kSpan;
+  const int before = static_cast<int>(pos % kSpan);  // tiles of the span in front of this one
+  if (wave == W - 1 && more && before != kSpan - 1) {
+    float p[V], s[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) p[v] = 1.0f, s[v] = h[v];
+#pragma unroll
+    for (int k = 0; k < W; ++k) {
+      const int w = REVERSE ? W - 1 - k : k;
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const float a = mine[w][v][lane];
+        s[v] = __builtin_fmaf(a, s[v], mine[w][V + v][lane]);
+        p[v] *= a;
+      }
+    }
+#pragma unroll
+    for (int v = 0; v < V; ++v) p[v] = above_zero(p[v]);
+    float* at = sp.pair<V>(pos, chain);
+    publish<V>(at, p);
+    publish<V>(at + 64 * V, s);
+  }
+  for (int j = wave; j <= before; j += W) {
+    if (j < before) {
+      const float* at = sp.pair<V>(span * kSpan + j, chain);
+      const float* const two[2] = {at, at + 64 * V};
+      float v2[2][V];
+      await<V, 2>(two, v2);
+#pragma unroll
+      for (int v = 0; v < V; ++v) lds.front[j][v][lane] = v2[0][v], lds.front[j][V + v][lane] = v2[1][v];
+    } else if (span > 0) {
+      const float* const one[1] = {sp.state<V>(span, chain)};
+      float v1[1][V];
+      await<V, 1>(one, v1);
+#pragma unroll
+      for (int v = 0; v < V; ++v) lds.state[v][lane] = v1[0][v];
+    }
+  }
+  if (threadIdx.x == 0) lds.ticket = next;
+  __syncthreads();
+  next = lds.ticket;
+  if (span > 0) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) h[v] = lds.state[v][lane];
+  }
+  for (int j = 0; j < before; ++j) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) h[v] = __builtin_fmaf(lds.front[j][v][lane], h[v], lds.front[j][V + v][lane]);
+  }
+  float own[V];
+#pragma unroll
+  for (int k = 0; k < W; ++k) {
+    const int w = REVERSE ? W - 1 - k : k;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      if (w == wave) own[v] = h[v];
+      h[v] = __builtin_fmaf(mine[w][v][lane], h[v], mine[w][V + v][lane]);
+    }
+  }
+  if (wave == 0 && more && before == kSpan - 1) publish<V>(sp.state<V>(span + 1, chain), h);
+#pragma unroll
+  for (int v = 0; v < V; ++v) out[v] = h[v], h[v] = own[v];
+}
+
+__global__ void chain_fill_kernel(uint32_t* p, int64_t n) {
+  typedef uint32_t vec4 __attribute__((ext_vector_type(4), aligned(8)));
+  const int64_t i = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * 4;
+  // the first 16 bytes are the counter's
+  if (i < n) *reinterpret_cast<vec4*>(p + i) = i == 0 ? vec4(0u) : vec4(kEmpty);
+}
+
 // A workgroup takes 64 V channels of one row and walks their steps, W waves of T
 // steps side by side.  Lanes past the last channel repeat the last V of the row
 // (which a lane whose V would reach past it takes too: both compute and write
@@ -230,6 +415,97 @@ __global__ __launch_bounds__(64 * W) void gated_fwd_kernel(const GatedParams prm
   if (prm.states != nullptr)
     for (int32_t c = tile / kChunk + wave; c < prm.n_states; c += W)
       VecIO<float>::store(prm.states + (static_cast<int64_t>(b) * prm.n_states + c) * prm.nd + d, h);
+}
+
+// The same with the row's tiles on different workgroups.
+template <typename IO, int V, int T, int W>
+__global__ __launch_bounds__(64 * W) void gated_fwd_chain_kernel(const GatedParams prm, const ChainSpace sp,
+                                                                 uint32_t tickets) {
+  __shared__ ChainLds<V, W> lds;
+  const int wave = wave_index(), lane = threadIdx.x % 64;
+  uint32_t next = 0;
+  if (threadIdx.x == 0) lds.ticket = atomicAdd(sp.counter, 1u);
+  __syncthreads();
+  uint32_t ticket = __builtin_amdgcn_readfirstlane(lds.ticket);
+  __syncthreads();
+  for (int buf = 0; ticket < tickets; ticket = __builtin_amdgcn_readfirstlane(next)) {
+    if (threadIdx.x == 0) next = atomicAdd(sp.counter, 1u);
+    const uint32_t pos = ticket / sp.chains, chain = ticket - pos * sp.chains;
+    const int32_t b = chain / prm.n_cg, cg = chain % prm.n_cg, tile = pos * (T * W), t0 = tile + wave * T;
+    const int32_t first = (cg * 64 + lane) * V, d = first < prm.nd - V ? first : prm.nd - V;
+    const bool mine = first < prm.nd;
+    const int32_t n = length_of(prm.valid_len, b, prm.L);
+    const int64_t bd = static_cast<int64_t>(b) * prm.nd + d;
+    IO* y = static_cast<IO*>(prm.y) + b * prm.y_bs;
+    float h[V] = {}, out[V];
+    if (pos == 0 && prm.h0 != nullptr) VecIO<float>::load(prm.h0 + bd, h);
+    if (tile < n) {
+      const IO* x = static_cast<const IO*>(prm.x) + b * prm.x_bs;
+      const IO* ag = static_cast<const IO*>(prm.ag) + b * prm.ag_bs;
+      const IO* xg = static_cast<const IO*>(prm.xg) + b * prm.xg_bs;
+      float rate2[V], a[T][V], u[T][V], P[V], S[V];
+      Steps<IO, V, T> sx, sa, sg;
+      sa.load(ag, prm.ag_ts, t0, n - 1, d);
+      sg.load(xg, prm.xg_ts, t0, n - 1, d);
+      sx.load(x, prm.x_ts, t0, n - 1, d);
+#pragma unroll
+      for (int v = 0; v < V; ++v) rate2[v] = expf(prm.A_log[d + v]) * kLog2e, P[v] = 1.0f, S[v] = 0.0f;
+#pragma unroll
+      for (int t = 0; t < T; ++t) {
+        float xv[V], av[V], gv[V];
+        sx.raw[t].unpack(xv);
+        sa.raw[t].unpack(av);
+        sg.raw[t].unpack(gv);
+        const bool valid = t0 + t < n;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          const Gate g = gate_of<IO>(av[v], gv[v], rate2[v]);
+          a[t][v] = valid ? g.a : 1.0f;
+          u[t][v] = valid ? g.c * g.i * xv[v] : 0.0f;
+          P[v] *= a[t][v];
+          S[v] = __builtin_fmaf(a[t][v], S[v], u[t][v]);
+        }
+      }
+      join_chain<V, W, false>(lds, sp, buf, wave, pos, chain, tile + T * W < n, P, S, h, out, next);
+      buf ^= 1;
+#pragma unroll
+      for (int t = 0; t < T; ++t) {
+        const bool valid = t0 + t < n;
+        float o[V];
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          h[v] = __builtin_fmaf(a[t][v], h[v], u[t][v]);
+          o[v] = valid ? h[v] : 0.0f;
+        }
+        if (mine && t0 + t < prm.L) VecIO<IO>::store(y + (t0 + t) * prm.y_ts + d, o);
+      }
+      if (prm.states != nullptr && mine && (t0 + T) % kChunk == 0 && (t0 + T) / kChunk <= prm.n_states)
+        VecIO<float>::store(prm.states + (static_cast<int64_t>(b) * prm.n_states + (t0 + T) / kChunk - 1) * prm.nd + d, h);
+    } else {
+#pragma unroll
+      for (int v = 0; v < V; ++v) out[v] = h[v];
+      if (mine) {
+        const int32_t end = tile + T * W < prm.L ? tile + T * W : static_cast<int32_t>(prm.L);
+        for (int32_t t = t0; t < t0 + T && t < end; ++t) {
+          const float zero[V] = {};
+          VecIO<IO>::store(y + t * prm.y_ts + d, zero);
+        }
+      }
+      if (threadIdx.x == 0) lds.ticket = next;
+      __syncthreads();
+      next = lds.ticket;
+      __syncthreads();
+    }
+    // the row's last tile (its first where it has no step) leaves the state
+    if (mine && (tile < n ? tile + T * W >= n : tile == 0)) {
+      if (wave == 0 && prm.h_last != nullptr) VecIO<float>::store(prm.h_last + bd, out);
+      if (prm.states != nullptr) {
+        const int32_t c0 = tile < n ? (tile + T * W) / kChunk : 0;
+        for (int32_t c = c0 + wave; c < prm.n_states; c += W)
+          VecIO<float>::store(prm.states + (static_cast<int64_t>(b) * prm.n_states + c) * prm.nd + d, out);
+      }
+    }
+  }
 }
 
 // The same from the row's end.  A tile's states come again from the kept one in
@@ -447,7 +723,39 @@ void for_gated(const ssm_gated_dims* dims, const F& f) {
     narrow ? f.template operator()<float, 1>() : f.template operator()<float, 2>();
 }
 
-constexpr int kSteps = 8, kWaves = 8;
+constexpr int kSteps = 8, kWaves = 8;          // of the kernels that walk
+constexpr int kFwdSteps = 16;                   // of the one whose workgroups share a row
+
+// How a row's steps are cut up, and the workspace that takes.
+struct Cut {
+  int64_t tiles, chains, tickets, words;
+  bool shared;
+};
+Cut cut_of(const ssm_gated_dims* dims, int64_t steps, int64_t V) {
+  Cut c;
+  c.tiles = (dims->seqlen + steps - 1) / steps;
+  c.chains = dims->batch * ((dims->dim + 64 * V - 1) / (64 * V));
+  c.tickets = c.tiles * c.chains;
+  c.shared = c.tiles >= 2 && c.tickets < (1 << 30);
+  c.words = c.shared ? 4 + 64 * V * c.chains * (2 * c.tiles + c.tiles / kSpan + 1) : 0;
+  return c;
+}
+Cut fwd_cut(const ssm_gated_dims* dims) {
+  return cut_of(dims, kFwdSteps * kWaves, dims->dim <= kNarrow ? 1 : 2);
+}
+
+ChainSpace chain_space(void* workspace, const Cut& c, int64_t V) {
+  ChainSpace sp;
+  sp.counter = static_cast<uint32_t*>(workspace);
+  sp.pairs = static_cast<float*>(workspace) + 4;
+  sp.states = sp.pairs + 2 * 64 * V * c.chains * c.tiles;
+  sp.chains = static_cast<uint32_t>(c.chains);
+  return sp;
+}
+void launch_fill(void* workspace, const Cut& c, hipStream_t s) {
+  hipLaunchKernelGGL(chain_fill_kernel, dim3(static_cast<unsigned>((c.words / 4 + 255) / 256)), dim3(256), 0, s,
+                     static_cast<uint32_t*>(workspace), c.words);
+}
 
 }  // namespace
 
@@ -457,7 +765,7 @@ int64_t ssm_gated_recurrence_chunk_len(void) { return kChunk; }
 
 int64_t ssm_gated_recurrence_fwd_workspace_bytes(const ssm_gated_dims* dims) {
   if (check_gated_dims(dims) != SSM_OK) return -1;
-  return 0;
+  return fwd_cut(dims).words * 4;
 }
 
 int ssm_gated_recurrence_fwd(ssm_scan_t handle, const ssm_gated_dims* dims, const ssm_gated_fwd_io* io, void* stream) {
@@ -509,8 +817,18 @@ int ssm_gated_recurrence_fwd(ssm_scan_t handle, const ssm_gated_dims* dims, cons
   p.y_bs = io->y_batch_stride, p.y_ts = io->y_time_stride;
   p.L = L, p.nd = static_cast<int32_t>(nd), p.n_states = static_cast<int32_t>(ns);
   bool fits = true;
+  const Cut cut = fwd_cut(dims);
+  if (cut.shared) launch_fill(io->workspace, cut, s);
   for_gated(dims, [&]<typename IO, int V>() {
     p.n_cg = static_cast<int32_t>((nd + 64 * V - 1) / (64 * V));
+    if (cut.shared) {
+      const int64_t resident = 2 * handle->cu_count;
+      hipLaunchKernelGGL((gated_fwd_chain_kernel<IO, V, kFwdSteps, kWaves>),
+                         dim3(static_cast<unsigned>(cut.tickets < resident ? cut.tickets : resident)),
+                         dim3(64 * kWaves), 0, s, p, chain_space(io->workspace, cut, V),
+                         static_cast<uint32_t>(cut.tickets));
+      return;
+    }
     fits = grid_fits(nb * p.n_cg, 64 * kWaves);
     if (fits)
       hipLaunchKernelGGL((gated_fwd_kernel<IO, V, kSteps, kWaves>), dim3(static_cast<unsigned>(nb * p.n_cg)),
