@@ -104,6 +104,21 @@ __device__ __forceinline__ Gate gate_of(float ag, float xg, float rate2) {
   return g;
 }
 
+// What the backward makes of a decay and its exponent: c, s a, and s a^2 / c, both
+// of which go to 0 with s and, where a is 0, for large s.
+struct Back {
+  float c, sa, ratio;
+};
+__device__ __forceinline__ Back back_of(float a, float s) {
+  Back b;
+  const float c2 = one_minus_square(a, 2.0f * s);
+  const float rc = c2 > 0.0f ? __builtin_amdgcn_rsqf(c2) : 0.0f;
+  b.c = c2 * rc;
+  b.sa = a > 0.0f ? s * a : 0.0f;
+  b.ratio = b.sa * a * rc;
+  return b;
+}
+
 __device__ __forceinline__ int32_t length_of(const int32_t* valid_len, int32_t b, int64_t L) {
   if (valid_len == nullptr) return static_cast<int32_t>(L);
   const int32_t n = valid_len[b];
@@ -112,15 +127,20 @@ __device__ __forceinline__ int32_t length_of(const int32_t* valid_len, int32_t b
 
 __device__ __forceinline__ int wave_index() { return __builtin_amdgcn_readfirstlane(threadIdx.x / 64); }
 
-// V channels of T steps as they stand in memory.  Steps past the last one read
-// it again (their values are not used).
+// V channels of T steps as they stand in memory.  Unless all of them are steps of
+// the row (FULL), those past the last one read it again (their values are not
+// used).
 template <typename IO, int V, int T>
 struct Steps {
   RawVec<IO, V> raw[T];
+  template <bool FULL>
   __device__ __forceinline__ void load(const void* base, int64_t ts, int32_t t0, int32_t last, int32_t d) {
-    const IO* p = static_cast<const IO*>(base);
+    const IO* p = static_cast<const IO*>(base) + (FULL || t0 < last ? t0 : last) * ts;  // the same for the wave
 #pragma unroll
-    for (int t = 0; t < T; ++t) raw[t].load(p + (t0 + t < last ? t0 + t : last) * ts + d);
+    for (int t = 0; t < T; ++t) {
+      raw[t].load(p + d);
+      p += FULL || t0 + t < last ? ts : 0;
+    }
   }
 };
 
@@ -152,6 +172,16 @@ __device__ __forceinline__ void join_waves(float (&lds)[W][2 * V][64], int wave,
   }
 #pragma unroll
   for (int v = 0; v < V; ++v) out[v] = h[v], h[v] = mine[v];
+}
+
+// A kernel's parameters, read again where they are used: held in scalar registers
+// from turn to turn, some fifty pointers and strides were spilled to vector ones.
+// The parameters are the kernel's first argument.
+template <typename P>
+__device__ __forceinline__ const __attribute__((address_space(4))) P& params_again() {
+  auto p = (const __attribute__((address_space(4))) P*)__builtin_amdgcn_kernarg_segment_ptr();
+  asm volatile("" : "+s"(p));
+  return *p;
 }
 
 // ---- rows cut into tiles ----------------------------------------------------
@@ -360,13 +390,14 @@ __global__ __launch_bounds__(64 * W) void gated_fwd_kernel(const GatedParams prm
   for (int v = 0; v < V; ++v) rate2[v] = expf(prm.A_log[d + v]) * kLog2e;
   if (prm.h0 != nullptr) VecIO<float>::load(prm.h0 + static_cast<int64_t>(b) * prm.nd + d, h);
   int32_t tile = 0;
+  constexpr bool FULL = false;
   for (; tile < n; tile += T * W) {
     const int32_t t0 = tile + wave * T;
     float a[T][V], u[T][V], P[V], S[V], out[V];
     Steps<IO, V, T> sx, sa, sg;
-    sx.load(x, prm.x_ts, t0, n - 1, d);
-    sa.load(ag, prm.ag_ts, t0, n - 1, d);
-    sg.load(xg, prm.xg_ts, t0, n - 1, d);
+    sx.template load<FULL>(x, prm.x_ts, t0, n - 1, d);
+    sa.template load<FULL>(ag, prm.ag_ts, t0, n - 1, d);
+    sg.template load<FULL>(xg, prm.xg_ts, t0, n - 1, d);
 #pragma unroll
     for (int v = 0; v < V; ++v) P[v] = 1.0f, S[v] = 0.0f;
 #pragma unroll
@@ -419,7 +450,7 @@ __global__ __launch_bounds__(64 * W) void gated_fwd_kernel(const GatedParams prm
 
 // The same with the row's tiles on different workgroups.
 template <typename IO, int V, int T, int W>
-__global__ __launch_bounds__(64 * W) void gated_fwd_chain_kernel(const GatedParams prm, const ChainSpace sp,
+__global__ __launch_bounds__(64 * W, 4) void gated_fwd_chain_kernel(const GatedParams, const ChainSpace sp,
                                                                  uint32_t tickets) {
   __shared__ ChainLds<V, W> lds;
   const int wave = wave_index(), lane = threadIdx.x % 64;
@@ -430,24 +461,24 @@ __global__ __launch_bounds__(64 * W) void gated_fwd_chain_kernel(const GatedPara
   __syncthreads();
   for (int buf = 0; ticket < tickets; ticket = __builtin_amdgcn_readfirstlane(next)) {
     if (threadIdx.x == 0) next = atomicAdd(sp.counter, 1u);
+    const auto& prm = params_again<GatedParams>();
     const uint32_t pos = ticket / sp.chains, chain = ticket - pos * sp.chains;
     const int32_t b = chain / prm.n_cg, cg = chain % prm.n_cg, tile = pos * (T * W), t0 = tile + wave * T;
     const int32_t first = (cg * 64 + lane) * V, d = first < prm.nd - V ? first : prm.nd - V;
     const bool mine = first < prm.nd;
     const int32_t n = length_of(prm.valid_len, b, prm.L);
     const int64_t bd = static_cast<int64_t>(b) * prm.nd + d;
-    IO* y = static_cast<IO*>(prm.y) + b * prm.y_bs;
     float h[V] = {}, out[V];
     if (pos == 0 && prm.h0 != nullptr) VecIO<float>::load(prm.h0 + bd, h);
-    if (tile < n) {
+    const auto body = [&]<bool FULL>() __attribute__((always_inline)) {
       const IO* x = static_cast<const IO*>(prm.x) + b * prm.x_bs;
       const IO* ag = static_cast<const IO*>(prm.ag) + b * prm.ag_bs;
       const IO* xg = static_cast<const IO*>(prm.xg) + b * prm.xg_bs;
       float rate2[V], a[T][V], u[T][V], P[V], S[V];
       Steps<IO, V, T> sx, sa, sg;
-      sa.load(ag, prm.ag_ts, t0, n - 1, d);
-      sg.load(xg, prm.xg_ts, t0, n - 1, d);
-      sx.load(x, prm.x_ts, t0, n - 1, d);
+      sa.template load<FULL>(ag, prm.ag_ts, t0, n - 1, d);
+      sg.template load<FULL>(xg, prm.xg_ts, t0, n - 1, d);
+      sx.template load<FULL>(x, prm.x_ts, t0, n - 1, d);
 #pragma unroll
       for (int v = 0; v < V; ++v) rate2[v] = expf(prm.A_log[d + v]) * kLog2e, P[v] = 1.0f, S[v] = 0.0f;
 #pragma unroll
@@ -456,7 +487,7 @@ __global__ __launch_bounds__(64 * W) void gated_fwd_chain_kernel(const GatedPara
         sx.raw[t].unpack(xv);
         sa.raw[t].unpack(av);
         sg.raw[t].unpack(gv);
-        const bool valid = t0 + t < n;
+        const bool valid = FULL || t0 + t < n;
 #pragma unroll
         for (int v = 0; v < V; ++v) {
           const Gate g = gate_of<IO>(av[v], gv[v], rate2[v]);
@@ -468,23 +499,32 @@ __global__ __launch_bounds__(64 * W) void gated_fwd_chain_kernel(const GatedPara
       }
       join_chain<V, W, false>(lds, sp, buf, wave, pos, chain, tile + T * W < n, P, S, h, out, next);
       buf ^= 1;
+      const auto& prm = params_again<GatedParams>();
+      IO* y = static_cast<IO*>(prm.y) + b * prm.y_bs + t0 * prm.y_ts;
 #pragma unroll
       for (int t = 0; t < T; ++t) {
-        const bool valid = t0 + t < n;
+        const bool valid = FULL || t0 + t < n;
         float o[V];
 #pragma unroll
         for (int v = 0; v < V; ++v) {
           h[v] = __builtin_fmaf(a[t][v], h[v], u[t][v]);
           o[v] = valid ? h[v] : 0.0f;
         }
-        if (mine && t0 + t < prm.L) VecIO<IO>::store(y + (t0 + t) * prm.y_ts + d, o);
+        if (mine && (FULL || t0 + t < prm.L)) VecIO<IO>::store(y + d, o);
+        y += prm.y_ts;
       }
       if (prm.states != nullptr && mine && (t0 + T) % kChunk == 0 && (t0 + T) / kChunk <= prm.n_states)
         VecIO<float>::store(prm.states + (static_cast<int64_t>(b) * prm.n_states + (t0 + T) / kChunk - 1) * prm.nd + d, h);
+    };
+    if (tile + T * W <= n) {
+      body.template operator()<true>();
+    } else if (tile < n) {
+      body.template operator()<false>();
     } else {
 #pragma unroll
       for (int v = 0; v < V; ++v) out[v] = h[v];
       if (mine) {
+        IO* y = static_cast<IO*>(prm.y) + b * prm.y_bs;
         const int32_t end = tile + T * W < prm.L ? tile + T * W : static_cast<int32_t>(prm.L);
         for (int32_t t = t0; t < t0 + T && t < end; ++t) {
           const float zero[V] = {};
@@ -496,13 +536,14 @@ __global__ __launch_bounds__(64 * W) void gated_fwd_chain_kernel(const GatedPara
       next = lds.ticket;
       __syncthreads();
     }
+    const auto& end = params_again<GatedParams>();
     // the row's last tile (its first where it has no step) leaves the state
     if (mine && (tile < n ? tile + T * W >= n : tile == 0)) {
-      if (wave == 0 && prm.h_last != nullptr) VecIO<float>::store(prm.h_last + bd, out);
-      if (prm.states != nullptr) {
+      if (wave == 0 && end.h_last != nullptr) VecIO<float>::store(end.h_last + bd, out);
+      if (end.states != nullptr) {
         const int32_t c0 = tile < n ? (tile + T * W) / kChunk : 0;
-        for (int32_t c = c0 + wave; c < prm.n_states; c += W)
-          VecIO<float>::store(prm.states + (static_cast<int64_t>(b) * prm.n_states + c) * prm.nd + d, out);
+        for (int32_t c = c0 + wave; c < end.n_states; c += W)
+          VecIO<float>::store(end.states + (static_cast<int64_t>(b) * end.n_states + c) * end.nd + d, out);
       }
     }
   }
@@ -532,14 +573,15 @@ __global__ __launch_bounds__(64 * W) void gated_bwd_kernel(const GatedBwdParams 
   for (int v = 0; v < V; ++v) rate2[v] = expf(prm.A_log[d + v]) * kLog2e;
   if (prm.dh_last != nullptr) VecIO<float>::load(prm.dh_last + bd, g);
   const int32_t tiles = (n + T * W - 1) / (T * W);
-  for (int32_t k = tiles - 1; k >= 0; --k) {
-    const int32_t tile = k * T * W, t0 = tile + wave * T;
+  constexpr bool FULL = false;
+  for (int32_t at = tiles - 1; at >= 0; --at) {
+    const int32_t tile = at * T * W, t0 = tile + wave * T;
     float a[T][V], hp[T][V], P[V], S[V], h[V] = {}, out[V];
     Steps<IO, V, T> sx, sa, sg, sd;
-    sx.load(x, prm.x_ts, t0, n - 1, d);
-    sa.load(ag, prm.ag_ts, t0, n - 1, d);
-    sg.load(xg, prm.xg_ts, t0, n - 1, d);
-    sd.load(dy, prm.dy_ts, t0, n - 1, d);
+    sx.template load<FULL>(x, prm.x_ts, t0, n - 1, d);
+    sa.template load<FULL>(ag, prm.ag_ts, t0, n - 1, d);
+    sg.template load<FULL>(xg, prm.xg_ts, t0, n - 1, d);
+    sd.template load<FULL>(dy, prm.dy_ts, t0, n - 1, d);
     if (tile > 0)
       VecIO<float>::load(prm.states + (static_cast<int64_t>(b) * prm.n_states + tile / kChunk - 1) * prm.nd + d, h);
     else if (prm.h0 != nullptr)
@@ -598,13 +640,11 @@ __global__ __launch_bounds__(64 * W) void gated_bwd_kernel(const GatedBwdParams 
 #pragma unroll
       for (int v = 0; v < V; ++v) {
         const Gate q = gate_of<IO>(av[v], gv[v], rate2[v]);
+        const Back k = back_of(q.a, q.s);
         const float gt = g[v] + dv[v], gi = gt * q.i, gx = gi * xv[v];
-        // s a -> 0 for large s too, where a is 0
-        const float sa = q.a > 0.0f ? q.s * q.a : 0.0f;
-        const float ratio = q.c > 0.0f ? sa * q.a * __builtin_amdgcn_rcpf(q.c) : 0.0f;
-        const float p = ratio * gx - sa * gt * hp[t][v];
-        ox[v] = valid ? gi * q.c : 0.0f;
-        og[v] = valid ? gx * q.c * (1.0f - q.i) : 0.0f;
+        const float p = k.ratio * gx - k.sa * gt * hp[t][v];
+        ox[v] = valid ? gi * k.c : 0.0f;
+        og[v] = valid ? gx * k.c * (1.0f - q.i) : 0.0f;
         oa[v] = valid ? p * (1.0f - q.r) : 0.0f;
         dA[v] += valid ? p : 0.0f;
         g[v] = valid ? gt * a[t][v] : g[v];
@@ -637,6 +677,163 @@ __global__ __launch_bounds__(64 * W) void gated_bwd_kernel(const GatedBwdParams 
     for (int v = 0; v < V; ++v)
       for (int w = 1; w < W; ++w) dA[v] += lds[w][v][lane];
     VecIO<float>::store(prm.ws + bd, dA);
+  }
+}
+
+// The same with the row's tiles on different workgroups, the last ones first.  What
+// a step needs of the forward pass comes from its own tile alone; the chain carries
+// the state's gradient.  A wave's product of decays is one for both directions.
+template <typename IO, int V, int T, int W>
+__global__ __launch_bounds__(64 * W) void gated_bwd_chain_kernel(const GatedBwdParams, const ChainSpace sp,
+                                                                 uint32_t tickets, uint32_t tiles) {
+  static_assert(T * W % kChunk == 0, "a tile begins behind a kept state");
+  __shared__ ChainLds<V, W> lds;
+  __shared__ float sums[2][W][V][64], dsum[W][V][64];
+  const int wave = wave_index(), lane = threadIdx.x % 64;
+  uint32_t next = 0;
+  if (threadIdx.x == 0) lds.ticket = atomicAdd(sp.counter, 1u);
+  __syncthreads();
+  uint32_t ticket = __builtin_amdgcn_readfirstlane(lds.ticket);
+  __syncthreads();
+  for (int buf = 0; ticket < tickets; ticket = __builtin_amdgcn_readfirstlane(next)) {
+    if (threadIdx.x == 0) next = atomicAdd(sp.counter, 1u);
+    const auto& prm = params_again<GatedBwdParams>();
+    const uint32_t turn = ticket / sp.chains, chain = ticket - turn * sp.chains, k = tiles - 1 - turn;
+    const int32_t b = chain / prm.n_cg, cg = chain % prm.n_cg, tile = k * (T * W), t0 = tile + wave * T;
+    const int32_t first = (cg * 64 + lane) * V, d = first < prm.nd - V ? first : prm.nd - V;
+    const bool mine = first < prm.nd;
+    const int32_t n = length_of(prm.valid_len, b, prm.L);
+    const int64_t bd = static_cast<int64_t>(b) * prm.nd + d;
+    const uint32_t pos = (n + T * W - 1) / (T * W) - 1 - k;  // from the row's last tile with a step
+    float g[V] = {}, out[V], dA[V] = {};
+    if ((tile < n ? pos == 0 : k == 0) && prm.dh_last != nullptr) VecIO<float>::load(prm.dh_last + bd, g);
+    const auto body = [&]<bool FULL>() __attribute__((always_inline)) {
+      const IO* x = static_cast<const IO*>(prm.x) + b * prm.x_bs;
+      const IO* ag = static_cast<const IO*>(prm.ag) + b * prm.ag_bs;
+      const IO* xg = static_cast<const IO*>(prm.xg) + b * prm.xg_bs;
+      const IO* dy = static_cast<const IO*>(prm.dy) + b * prm.dy_bs;
+      float rate2[V], r[T][V], i[T][V], a[T][V], hp[T][V], P[V], S[V], h[V] = {};
+      Steps<IO, V, T> sx, sa, sg, sd;
+      sa.template load<FULL>(ag, prm.ag_ts, t0, n - 1, d);
+      sg.template load<FULL>(xg, prm.xg_ts, t0, n - 1, d);
+      sx.template load<FULL>(x, prm.x_ts, t0, n - 1, d);
+      sd.template load<FULL>(dy, prm.dy_ts, t0, n - 1, d);
+      if (tile > 0)
+        VecIO<float>::load(prm.states + (static_cast<int64_t>(b) * prm.n_states + tile / kChunk - 1) * prm.nd + d, h);
+      else if (prm.h0 != nullptr)
+        VecIO<float>::load(prm.h0 + bd, h);
+#pragma unroll
+      for (int v = 0; v < V; ++v) rate2[v] = expf(prm.A_log[d + v]) * kLog2e, P[v] = 1.0f, S[v] = 0.0f;
+#pragma unroll
+      for (int t = 0; t < T; ++t) {
+        float xv[V], av[V], gv[V];
+        sx.raw[t].unpack(xv);
+        sa.raw[t].unpack(av);
+        sg.raw[t].unpack(gv);
+        const bool valid = FULL || t0 + t < n;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          const Gate q = gate_of<IO>(av[v], gv[v], rate2[v]);
+          r[t][v] = q.r, i[t][v] = q.i;
+          a[t][v] = valid ? q.a : 1.0f;
+          hp[t][v] = valid ? q.c * q.i * xv[v] : 0.0f;
+          P[v] *= a[t][v];
+          S[v] = __builtin_fmaf(a[t][v], S[v], hp[t][v]);
+        }
+      }
+#pragma unroll
+      for (int v = 0; v < V; ++v) sums[buf][wave][v][lane] = S[v], S[v] = 0.0f;
+      // what comes into a wave from behind leaves it as a (dy + .) of its first step
+#pragma unroll
+      for (int t = T - 1; t >= 0; --t) {
+        float dv[V];
+        sd.raw[t].unpack(dv);
+        const bool valid = FULL || t0 + t < n;
+#pragma unroll
+        for (int v = 0; v < V; ++v) S[v] = a[t][v] * (S[v] + (valid ? dv[v] : 0.0f));
+      }
+      join_chain<V, W, true>(lds, sp, buf, wave, pos, chain, k > 0, P, S, g, out, next);
+      for (int w = 0; w < wave; ++w) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) h[v] = __builtin_fmaf(lds.waves[buf][w][v][lane], h[v], sums[buf][w][v][lane]);
+      }
+      buf ^= 1;
+      // hp becomes the state in front of each step
+#pragma unroll
+      for (int t = 0; t < T; ++t)
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          const float u = hp[t][v];
+          hp[t][v] = h[v];
+          h[v] = __builtin_fmaf(a[t][v], h[v], u);
+        }
+      const auto& prm = params_again<GatedBwdParams>();
+      IO* px = static_cast<IO*>(prm.dx) + b * prm.dx_bs + (t0 + T - 1) * prm.dx_ts;
+      IO* pa = static_cast<IO*>(prm.dag) + b * prm.dag_bs + (t0 + T - 1) * prm.dag_ts;
+      IO* pg = static_cast<IO*>(prm.dxg) + b * prm.dxg_bs + (t0 + T - 1) * prm.dxg_ts;
+#pragma unroll
+      for (int t = T - 1; t >= 0; --t) {
+        float xv[V], dv[V], ox[V], oa[V], og[V];
+        sx.raw[t].unpack(xv);
+        sd.raw[t].unpack(dv);
+        const bool valid = FULL || t0 + t < n;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          // made again rather than kept: the registers are worth more
+          asm volatile("" : "+v"(r[t][v]));
+          const float s = rate2[v] * r[t][v] * kLn2;
+          const float gt = g[v] + dv[v], gi = gt * i[t][v], gx = gi * xv[v];
+          const Back q = back_of(a[t][v], s);
+          const float p = q.ratio * gx - q.sa * gt * hp[t][v];
+          ox[v] = valid ? gi * q.c : 0.0f;
+          og[v] = valid ? gx * q.c * (1.0f - i[t][v]) : 0.0f;
+          oa[v] = valid ? p * (1.0f - r[t][v]) : 0.0f;
+          dA[v] += valid ? p : 0.0f;
+          g[v] = valid ? gt * a[t][v] : g[v];
+        }
+        if (mine && (FULL || t0 + t < prm.L)) {
+          VecIO<IO>::store(px + d, ox);
+          VecIO<IO>::store(pa + d, oa);
+          VecIO<IO>::store(pg + d, og);
+        }
+        px -= prm.dx_ts, pa -= prm.dag_ts, pg -= prm.dxg_ts;
+      }
+    };
+    if (tile + T * W <= n) {
+      body.template operator()<true>();
+    } else if (tile < n) {
+      body.template operator()<false>();
+    } else {
+#pragma unroll
+      for (int v = 0; v < V; ++v) out[v] = g[v];
+      if (mine) {
+        IO* dx = static_cast<IO*>(prm.dx) + b * prm.dx_bs;
+        IO* dag = static_cast<IO*>(prm.dag) + b * prm.dag_bs;
+        IO* dxg = static_cast<IO*>(prm.dxg) + b * prm.dxg_bs;
+        const int32_t end = tile + T * W < prm.L ? tile + T * W : static_cast<int32_t>(prm.L);
+        for (int32_t t = t0; t < t0 + T && t < end; ++t) {
+          const float zero[V] = {};
+          VecIO<IO>::store(dx + t * prm.dx_ts + d, zero);
+          VecIO<IO>::store(dag + t * prm.dag_ts + d, zero);
+          VecIO<IO>::store(dxg + t * prm.dxg_ts + d, zero);
+        }
+      }
+      if (threadIdx.x == 0) lds.ticket = next;
+      __syncthreads();
+      next = lds.ticket;
+    }
+    const auto& end = params_again<GatedBwdParams>();
+    if (wave == 0 && mine && k == 0 && end.dh0 != nullptr) VecIO<float>::store(end.dh0 + bd, out);
+    // the waves' sums of q, in order
+#pragma unroll
+    for (int v = 0; v < V; ++v) dsum[wave][v][lane] = dA[v];
+    __syncthreads();
+    if (wave == 0 && mine) {
+#pragma unroll
+      for (int v = 0; v < V; ++v)
+        for (int w = 1; w < W; ++w) dA[v] += dsum[w][v][lane];
+      VecIO<float>::store(end.ws + (static_cast<int64_t>(k) * (sp.chains / end.n_cg) + b) * end.nd + d, dA);
+    }
   }
 }
 
@@ -724,7 +921,7 @@ void for_gated(const ssm_gated_dims* dims, const F& f) {
 }
 
 constexpr int kSteps = 8, kWaves = 8;          // of the kernels that walk
-constexpr int kFwdSteps = 16;                   // of the one whose workgroups share a row
+constexpr int kFwdSteps = 16, kBwdSteps = 8;   // of those whose workgroups share a row
 
 // How a row's steps are cut up, and the workspace that takes.
 struct Cut {
@@ -742,6 +939,10 @@ Cut cut_of(const ssm_gated_dims* dims, int64_t steps, int64_t V) {
 }
 Cut fwd_cut(const ssm_gated_dims* dims) {
   return cut_of(dims, kFwdSteps * kWaves, dims->dim <= kNarrow ? 1 : 2);
+}
+
+Cut bwd_cut(const ssm_gated_dims* dims) {
+  return cut_of(dims, kBwdSteps * kWaves, dims->dim <= kNarrow ? 1 : 2);
 }
 
 ChainSpace chain_space(void* workspace, const Cut& c, int64_t V) {
@@ -839,7 +1040,9 @@ int ssm_gated_recurrence_fwd(ssm_scan_t handle, const ssm_gated_dims* dims, cons
 
 int64_t ssm_gated_recurrence_bwd_workspace_bytes(const ssm_gated_dims* dims) {
   if (check_gated_dims(dims) != SSM_OK) return -1;
-  return dims->batch * dims->dim * 4;
+  // the chains' words, then a row of sums for every tile that a workgroup took
+  const Cut c = bwd_cut(dims);
+  return (c.words + (c.shared ? c.tiles : 1) * dims->batch * dims->dim) * 4;
 }
 
 int ssm_gated_recurrence_bwd(ssm_scan_t handle, const ssm_gated_dims* dims, const ssm_gated_bwd_io* io, void* stream) {
@@ -902,8 +1105,19 @@ int ssm_gated_recurrence_bwd(ssm_scan_t handle, const ssm_gated_dims* dims, cons
   p.dxg_bs = io->dx_gate_batch_stride, p.dxg_ts = io->dx_gate_time_stride;
   p.L = L, p.nd = static_cast<int32_t>(nd), p.n_states = static_cast<int32_t>(ns);
   bool fits = true;
+  const Cut cut = bwd_cut(dims);
+  p.ws += cut.words;
+  if (cut.shared) launch_fill(io->workspace, cut, s);
   for_gated(dims, [&]<typename IO, int V>() {
     p.n_cg = static_cast<int32_t>((nd + 64 * V - 1) / (64 * V));
+    if (cut.shared) {
+      const int64_t resident = 2 * handle->cu_count;
+      hipLaunchKernelGGL((gated_bwd_chain_kernel<IO, V, kBwdSteps, kWaves>),
+                         dim3(static_cast<unsigned>(cut.tickets < resident ? cut.tickets : resident)),
+                         dim3(64 * kWaves), 0, s, p, chain_space(io->workspace, cut, V),
+                         static_cast<uint32_t>(cut.tickets), static_cast<uint32_t>(cut.tiles));
+      return;
+    }
     fits = grid_fits(nb * p.n_cg, 64 * kWaves);
     if (fits)
       hipLaunchKernelGGL((gated_bwd_kernel<IO, V, kSteps, kWaves>), dim3(static_cast<unsigned>(nb * p.n_cg)),
@@ -911,7 +1125,7 @@ int ssm_gated_recurrence_bwd(ssm_scan_t handle, const ssm_gated_dims* dims, cons
   });
   if (!fits) return SSM_ERR_UNSUPPORTED;
   if (launched() != SSM_OK) return SSM_ERR_HIP;
-  launch_reduce(p.ws, nb, nd, GatedGrads{io->dA_log}, s);
+  launch_reduce(p.ws, (cut.shared ? cut.tiles : 1) * nb, nd, GatedGrads{io->dA_log}, s);
   return launched();
 }
 
