@@ -65,19 +65,17 @@ struct GatedBwdParams {
   int32_t nd, n_cg, n_states;
 };
 
-// 1 - a^2 for a = e^(-q/2): near q = 0, where the difference would cancel, the
-// series q - q^2/2! + q^3/3! - ..., whose first term left out is at most
-// q^8/9! = 1e-8 of it at q = 1/2; from there on the difference loses at most 1.5
-// times a^2's own rounding.
-__device__ __forceinline__ float one_minus_square(float a, float q) {
-  float p = __builtin_fmaf(q, -1.0f / 40320, 1.0f / 5040);
-  p = __builtin_fmaf(q, p, -1.0f / 720);
-  p = __builtin_fmaf(q, p, 1.0f / 120);
-  p = __builtin_fmaf(q, p, -1.0f / 24);
-  p = __builtin_fmaf(q, p, 1.0f / 6);
-  p = __builtin_fmaf(q, p, -0.5f);
-  p = __builtin_fmaf(q, p, 1.0f) * q;
-  return q < 0.5f ? p : __builtin_fmaf(-a, a, 1.0f);
+// 1 - a^2 for a = 2^-s2.  Near s2 = 0, where the difference would cancel, s2 times a
+// polynomial: the one of degree 4 nearest to (1 - 2^-2x) / x on [0, 0.36] by its
+// largest relative error (1.5 U with these coefficients, U = 2^-24; found by
+// exchange of its extrema).  From there on, 1 - a^2 >= 0.39, the difference loses
+// at most 1.5 times a^2's own rounding.
+__device__ __forceinline__ float one_minus_square(float a, float s2) {
+  float p = __builtin_fmaf(s2, 0.0346816927f, -0.151441112f);
+  p = __builtin_fmaf(s2, p, 0.443718821f);
+  p = __builtin_fmaf(s2, p, -0.960891724f);
+  p = __builtin_fmaf(s2, p, 1.38629425f) * s2;
+  return s2 < 0.36f ? p : __builtin_fmaf(-a, a, 1.0f);
 }
 
 // A gate's sigmoid.  sigmoid_exact cuts its argument, and a NaN there comes out as
@@ -88,34 +86,41 @@ __device__ __forceinline__ float gate_sigmoid(float v) {
   return sizeof(IO) == 2 || v == v ? s : v;
 }
 
-// A step's gates.  rate2 = exp(A_log) log2(e), so that a = 2^(-s2).
+// A step's gates.  rate2 = exp(A_log) log2(e), so that a = 2^-s2 with s2 = s log2(e).
 struct Gate {
-  float r, i, s, a, c;
+  float r, i, s2, a, c;
 };
 template <typename IO>
 __device__ __forceinline__ Gate gate_of(float ag, float xg, float rate2) {
   Gate g;
   g.r = gate_sigmoid<IO>(ag);
   g.i = gate_sigmoid<IO>(xg);
-  const float s2 = rate2 * g.r;
-  g.s = s2 * kLn2;
-  g.a = fast_exp2(-s2);
-  g.c = __builtin_amdgcn_sqrtf(one_minus_square(g.a, 2.0f * g.s));
+  g.s2 = rate2 * g.r;
+  g.a = fast_exp2(-g.s2);
+  g.c = __builtin_amdgcn_sqrtf(one_minus_square(g.a, g.s2));
   return g;
 }
 
-// What the backward makes of a decay and its exponent: c, s a, and s a^2 / c, both
-// of which go to 0 with s and, where a is 0, for large s.
+// What the backward takes of a step besides a and u: with g the state's gradient
+// and h the state in front,
+//     dx = g kx,  dx_gate = g kg,  q = g (k1 - k2 h),  da_gate = q kr
+// k1 = s a^2 i x / c and k2 = s a go to 0 with s, and, where a is 0, for large s.
 struct Back {
-  float c, sa, ratio;
+  float a, u, kx, kg, k1, k2, kr;
 };
-__device__ __forceinline__ Back back_of(float a, float s) {
+template <typename IO>
+__device__ __forceinline__ Back back_of(float x, float ag, float xg, float rate2) {
   Back b;
-  const float c2 = one_minus_square(a, 2.0f * s);
-  const float rc = c2 > 0.0f ? __builtin_amdgcn_rsqf(c2) : 0.0f;
-  b.c = c2 * rc;
-  b.sa = a > 0.0f ? s * a : 0.0f;
-  b.ratio = b.sa * a * rc;
+  const float r = gate_sigmoid<IO>(ag), i = gate_sigmoid<IO>(xg), s2 = rate2 * r;
+  b.a = fast_exp2(-s2);
+  const float c2 = one_minus_square(b.a, s2);
+  const float rc = c2 > 0.0f ? __builtin_amdgcn_rsqf(c2) : c2 * 0.0f, c = c2 * rc, ix = i * x;
+  b.u = c * ix;
+  b.kx = c * i;
+  b.kg = __builtin_fmaf(-i, b.u, b.u);
+  b.k2 = __builtin_fminf(s2, 0x1p127f) * kLn2 * b.a;
+  b.k1 = b.k2 * b.a * (rc * ix);
+  b.kr = 1.0f - r;
   return b;
 }
 
@@ -576,7 +581,7 @@ __global__ __launch_bounds__(64 * W) void gated_bwd_kernel(const GatedBwdParams 
   constexpr bool FULL = false;
   for (int32_t at = tiles - 1; at >= 0; --at) {
     const int32_t tile = at * T * W, t0 = tile + wave * T;
-    float a[T][V], hp[T][V], P[V], S[V], h[V] = {}, out[V];
+    float a[T][V], u[T][V], kx[T][V], kg[T][V], k1[T][V], k2[T][V], kr[T][V], P[V], S[V], h[V] = {}, out[V];
     Steps<IO, V, T> sx, sa, sg, sd;
     sx.template load<FULL>(x, prm.x_ts, t0, n - 1, d);
     sa.template load<FULL>(ag, prm.ag_ts, t0, n - 1, d);
@@ -597,22 +602,22 @@ __global__ __launch_bounds__(64 * W) void gated_bwd_kernel(const GatedBwdParams 
       const bool valid = t0 + t < n;
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        const Gate q = gate_of<IO>(av[v], gv[v], rate2[v]);
+        const Back q = back_of<IO>(xv[v], av[v], gv[v], rate2[v]);
         a[t][v] = valid ? q.a : 1.0f;
-        hp[t][v] = valid ? q.c * q.i * xv[v] : 0.0f;
+        u[t][v] = valid ? q.u : 0.0f;
+        kx[t][v] = q.kx, kg[t][v] = q.kg, k1[t][v] = q.k1, k2[t][v] = q.k2, kr[t][v] = q.kr;
         P[v] *= a[t][v];
-        S[v] = __builtin_fmaf(a[t][v], S[v], hp[t][v]);
+        S[v] = __builtin_fmaf(a[t][v], S[v], u[t][v]);
       }
     }
     join_waves<V, W, false>(lds, wave, P, S, h, out);
-    // hp becomes the state in front of each step
+    // k1 becomes k1 - k2 h
 #pragma unroll
     for (int t = 0; t < T; ++t)
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        const float u = hp[t][v];
-        hp[t][v] = h[v];
-        h[v] = __builtin_fmaf(a[t][v], h[v], u);
+        k1[t][v] = __builtin_fmaf(-k2[t][v], h[v], k1[t][v]);
+        h[v] = __builtin_fmaf(a[t][v], h[v], u[t][v]);
       }
     // what comes into a wave from behind leaves it as a (dy + .) of its first step
 #pragma unroll
@@ -631,22 +636,16 @@ __global__ __launch_bounds__(64 * W) void gated_bwd_kernel(const GatedBwdParams 
     join_waves<V, W, true>(lds, wave, P, S, g, out);
 #pragma unroll
     for (int t = T - 1; t >= 0; --t) {
-      float xv[V], av[V], gv[V], dv[V], ox[V], oa[V], og[V];
-      sx.raw[t].unpack(xv);
-      sa.raw[t].unpack(av);
-      sg.raw[t].unpack(gv);
+      float dv[V], ox[V], oa[V], og[V];
       sd.raw[t].unpack(dv);
       const bool valid = t0 + t < n;
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        const Gate q = gate_of<IO>(av[v], gv[v], rate2[v]);
-        const Back k = back_of(q.a, q.s);
-        const float gt = g[v] + dv[v], gi = gt * q.i, gx = gi * xv[v];
-        const float p = k.ratio * gx - k.sa * gt * hp[t][v];
-        ox[v] = valid ? gi * k.c : 0.0f;
-        og[v] = valid ? gx * k.c * (1.0f - q.i) : 0.0f;
-        oa[v] = valid ? p * (1.0f - q.r) : 0.0f;
-        dA[v] += valid ? p : 0.0f;
+        const float gt = g[v] + dv[v], q = gt * k1[t][v];
+        ox[v] = valid ? gt * kx[t][v] : 0.0f;
+        og[v] = valid ? gt * kg[t][v] : 0.0f;
+        oa[v] = valid ? q * kr[t][v] : 0.0f;
+        dA[v] += valid ? q : 0.0f;
         g[v] = valid ? gt * a[t][v] : g[v];
       }
       if (mine && t0 + t < prm.L) {
@@ -684,7 +683,7 @@ __global__ __launch_bounds__(64 * W) void gated_bwd_kernel(const GatedBwdParams 
 // a step needs of the forward pass comes from its own tile alone; the chain carries
 // the state's gradient.  A wave's product of decays is one for both directions.
 template <typename IO, int V, int T, int W>
-__global__ __launch_bounds__(64 * W) void gated_bwd_chain_kernel(const GatedBwdParams, const ChainSpace sp,
+__global__ __launch_bounds__(64 * W, 4) void gated_bwd_chain_kernel(const GatedBwdParams, const ChainSpace sp,
                                                                  uint32_t tickets, uint32_t tiles) {
   static_assert(T * W % kChunk == 0, "a tile begins behind a kept state");
   __shared__ ChainLds<V, W> lds;
@@ -712,7 +711,7 @@ __global__ __launch_bounds__(64 * W) void gated_bwd_chain_kernel(const GatedBwdP
       const IO* ag = static_cast<const IO*>(prm.ag) + b * prm.ag_bs;
       const IO* xg = static_cast<const IO*>(prm.xg) + b * prm.xg_bs;
       const IO* dy = static_cast<const IO*>(prm.dy) + b * prm.dy_bs;
-      float rate2[V], r[T][V], i[T][V], a[T][V], hp[T][V], P[V], S[V], h[V] = {};
+      float rate2[V], a[T][V], u[T][V], kx[T][V], kg[T][V], k1[T][V], k2[T][V], kr[T][V], P[V], S[V], h[V] = {};
       Steps<IO, V, T> sx, sa, sg, sd;
       sa.template load<FULL>(ag, prm.ag_ts, t0, n - 1, d);
       sg.template load<FULL>(xg, prm.xg_ts, t0, n - 1, d);
@@ -733,12 +732,12 @@ __global__ __launch_bounds__(64 * W) void gated_bwd_chain_kernel(const GatedBwdP
         const bool valid = FULL || t0 + t < n;
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-          const Gate q = gate_of<IO>(av[v], gv[v], rate2[v]);
-          r[t][v] = q.r, i[t][v] = q.i;
+          const Back q = back_of<IO>(xv[v], av[v], gv[v], rate2[v]);
           a[t][v] = valid ? q.a : 1.0f;
-          hp[t][v] = valid ? q.c * q.i * xv[v] : 0.0f;
+          u[t][v] = valid ? q.u : 0.0f;
+          kx[t][v] = q.kx, kg[t][v] = q.kg, k1[t][v] = q.k1, k2[t][v] = q.k2, kr[t][v] = q.kr;
           P[v] *= a[t][v];
-          S[v] = __builtin_fmaf(a[t][v], S[v], hp[t][v]);
+          S[v] = __builtin_fmaf(a[t][v], S[v], u[t][v]);
         }
       }
 #pragma unroll
@@ -758,14 +757,13 @@ __global__ __launch_bounds__(64 * W) void gated_bwd_chain_kernel(const GatedBwdP
         for (int v = 0; v < V; ++v) h[v] = __builtin_fmaf(lds.waves[buf][w][v][lane], h[v], sums[buf][w][v][lane]);
       }
       buf ^= 1;
-      // hp becomes the state in front of each step
+      // k1 becomes k1 - k2 h
 #pragma unroll
       for (int t = 0; t < T; ++t)
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-          const float u = hp[t][v];
-          hp[t][v] = h[v];
-          h[v] = __builtin_fmaf(a[t][v], h[v], u);
+          k1[t][v] = __builtin_fmaf(-k2[t][v], h[v], k1[t][v]);
+          h[v] = __builtin_fmaf(a[t][v], h[v], u[t][v]);
         }
       const auto& prm = params_again<GatedBwdParams>();
       IO* px = static_cast<IO*>(prm.dx) + b * prm.dx_bs + (t0 + T - 1) * prm.dx_ts;
@@ -773,22 +771,16 @@ __global__ __launch_bounds__(64 * W) void gated_bwd_chain_kernel(const GatedBwdP
       IO* pg = static_cast<IO*>(prm.dxg) + b * prm.dxg_bs + (t0 + T - 1) * prm.dxg_ts;
 #pragma unroll
       for (int t = T - 1; t >= 0; --t) {
-        float xv[V], dv[V], ox[V], oa[V], og[V];
-        sx.raw[t].unpack(xv);
+        float dv[V], ox[V], oa[V], og[V];
         sd.raw[t].unpack(dv);
         const bool valid = FULL || t0 + t < n;
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-          // made again rather than kept: the registers are worth more
-          asm volatile("" : "+v"(r[t][v]));
-          const float s = rate2[v] * r[t][v] * kLn2;
-          const float gt = g[v] + dv[v], gi = gt * i[t][v], gx = gi * xv[v];
-          const Back q = back_of(a[t][v], s);
-          const float p = q.ratio * gx - q.sa * gt * hp[t][v];
-          ox[v] = valid ? gi * q.c : 0.0f;
-          og[v] = valid ? gx * q.c * (1.0f - i[t][v]) : 0.0f;
-          oa[v] = valid ? p * (1.0f - r[t][v]) : 0.0f;
-          dA[v] += valid ? p : 0.0f;
+          const float gt = g[v] + dv[v], q = gt * k1[t][v];
+          ox[v] = valid ? gt * kx[t][v] : 0.0f;
+          og[v] = valid ? gt * kg[t][v] : 0.0f;
+          oa[v] = valid ? q * kr[t][v] : 0.0f;
+          dA[v] += valid ? q : 0.0f;
           g[v] = valid ? gt * a[t][v] : g[v];
         }
         if (mine && (FULL || t0 + t < prm.L)) {
@@ -911,17 +903,19 @@ int64_t n_states(const ssm_gated_dims* dims) { return (dims->seqlen + kChunk - 1
 // idle.
 constexpr int64_t kNarrow = 64;
 
-template <typename F>
+template <int WIDE, typename F>
 void for_gated(const ssm_gated_dims* dims, const F& f) {
   const bool narrow = dims->dim <= kNarrow;
   if (dims->io_dtype == SSM_IO_BF16)
-    narrow ? f.template operator()<uint16_t, 1>() : f.template operator()<uint16_t, 2>();
+    narrow ? f.template operator()<uint16_t, 1>() : f.template operator()<uint16_t, WIDE>();
   else
-    narrow ? f.template operator()<float, 1>() : f.template operator()<float, 2>();
+    narrow ? f.template operator()<float, 1>() : f.template operator()<float, WIDE>();
 }
 
 constexpr int kSteps = 8, kWaves = 8;          // of the kernels that walk
-constexpr int kFwdSteps = 16, kBwdSteps = 8;   // of those whose workgroups share a row
+// of those whose workgroups share a row, and the most channels of a lane
+constexpr int kFwdSteps = 16, kFwdWaves = 8, kFwdWide = 2;
+constexpr int kBwdSteps = 8, kBwdWaves = 8, kBwdWide = 1;
 
 // How a row's steps are cut up, and the workspace that takes.
 struct Cut {
@@ -938,11 +932,11 @@ Cut cut_of(const ssm_gated_dims* dims, int64_t steps, int64_t V) {
   return c;
 }
 Cut fwd_cut(const ssm_gated_dims* dims) {
-  return cut_of(dims, kFwdSteps * kWaves, dims->dim <= kNarrow ? 1 : 2);
+  return cut_of(dims, kFwdSteps * kFwdWaves, dims->dim <= kNarrow ? 1 : kFwdWide);
 }
 
 Cut bwd_cut(const ssm_gated_dims* dims) {
-  return cut_of(dims, kBwdSteps * kWaves, dims->dim <= kNarrow ? 1 : 2);
+  return cut_of(dims, kBwdSteps * kBwdWaves, dims->dim <= kNarrow ? 1 : kBwdWide);
 }
 
 ChainSpace chain_space(void* workspace, const Cut& c, int64_t V) {
@@ -1020,13 +1014,13 @@ int ssm_gated_recurrence_fwd(ssm_scan_t handle, const ssm_gated_dims* dims, cons
   bool fits = true;
   const Cut cut = fwd_cut(dims);
   if (cut.shared) launch_fill(io->workspace, cut, s);
-  for_gated(dims, [&]<typename IO, int V>() {
+  for_gated<kFwdWide>(dims, [&]<typename IO, int V>() {
     p.n_cg = static_cast<int32_t>((nd + 64 * V - 1) / (64 * V));
     if (cut.shared) {
-      const int64_t resident = 2 * handle->cu_count;
-      hipLaunchKernelGGL((gated_fwd_chain_kernel<IO, V, kFwdSteps, kWaves>),
+      const int64_t resident = 6 * handle->cu_count;
+      hipLaunchKernelGGL((gated_fwd_chain_kernel<IO, V, kFwdSteps, kFwdWaves>),
                          dim3(static_cast<unsigned>(cut.tickets < resident ? cut.tickets : resident)),
-                         dim3(64 * kWaves), 0, s, p, chain_space(io->workspace, cut, V),
+                         dim3(64 * kFwdWaves), 0, s, p, chain_space(io->workspace, cut, V),
                          static_cast<uint32_t>(cut.tickets));
       return;
     }
@@ -1108,13 +1102,13 @@ int ssm_gated_recurrence_bwd(ssm_scan_t handle, const ssm_gated_dims* dims, cons
   const Cut cut = bwd_cut(dims);
   p.ws += cut.words;
   if (cut.shared) launch_fill(io->workspace, cut, s);
-  for_gated(dims, [&]<typename IO, int V>() {
+  for_gated<kBwdWide>(dims, [&]<typename IO, int V>() {
     p.n_cg = static_cast<int32_t>((nd + 64 * V - 1) / (64 * V));
     if (cut.shared) {
-      const int64_t resident = 2 * handle->cu_count;
-      hipLaunchKernelGGL((gated_bwd_chain_kernel<IO, V, kBwdSteps, kWaves>),
+      const int64_t resident = 6 * handle->cu_count;
+      hipLaunchKernelGGL((gated_bwd_chain_kernel<IO, V, kBwdSteps, kBwdWaves>),
                          dim3(static_cast<unsigned>(cut.tickets < resident ? cut.tickets : resident)),
-                         dim3(64 * kWaves), 0, s, p, chain_space(io->workspace, cut, V),
+                         dim3(64 * kBwdWaves), 0, s, p, chain_space(io->workspace, cut, V),
                          static_cast<uint32_t>(cut.tickets), static_cast<uint32_t>(cut.tiles));
       return;
     }
