@@ -103,11 +103,15 @@ __device__ __forceinline__ Gate gate_of(float ag, float xg, float rate2) {
 
 // What the backward takes of a step besides a and u: with g the state's gradient
 // and h the state in front,
-//     dx = g kx,  dx_gate = g kg,  q = g (k1 - k2 h),  da_gate = q kr
+//     dx = g kx,  dx_gate = g u ki,  q = g (k1 - k2 h),  da_gate = q (1 - r)
 // k1 = s a^2 i x / c and k2 = s a go to 0 with s, and, where a is 0, for large s.
 struct Back {
-  float a, u, kx, kg, k1, k2, kr;
+  float a, u, kx, ki, k1, r;
 };
+// k2
+__device__ __forceinline__ float k2_of(float a, float r, float rate2) {
+  return __builtin_fminf(rate2 * r, 0x1p127f) * kLn2 * a;
+}
 template <typename IO>
 __device__ __forceinline__ Back back_of(float x, float ag, float xg, float rate2) {
   Back b;
@@ -117,10 +121,9 @@ __device__ __forceinline__ Back back_of(float x, float ag, float xg, float rate2
   const float rc = c2 > 0.0f ? __builtin_amdgcn_rsqf(c2) : c2 * 0.0f, c = c2 * rc, ix = i * x;
   b.u = c * ix;
   b.kx = c * i;
-  b.kg = __builtin_fmaf(-i, b.u, b.u);
-  b.k2 = __builtin_fminf(s2, 0x1p127f) * kLn2 * b.a;
-  b.k1 = b.k2 * b.a * (rc * ix);
-  b.kr = 1.0f - r;
+  b.ki = 1.0f - i;
+  b.k1 = k2_of(b.a, r, rate2) * b.a * (rc * ix);
+  b.r = r;
   return b;
 }
 
@@ -132,22 +135,34 @@ __device__ __forceinline__ int32_t length_of(const int32_t* valid_len, int32_t b
 
 __device__ __forceinline__ int wave_index() { return __builtin_amdgcn_readfirstlane(threadIdx.x / 64); }
 
-// V channels of T steps as they stand in memory.  Unless all of them are steps of
-// the row (FULL), those past the last one read it again (their values are not
-// used).
-template <typename IO, int V, int T>
-struct Steps {
-  RawVec<IO, V> raw[T];
-  template <bool FULL>
-  __device__ __forceinline__ void load(const void* base, int64_t ts, int32_t t0, int32_t last, int32_t d) {
-    const IO* p = static_cast<const IO*>(base) + (FULL || t0 < last ? t0 : last) * ts;  // the same for the wave
-#pragma unroll
-    for (int t = 0; t < T; ++t) {
-      raw[t].load(p + d);
-      p += FULL || t0 + t < last ? ts : 0;
-    }
+// V channels of a wave's steps of one tensor, loaded one step after another.  Unless
+// all of them are steps of the row (FULL), those past the last one read it again
+// (their values are not used).
+template <typename IO, int V, bool FULL>
+struct Feed {
+  const IO* p;  // the same for the wave
+  int64_t ts;
+  int32_t left;
+  __device__ __forceinline__ Feed(const void* base, int64_t bs, int64_t step, int32_t b, int32_t t0, int32_t last)
+      : p(static_cast<const IO*>(base) + b * bs + (FULL || t0 < last ? t0 : last) * step), ts(step), left(last - t0) {}
+  __device__ __forceinline__ RawVec<IO, V> next(int t, int32_t d) {
+    RawVec<IO, V> raw;
+    raw.load(p + d);
+    p += FULL || t < left ? ts : 0;
+    return raw;
   }
 };
+
+// A wave's steps of both gates and x.  Loads come back in order: what the first step
+// takes is asked for first.
+template <bool FULL, typename IO, int V, int T, typename P>
+__device__ __forceinline__ void load_steps(const P& prm, int32_t b, int32_t t0, int32_t last, int32_t d,
+                                           RawVec<IO, V> (&ra)[T], RawVec<IO, V> (&rg)[T], RawVec<IO, V> (&rx)[T]) {
+  Feed<IO, V, FULL> fa(prm.ag, prm.ag_bs, prm.ag_ts, b, t0, last), fg(prm.xg, prm.xg_bs, prm.xg_ts, b, t0, last),
+      fx(prm.x, prm.x_bs, prm.x_ts, b, t0, last);
+#pragma unroll
+  for (int t = 0; t < T; ++t) ra[t] = fa.next(t, d), rg[t] = fg.next(t, d), rx[t] = fx.next(t, d);
+}
 
 // The states of a workgroup's waves in front of their steps: (P, S) of every
 // wave meet in LDS, and each composes those of the waves in front of it behind
@@ -287,15 +302,17 @@ struct ChainLds {
   uint32_t ticket;
 };
 
-// From a wave's pair (P, S) to the state `h` in front of the wave's steps and `out`,
-// the one behind the tile.  Called with the chain's initial state for its first
-// tile, which takes it into its pair, and zero for the others.  pos: the tile's
-// place in its chain; more: whether another follows.  `next` becomes the ticket
-// that thread 0 drew.
+// Joining a tile to its chain, in two halves, each with a barrier.  The first takes
+// every wave's pair (P, S) and publishes the tile's; it is called with the chain's
+// initial state in `h` for its first tile, which takes it into its pair, and zero
+// for the others.  The second waits for the pairs in front and the span's state, and
+// leaves in `h` the state in front of the wave's steps and in `out` the one behind
+// the tile.  pos: the tile's place in its chain; more: whether another follows.
+// `next` becomes the ticket that thread 0 drew.
 template <int V, int W, bool REVERSE>
-__device__ __forceinline__ void join_chain(ChainLds<V, W>& lds, const ChainSpace& sp, int buf, int wave, uint32_t pos,
+__device__ __forceinline__ void join_begin(ChainLds<V, W>& lds, const ChainSpace& sp, int buf, int wave, uint32_t pos,
                                            uint32_t chain, bool more, const float (&P)[V], const float (&S)[V],
-                                           float (&h)[V], float (&out)[V], uint32_t& next) {
+                                           float (&h)[V]) {
   const int lane = threadIdx.x % 64;
   auto& mine = lds.waves[buf];
 #pragma unroll
@@ -303,9 +320,7 @@ __device__ __forceinline__ void join_chain(ChainLds<V, W>& lds, const ChainSpace
 #pragma unroll
   for (int v = 0; v < V; ++v) mine[wave][v][lane] = above_zero(P[v]), mine[wave][V + v][lane] = S[v];
   __syncthreads();
-  const uint32_t span = pos / kSpan;
-  const int before = static_cast<int>(pos % kSpan);  // tiles of the span in front of this one
-  if (wave == W - 1 && more && before != kSpan - 1) {
+  if (wave == W - 1 && more && pos % kSpan != kSpan - 1) {
     float p[V], s[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) p[v] = 1.0f, s[v] = h[v];
@@ -325,6 +340,15 @@ __device__ __forceinline__ void join_chain(ChainLds<V, W>& lds, const ChainSpace
     publish<V>(at, p);
     publish<V>(at + 64 * V, s);
   }
+}
+
+template <int V, int W, bool REVERSE>
+__device__ __forceinline__ void join_end(ChainLds<V, W>& lds, const ChainSpace& sp, int buf, int wave, uint32_t pos,
+                                         uint32_t chain, bool more, float (&h)[V], float (&out)[V], uint32_t& next) {
+  const int lane = threadIdx.x % 64;
+  auto& mine = lds.waves[buf];
+  const uint32_t span = pos / kSpan;
+  const int before = static_cast<int>(pos % kSpan);  // tiles of the span in front of this one
   for (int j = wave; j <= before; j += W) {
     if (j < before) {
       const float* at = sp.pair<V>(span * kSpan + j, chain);
@@ -386,9 +410,6 @@ __global__ __launch_bounds__(64 * W) void gated_fwd_kernel(const GatedParams prm
   const int32_t first = (cg * 64 + lane) * V, d = first < prm.nd - V ? first : prm.nd - V;
   const bool mine = first < prm.nd;
   const int32_t n = length_of(prm.valid_len, b, prm.L);
-  const IO* x = static_cast<const IO*>(prm.x) + b * prm.x_bs;
-  const IO* ag = static_cast<const IO*>(prm.ag) + b * prm.ag_bs;
-  const IO* xg = static_cast<const IO*>(prm.xg) + b * prm.xg_bs;
   IO* y = static_cast<IO*>(prm.y) + b * prm.y_bs;
   float rate2[V], h[V] = {};
 #pragma unroll
@@ -399,18 +420,16 @@ __global__ __launch_bounds__(64 * W) void gated_fwd_kernel(const GatedParams prm
   for (; tile < n; tile += T * W) {
     const int32_t t0 = tile + wave * T;
     float a[T][V], u[T][V], P[V], S[V], out[V];
-    Steps<IO, V, T> sx, sa, sg;
-    sx.template load<FULL>(x, prm.x_ts, t0, n - 1, d);
-    sa.template load<FULL>(ag, prm.ag_ts, t0, n - 1, d);
-    sg.template load<FULL>(xg, prm.xg_ts, t0, n - 1, d);
+    RawVec<IO, V> ra[T], rg[T], rx[T];
+    load_steps<FULL>(prm, b, t0, n - 1, d, ra, rg, rx);
 #pragma unroll
     for (int v = 0; v < V; ++v) P[v] = 1.0f, S[v] = 0.0f;
 #pragma unroll
     for (int t = 0; t < T; ++t) {
       float xv[V], av[V], gv[V];
-      sx.raw[t].unpack(xv);
-      sa.raw[t].unpack(av);
-      sg.raw[t].unpack(gv);
+      rx[t].unpack(xv);
+      ra[t].unpack(av);
+      rg[t].unpack(gv);
       const bool valid = t0 + t < n;
 #pragma unroll
       for (int v = 0; v < V; ++v) {
@@ -476,22 +495,18 @@ __global__ __launch_bounds__(64 * W, 4) void gated_fwd_chain_kernel(const GatedP
     float h[V] = {}, out[V];
     if (pos == 0 && prm.h0 != nullptr) VecIO<float>::load(prm.h0 + bd, h);
     const auto body = [&]<bool FULL>() __attribute__((always_inline)) {
-      const IO* x = static_cast<const IO*>(prm.x) + b * prm.x_bs;
-      const IO* ag = static_cast<const IO*>(prm.ag) + b * prm.ag_bs;
-      const IO* xg = static_cast<const IO*>(prm.xg) + b * prm.xg_bs;
-      float rate2[V], a[T][V], u[T][V], P[V], S[V];
-      Steps<IO, V, T> sx, sa, sg;
-      sa.template load<FULL>(ag, prm.ag_ts, t0, n - 1, d);
-      sg.template load<FULL>(xg, prm.xg_ts, t0, n - 1, d);
-      sx.template load<FULL>(x, prm.x_ts, t0, n - 1, d);
+      float al[V], rate2[V], a[T][V], u[T][V], P[V], S[V];
+      RawVec<IO, V> ra[T], rg[T], rx[T];
+      VecIO<float>::load(prm.A_log + d, al);
+      load_steps<FULL>(prm, b, t0, n - 1, d, ra, rg, rx);
 #pragma unroll
-      for (int v = 0; v < V; ++v) rate2[v] = expf(prm.A_log[d + v]) * kLog2e, P[v] = 1.0f, S[v] = 0.0f;
+      for (int v = 0; v < V; ++v) rate2[v] = expf(al[v]) * kLog2e, P[v] = 1.0f, S[v] = 0.0f;
 #pragma unroll
       for (int t = 0; t < T; ++t) {
         float xv[V], av[V], gv[V];
-        sx.raw[t].unpack(xv);
-        sa.raw[t].unpack(av);
-        sg.raw[t].unpack(gv);
+        rx[t].unpack(xv);
+        ra[t].unpack(av);
+        rg[t].unpack(gv);
         const bool valid = FULL || t0 + t < n;
 #pragma unroll
         for (int v = 0; v < V; ++v) {
@@ -502,7 +517,8 @@ __global__ __launch_bounds__(64 * W, 4) void gated_fwd_chain_kernel(const GatedP
           S[v] = __builtin_fmaf(a[t][v], S[v], u[t][v]);
         }
       }
-      join_chain<V, W, false>(lds, sp, buf, wave, pos, chain, tile + T * W < n, P, S, h, out, next);
+      join_begin<V, W, false>(lds, sp, buf, wave, pos, chain, tile + T * W < n, P, S, h);
+      join_end<V, W, false>(lds, sp, buf, wave, pos, chain, tile + T * W < n, h, out, next);
       buf ^= 1;
       const auto& prm = params_again<GatedParams>();
       IO* y = static_cast<IO*>(prm.y) + b * prm.y_bs + t0 * prm.y_ts;
@@ -566,10 +582,6 @@ __global__ __launch_bounds__(64 * W) void gated_bwd_kernel(const GatedBwdParams 
   const bool mine = first < prm.nd;
   const int32_t n = length_of(prm.valid_len, b, prm.L);
   const int64_t bd = static_cast<int64_t>(b) * prm.nd + d;
-  const IO* x = static_cast<const IO*>(prm.x) + b * prm.x_bs;
-  const IO* ag = static_cast<const IO*>(prm.ag) + b * prm.ag_bs;
-  const IO* xg = static_cast<const IO*>(prm.xg) + b * prm.xg_bs;
-  const IO* dy = static_cast<const IO*>(prm.dy) + b * prm.dy_bs;
   IO* dx = static_cast<IO*>(prm.dx) + b * prm.dx_bs;
   IO* dag = static_cast<IO*>(prm.dag) + b * prm.dag_bs;
   IO* dxg = static_cast<IO*>(prm.dxg) + b * prm.dxg_bs;
@@ -581,12 +593,12 @@ __global__ __launch_bounds__(64 * W) void gated_bwd_kernel(const GatedBwdParams 
   constexpr bool FULL = false;
   for (int32_t at = tiles - 1; at >= 0; --at) {
     const int32_t tile = at * T * W, t0 = tile + wave * T;
-    float a[T][V], u[T][V], kx[T][V], kg[T][V], k1[T][V], k2[T][V], kr[T][V], P[V], S[V], h[V] = {}, out[V];
-    Steps<IO, V, T> sx, sa, sg, sd;
-    sx.template load<FULL>(x, prm.x_ts, t0, n - 1, d);
-    sa.template load<FULL>(ag, prm.ag_ts, t0, n - 1, d);
-    sg.template load<FULL>(xg, prm.xg_ts, t0, n - 1, d);
-    sd.template load<FULL>(dy, prm.dy_ts, t0, n - 1, d);
+    float a[T][V], u[T][V], kx[T][V], ki[T][V], k1[T][V], r[T][V], P[V], S[V], h[V] = {}, out[V];
+    RawVec<IO, V> ra[T], rg[T], rx[T], rd[T];
+    load_steps<FULL>(prm, b, t0, n - 1, d, ra, rg, rx);
+    Feed<IO, V, FULL> fd(prm.dy, prm.dy_bs, prm.dy_ts, b, t0, n - 1);
+#pragma unroll
+    for (int t = 0; t < T; ++t) rd[t] = fd.next(t, d);
     if (tile > 0)
       VecIO<float>::load(prm.states + (static_cast<int64_t>(b) * prm.n_states + tile / kChunk - 1) * prm.nd + d, h);
     else if (prm.h0 != nullptr)
@@ -596,16 +608,16 @@ __global__ __launch_bounds__(64 * W) void gated_bwd_kernel(const GatedBwdParams 
 #pragma unroll
     for (int t = 0; t < T; ++t) {
       float xv[V], av[V], gv[V];
-      sx.raw[t].unpack(xv);
-      sa.raw[t].unpack(av);
-      sg.raw[t].unpack(gv);
+      rx[t].unpack(xv);
+      ra[t].unpack(av);
+      rg[t].unpack(gv);
       const bool valid = t0 + t < n;
 #pragma unroll
       for (int v = 0; v < V; ++v) {
         const Back q = back_of<IO>(xv[v], av[v], gv[v], rate2[v]);
         a[t][v] = valid ? q.a : 1.0f;
         u[t][v] = valid ? q.u : 0.0f;
-        kx[t][v] = q.kx, kg[t][v] = q.kg, k1[t][v] = q.k1, k2[t][v] = q.k2, kr[t][v] = q.kr;
+        kx[t][v] = q.kx, ki[t][v] = q.ki, k1[t][v] = q.k1, r[t][v] = q.r;
         P[v] *= a[t][v];
         S[v] = __builtin_fmaf(a[t][v], S[v], u[t][v]);
       }
@@ -616,7 +628,7 @@ __global__ __launch_bounds__(64 * W) void gated_bwd_kernel(const GatedBwdParams 
     for (int t = 0; t < T; ++t)
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        k1[t][v] = __builtin_fmaf(-k2[t][v], h[v], k1[t][v]);
+        k1[t][v] = __builtin_fmaf(-k2_of(a[t][v], r[t][v], rate2[v]), h[v], k1[t][v]);
         h[v] = __builtin_fmaf(a[t][v], h[v], u[t][v]);
       }
     // what comes into a wave from behind leaves it as a (dy + .) of its first step
@@ -625,7 +637,7 @@ __global__ __launch_bounds__(64 * W) void gated_bwd_kernel(const GatedBwdParams 
 #pragma unroll
     for (int t = T - 1; t >= 0; --t) {
       float dv[V];
-      sd.raw[t].unpack(dv);
+      rd[t].unpack(dv);
       const bool valid = t0 + t < n;
 #pragma unroll
       for (int v = 0; v < V; ++v) {
@@ -637,14 +649,14 @@ __global__ __launch_bounds__(64 * W) void gated_bwd_kernel(const GatedBwdParams 
 #pragma unroll
     for (int t = T - 1; t >= 0; --t) {
       float dv[V], ox[V], oa[V], og[V];
-      sd.raw[t].unpack(dv);
+      rd[t].unpack(dv);
       const bool valid = t0 + t < n;
 #pragma unroll
       for (int v = 0; v < V; ++v) {
         const float gt = g[v] + dv[v], q = gt * k1[t][v];
         ox[v] = valid ? gt * kx[t][v] : 0.0f;
-        og[v] = valid ? gt * kg[t][v] : 0.0f;
-        oa[v] = valid ? q * kr[t][v] : 0.0f;
+        og[v] = valid ? gt * u[t][v] * ki[t][v] : 0.0f;
+        oa[v] = valid ? q * (1.0f - r[t][v]) : 0.0f;
         dA[v] += valid ? q : 0.0f;
         g[v] = valid ? gt * a[t][v] : g[v];
       }
@@ -687,9 +699,23 @@ __global__ __launch_bounds__(64 * W, 4) void gated_bwd_chain_kernel(const GatedB
                                                                  uint32_t tickets, uint32_t tiles) {
   static_assert(T * W % kChunk == 0, "a tile begins behind a kept state");
   __shared__ ChainLds<V, W> lds;
-  __shared__ float sums[2][W][V][64], dsum[W][V][64];
+  __shared__ float sums[2][W][V][64], dsum[2][W][V][64];
   const int wave = wave_index(), lane = threadIdx.x % 64;
   uint32_t next = 0;
+  // A tile's sums of q, one a wave, wait for the next barrier; then the first wave
+  // adds them in order.
+  float* sum_to = nullptr;
+  int sum_buf = 0;
+  const auto flush = [&]() __attribute__((always_inline)) {
+    if (wave == 0 && sum_to != nullptr) {
+      float t[V] = {};
+#pragma unroll
+      for (int w = 0; w < W; ++w)
+#pragma unroll
+        for (int v = 0; v < V; ++v) t[v] += dsum[sum_buf][w][v][lane];
+      VecIO<float>::store(sum_to, t);
+    }
+  };
   if (threadIdx.x == 0) lds.ticket = atomicAdd(sp.counter, 1u);
   __syncthreads();
   uint32_t ticket = __builtin_amdgcn_readfirstlane(lds.ticket);
@@ -707,38 +733,36 @@ __global__ __launch_bounds__(64 * W, 4) void gated_bwd_chain_kernel(const GatedB
     float g[V] = {}, out[V], dA[V] = {};
     if ((tile < n ? pos == 0 : k == 0) && prm.dh_last != nullptr) VecIO<float>::load(prm.dh_last + bd, g);
     const auto body = [&]<bool FULL>() __attribute__((always_inline)) {
-      const IO* x = static_cast<const IO*>(prm.x) + b * prm.x_bs;
-      const IO* ag = static_cast<const IO*>(prm.ag) + b * prm.ag_bs;
-      const IO* xg = static_cast<const IO*>(prm.xg) + b * prm.xg_bs;
-      const IO* dy = static_cast<const IO*>(prm.dy) + b * prm.dy_bs;
-      float rate2[V], a[T][V], u[T][V], kx[T][V], kg[T][V], k1[T][V], k2[T][V], kr[T][V], P[V], S[V], h[V] = {};
-      Steps<IO, V, T> sx, sa, sg, sd;
-      sa.template load<FULL>(ag, prm.ag_ts, t0, n - 1, d);
-      sg.template load<FULL>(xg, prm.xg_ts, t0, n - 1, d);
-      sx.template load<FULL>(x, prm.x_ts, t0, n - 1, d);
-      sd.template load<FULL>(dy, prm.dy_ts, t0, n - 1, d);
+      float al[V], rate2[V], a[T][V], u[T][V], kx[T][V], ki[T][V], k1[T][V], r[T][V], P[V], S[V], h[V] = {};
+      RawVec<IO, V> ra[T], rg[T], rx[T], rd[T];
+      VecIO<float>::load(prm.A_log + d, al);
+      load_steps<FULL>(prm, b, t0, n - 1, d, ra, rg, rx);
+      Feed<IO, V, FULL> fd(prm.dy, prm.dy_bs, prm.dy_ts, b, t0, n - 1);
+#pragma unroll
+      for (int t = 0; t < T; ++t) rd[t] = fd.next(t, d);
       if (tile > 0)
         VecIO<float>::load(prm.states + (static_cast<int64_t>(b) * prm.n_states + tile / kChunk - 1) * prm.nd + d, h);
       else if (prm.h0 != nullptr)
         VecIO<float>::load(prm.h0 + bd, h);
 #pragma unroll
-      for (int v = 0; v < V; ++v) rate2[v] = expf(prm.A_log[d + v]) * kLog2e, P[v] = 1.0f, S[v] = 0.0f;
+      for (int v = 0; v < V; ++v) rate2[v] = expf(al[v]) * kLog2e, P[v] = 1.0f, S[v] = 0.0f;
 #pragma unroll
       for (int t = 0; t < T; ++t) {
         float xv[V], av[V], gv[V];
-        sx.raw[t].unpack(xv);
-        sa.raw[t].unpack(av);
-        sg.raw[t].unpack(gv);
+        rx[t].unpack(xv);
+        ra[t].unpack(av);
+        rg[t].unpack(gv);
         const bool valid = FULL || t0 + t < n;
 #pragma unroll
         for (int v = 0; v < V; ++v) {
           const Back q = back_of<IO>(xv[v], av[v], gv[v], rate2[v]);
           a[t][v] = valid ? q.a : 1.0f;
           u[t][v] = valid ? q.u : 0.0f;
-          kx[t][v] = q.kx, kg[t][v] = q.kg, k1[t][v] = q.k1, k2[t][v] = q.k2, kr[t][v] = q.kr;
+          kx[t][v] = q.kx, ki[t][v] = q.ki, k1[t][v] = q.k1, r[t][v] = q.r;
           P[v] *= a[t][v];
           S[v] = __builtin_fmaf(a[t][v], S[v], u[t][v]);
         }
+
       }
 #pragma unroll
       for (int v = 0; v < V; ++v) sums[buf][wave][v][lane] = S[v], S[v] = 0.0f;
@@ -746,25 +770,27 @@ __global__ __launch_bounds__(64 * W, 4) void gated_bwd_chain_kernel(const GatedB
 #pragma unroll
       for (int t = T - 1; t >= 0; --t) {
         float dv[V];
-        sd.raw[t].unpack(dv);
+        rd[t].unpack(dv);
         const bool valid = FULL || t0 + t < n;
 #pragma unroll
         for (int v = 0; v < V; ++v) S[v] = a[t][v] * (S[v] + (valid ? dv[v] : 0.0f));
       }
-      join_chain<V, W, true>(lds, sp, buf, wave, pos, chain, k > 0, P, S, g, out, next);
+      join_begin<V, W, true>(lds, sp, buf, wave, pos, chain, k > 0, P, S, g);
+      flush();
       for (int w = 0; w < wave; ++w) {
 #pragma unroll
         for (int v = 0; v < V; ++v) h[v] = __builtin_fmaf(lds.waves[buf][w][v][lane], h[v], sums[buf][w][v][lane]);
       }
-      buf ^= 1;
       // k1 becomes k1 - k2 h
 #pragma unroll
       for (int t = 0; t < T; ++t)
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-          k1[t][v] = __builtin_fmaf(-k2[t][v], h[v], k1[t][v]);
+          k1[t][v] = __builtin_fmaf(-k2_of(a[t][v], r[t][v], rate2[v]), h[v], k1[t][v]);
           h[v] = __builtin_fmaf(a[t][v], h[v], u[t][v]);
         }
+      join_end<V, W, true>(lds, sp, buf, wave, pos, chain, k > 0, g, out, next);
+      buf ^= 1;
       const auto& prm = params_again<GatedBwdParams>();
       IO* px = static_cast<IO*>(prm.dx) + b * prm.dx_bs + (t0 + T - 1) * prm.dx_ts;
       IO* pa = static_cast<IO*>(prm.dag) + b * prm.dag_bs + (t0 + T - 1) * prm.dag_ts;
@@ -772,14 +798,14 @@ __global__ __launch_bounds__(64 * W, 4) void gated_bwd_chain_kernel(const GatedB
 #pragma unroll
       for (int t = T - 1; t >= 0; --t) {
         float dv[V], ox[V], oa[V], og[V];
-        sd.raw[t].unpack(dv);
+        rd[t].unpack(dv);
         const bool valid = FULL || t0 + t < n;
 #pragma unroll
         for (int v = 0; v < V; ++v) {
           const float gt = g[v] + dv[v], q = gt * k1[t][v];
           ox[v] = valid ? gt * kx[t][v] : 0.0f;
-          og[v] = valid ? gt * kg[t][v] : 0.0f;
-          oa[v] = valid ? q * kr[t][v] : 0.0f;
+          og[v] = valid ? gt * u[t][v] * ki[t][v] : 0.0f;
+          oa[v] = valid ? q * (1.0f - r[t][v]) : 0.0f;
           dA[v] += valid ? q : 0.0f;
           g[v] = valid ? gt * a[t][v] : g[v];
         }
@@ -789,6 +815,7 @@ __global__ __launch_bounds__(64 * W, 4) void gated_bwd_chain_kernel(const GatedB
           VecIO<IO>::store(pg + d, og);
         }
         px -= prm.dx_ts, pa -= prm.dag_ts, pg -= prm.dxg_ts;
+
       }
     };
     if (tile + T * W <= n) {
@@ -813,20 +840,18 @@ __global__ __launch_bounds__(64 * W, 4) void gated_bwd_chain_kernel(const GatedB
       if (threadIdx.x == 0) lds.ticket = next;
       __syncthreads();
       next = lds.ticket;
+      flush();
+      __syncthreads();
     }
     const auto& end = params_again<GatedBwdParams>();
     if (wave == 0 && mine && k == 0 && end.dh0 != nullptr) VecIO<float>::store(end.dh0 + bd, out);
-    // the waves' sums of q, in order
+    sum_buf ^= 1;
+    sum_to = mine ? end.ws + (static_cast<int64_t>(k) * (sp.chains / end.n_cg) + b) * end.nd + d : nullptr;
 #pragma unroll
-    for (int v = 0; v < V; ++v) dsum[wave][v][lane] = dA[v];
-    __syncthreads();
-    if (wave == 0 && mine) {
-#pragma unroll
-      for (int v = 0; v < V; ++v)
-        for (int w = 1; w < W; ++w) dA[v] += dsum[w][v][lane];
-      VecIO<float>::store(end.ws + (static_cast<int64_t>(k) * (sp.chains / end.n_cg) + b) * end.nd + d, dA);
-    }
+    for (int v = 0; v < V; ++v) dsum[sum_buf][wave][v][lane] = dA[v];
   }
+  __syncthreads();
+  flush();
 }
 
 struct GatedGrads {
