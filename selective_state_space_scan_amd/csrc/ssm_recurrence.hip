@@ -127,10 +127,23 @@ __device__ __forceinline__ Back back_of(float x, float ag, float xg, float rate2
   return b;
 }
 
+// A row's valid length, the same row for the whole wave: by a scalar load, which does
+// not wait for the vector loads and stores in flight.
 __device__ __forceinline__ int32_t length_of(const int32_t* valid_len, int32_t b, int64_t L) {
   if (valid_len == nullptr) return static_cast<int32_t>(L);
-  const int32_t n = valid_len[b];
+  typedef const __attribute__((address_space(4))) int32_t* scalar;
+  const int32_t n = ((scalar)(uintptr_t)valid_len)[__builtin_amdgcn_readfirstlane(b)];
   return n < 0 ? 0 : (n > L ? static_cast<int32_t>(L) : n);
+}
+
+// V elements at a lane's byte offset from an address that is the same for the wave.
+template <typename IO>
+__device__ __forceinline__ const IO* lane_at(const IO* p, uint32_t off) {
+  return reinterpret_cast<const IO*>(reinterpret_cast<const char*>(p) + off);
+}
+template <typename IO>
+__device__ __forceinline__ IO* lane_at(IO* p, uint32_t off) {
+  return reinterpret_cast<IO*>(reinterpret_cast<char*>(p) + off);
 }
 
 __device__ __forceinline__ int wave_index() { return __builtin_amdgcn_readfirstlane(threadIdx.x / 64); }
@@ -147,7 +160,7 @@ struct Feed {
       : p(static_cast<const IO*>(base) + b * bs + (FULL || t0 < last ? t0 : last) * step), ts(step), left(last - t0) {}
   __device__ __forceinline__ RawVec<IO, V> next(int t, int32_t d) {
     RawVec<IO, V> raw;
-    raw.load(p + d);
+    raw.load(lane_at(p, static_cast<uint32_t>(d) * static_cast<uint32_t>(sizeof(IO))));
     p += FULL || t < left ? ts : 0;
     return raw;
   }
@@ -307,8 +320,8 @@ struct ChainLds {
 // initial state in `h` for its first tile, which takes it into its pair, and zero
 // for the others.  The second waits for the pairs in front and the span's state, and
 // leaves in `h` the state in front of the wave's steps and in `out` the one behind
-// the tile.  pos: the tile's place in its chain; more: whether another follows.
-// `next` becomes the ticket that thread 0 drew.
+// the tile.  pos: the tile's place in its chain; more: whether another follows.  The
+// workgroup's next ticket is drawn here, where all wait anyway.
 template <int V, int W, bool REVERSE>
 __device__ __forceinline__ void join_begin(ChainLds<V, W>& lds, const ChainSpace& sp, int buf, int wave, uint32_t pos,
                                            uint32_t chain, bool more, const float (&P)[V], const float (&S)[V],
@@ -344,11 +357,12 @@ __device__ __forceinline__ void join_begin(ChainLds<V, W>& lds, const ChainSpace
 
 template <int V, int W, bool REVERSE>
 __device__ __forceinline__ void join_end(ChainLds<V, W>& lds, const ChainSpace& sp, int buf, int wave, uint32_t pos,
-                                         uint32_t chain, bool more, float (&h)[V], float (&out)[V], uint32_t& next) {
+                                         uint32_t chain, bool more, float (&h)[V], float (&out)[V], uint32_t& ticket) {
   const int lane = threadIdx.x % 64;
   auto& mine = lds.waves[buf];
   const uint32_t span = pos / kSpan;
   const int before = static_cast<int>(pos % kSpan);  // tiles of the span in front of this one
+  if (threadIdx.x == 0) lds.ticket = atomicAdd(sp.counter, 1u);
   for (int j = wave; j <= before; j += W) {
     if (j < before) {
       const float* at = sp.pair<V>(span * kSpan + j, chain);
@@ -365,9 +379,8 @@ __device__ __forceinline__ void join_end(ChainLds<V, W>& lds, const ChainSpace& 
       for (int v = 0; v < V; ++v) lds.state[v][lane] = v1[0][v];
     }
   }
-  if (threadIdx.x == 0) lds.ticket = next;
   __syncthreads();
-  next = lds.ticket;
+  ticket = __builtin_amdgcn_readfirstlane(lds.ticket);
   if (span > 0) {
 #pragma unroll
     for (int v = 0; v < V; ++v) h[v] = lds.state[v][lane];
@@ -478,18 +491,17 @@ __global__ __launch_bounds__(64 * W, 4) void gated_fwd_chain_kernel(const GatedP
                                                                  uint32_t tickets) {
   __shared__ ChainLds<V, W> lds;
   const int wave = wave_index(), lane = threadIdx.x % 64;
-  uint32_t next = 0;
   if (threadIdx.x == 0) lds.ticket = atomicAdd(sp.counter, 1u);
   __syncthreads();
   uint32_t ticket = __builtin_amdgcn_readfirstlane(lds.ticket);
   __syncthreads();
-  for (int buf = 0; ticket < tickets; ticket = __builtin_amdgcn_readfirstlane(next)) {
-    if (threadIdx.x == 0) next = atomicAdd(sp.counter, 1u);
+  for (int buf = 0; ticket < tickets;) {
     const auto& prm = params_again<GatedParams>();
     const uint32_t pos = ticket / sp.chains, chain = ticket - pos * sp.chains;
     const int32_t b = chain / prm.n_cg, cg = chain % prm.n_cg, tile = pos * (T * W), t0 = tile + wave * T;
     const int32_t first = (cg * 64 + lane) * V, d = first < prm.nd - V ? first : prm.nd - V;
     const bool mine = first < prm.nd;
+    const uint32_t off = static_cast<uint32_t>(d) * static_cast<uint32_t>(sizeof(IO));
     const int32_t n = length_of(prm.valid_len, b, prm.L);
     const int64_t bd = static_cast<int64_t>(b) * prm.nd + d;
     float h[V] = {}, out[V];
@@ -518,7 +530,7 @@ __global__ __launch_bounds__(64 * W, 4) void gated_fwd_chain_kernel(const GatedP
         }
       }
       join_begin<V, W, false>(lds, sp, buf, wave, pos, chain, tile + T * W < n, P, S, h);
-      join_end<V, W, false>(lds, sp, buf, wave, pos, chain, tile + T * W < n, h, out, next);
+      join_end<V, W, false>(lds, sp, buf, wave, pos, chain, tile + T * W < n, h, out, ticket);
       buf ^= 1;
       const auto& prm = params_again<GatedParams>();
       IO* y = static_cast<IO*>(prm.y) + b * prm.y_bs + t0 * prm.y_ts;
@@ -531,7 +543,7 @@ __global__ __launch_bounds__(64 * W, 4) void gated_fwd_chain_kernel(const GatedP
           h[v] = __builtin_fmaf(a[t][v], h[v], u[t][v]);
           o[v] = valid ? h[v] : 0.0f;
         }
-        if (mine && (FULL || t0 + t < prm.L)) VecIO<IO>::store(y + d, o);
+        if (mine && (FULL || t0 + t < prm.L)) VecIO<IO>::store(lane_at(y, off), o);
         y += prm.y_ts;
       }
       if (prm.states != nullptr && mine && (t0 + T) % kChunk == 0 && (t0 + T) / kChunk <= prm.n_states)
@@ -552,10 +564,10 @@ __global__ __launch_bounds__(64 * W, 4) void gated_fwd_chain_kernel(const GatedP
           VecIO<IO>::store(y + t * prm.y_ts + d, zero);
         }
       }
-      if (threadIdx.x == 0) lds.ticket = next;
+      __syncthreads();  // this turn's ticket has been read
+      if (threadIdx.x == 0) lds.ticket = atomicAdd(sp.counter, 1u);
       __syncthreads();
-      next = lds.ticket;
-      __syncthreads();
+      ticket = __builtin_amdgcn_readfirstlane(lds.ticket);
     }
     const auto& end = params_again<GatedParams>();
     // the row's last tile (its first where it has no step) leaves the state
@@ -701,7 +713,6 @@ __global__ __launch_bounds__(64 * W, 4) void gated_bwd_chain_kernel(const GatedB
   __shared__ ChainLds<V, W> lds;
   __shared__ float sums[2][W][V][64], dsum[2][W][V][64];
   const int wave = wave_index(), lane = threadIdx.x % 64;
-  uint32_t next = 0;
   // A tile's sums of q, one a wave, wait for the next barrier; then the first wave
   // adds them in order.
   float* sum_to = nullptr;
@@ -720,13 +731,13 @@ __global__ __launch_bounds__(64 * W, 4) void gated_bwd_chain_kernel(const GatedB
   __syncthreads();
   uint32_t ticket = __builtin_amdgcn_readfirstlane(lds.ticket);
   __syncthreads();
-  for (int buf = 0; ticket < tickets; ticket = __builtin_amdgcn_readfirstlane(next)) {
-    if (threadIdx.x == 0) next = atomicAdd(sp.counter, 1u);
+  for (int buf = 0; ticket < tickets;) {
     const auto& prm = params_again<GatedBwdParams>();
     const uint32_t turn = ticket / sp.chains, chain = ticket - turn * sp.chains, k = tiles - 1 - turn;
     const int32_t b = chain / prm.n_cg, cg = chain % prm.n_cg, tile = k * (T * W), t0 = tile + wave * T;
     const int32_t first = (cg * 64 + lane) * V, d = first < prm.nd - V ? first : prm.nd - V;
     const bool mine = first < prm.nd;
+    const uint32_t off = static_cast<uint32_t>(d) * static_cast<uint32_t>(sizeof(IO));
     const int32_t n = length_of(prm.valid_len, b, prm.L);
     const int64_t bd = static_cast<int64_t>(b) * prm.nd + d;
     const uint32_t pos = (n + T * W - 1) / (T * W) - 1 - k;  // from the row's last tile with a step
@@ -789,7 +800,7 @@ __global__ __launch_bounds__(64 * W, 4) void gated_bwd_chain_kernel(const GatedB
           k1[t][v] = __builtin_fmaf(-k2_of(a[t][v], r[t][v], rate2[v]), h[v], k1[t][v]);
           h[v] = __builtin_fmaf(a[t][v], h[v], u[t][v]);
         }
-      join_end<V, W, true>(lds, sp, buf, wave, pos, chain, k > 0, g, out, next);
+      join_end<V, W, true>(lds, sp, buf, wave, pos, chain, k > 0, g, out, ticket);
       buf ^= 1;
       const auto& prm = params_again<GatedBwdParams>();
       IO* px = static_cast<IO*>(prm.dx) + b * prm.dx_bs + (t0 + T - 1) * prm.dx_ts;
@@ -810,9 +821,9 @@ __global__ __launch_bounds__(64 * W, 4) void gated_bwd_chain_kernel(const GatedB
           g[v] = valid ? gt * a[t][v] : g[v];
         }
         if (mine && (FULL || t0 + t < prm.L)) {
-          VecIO<IO>::store(px + d, ox);
-          VecIO<IO>::store(pa + d, oa);
-          VecIO<IO>::store(pg + d, og);
+          VecIO<IO>::store(lane_at(px, off), ox);
+          VecIO<IO>::store(lane_at(pa, off), oa);
+          VecIO<IO>::store(lane_at(pg, off), og);
         }
         px -= prm.dx_ts, pa -= prm.dag_ts, pg -= prm.dxg_ts;
 
@@ -837,11 +848,11 @@ __global__ __launch_bounds__(64 * W, 4) void gated_bwd_chain_kernel(const GatedB
           VecIO<IO>::store(dxg + t * prm.dxg_ts + d, zero);
         }
       }
-      if (threadIdx.x == 0) lds.ticket = next;
-      __syncthreads();
-      next = lds.ticket;
+      __syncthreads();  // this turn's ticket has been read
       flush();
+      if (threadIdx.x == 0) lds.ticket = atomicAdd(sp.counter, 1u);
       __syncthreads();
+      ticket = __builtin_amdgcn_readfirstlane(lds.ticket);
     }
     const auto& end = params_again<GatedBwdParams>();
     if (wave == 0 && mine && k == 0 && end.dh0 != nullptr) VecIO<float>::store(end.dh0 + bd, out);
