@@ -333,6 +333,7 @@ __device__ __forceinline__ void join_begin(ChainLds<V, W>& lds, const ChainSpace
 #pragma unroll
   for (int v = 0; v < V; ++v) mine[wave][v][lane] = above_zero(P[v]), mine[wave][V + v][lane] = S[v];
   __syncthreads();
+  __builtin_amdgcn_s_setprio(3);  // others wait for what this workgroup publishes
   if (wave == W - 1 && more && pos % kSpan != kSpan - 1) {
     float p[V], s[V];
 #pragma unroll
@@ -399,6 +400,7 @@ __device__ __forceinline__ void join_end(ChainLds<V, W>& lds, const ChainSpace& 
       h[v] = __builtin_fmaf(mine[w][v][lane], h[v], mine[w][V + v][lane]);
     }
   }
+  __builtin_amdgcn_s_setprio(0);
   if (wave == 0 && more && before == kSpan - 1) publish<V>(sp.state<V>(span + 1, chain), h);
 #pragma unroll
   for (int v = 0; v < V; ++v) out[v] = h[v], h[v] = own[v];
@@ -949,30 +951,43 @@ void for_gated(const ssm_gated_dims* dims, const F& f) {
 }
 
 constexpr int kSteps = 8, kWaves = 8;          // of the kernels that walk
-// of those whose workgroups share a row, and the most channels of a lane
-constexpr int kFwdSteps = 16, kFwdWaves = 8, kFwdWide = 2;
-constexpr int kBwdSteps = 8, kBwdWaves = 8, kBwdWide = 1;
+// Of those whose workgroups share a row: steps of a wave, and the most channels of a
+// lane.
+constexpr int kFwdSteps = 16, kFwdWide = 2;
+constexpr int kBwdSteps = 8, kBwdWide = 1;
 
-// How a row's steps are cut up, and the workspace that takes.
+// How a row's steps are cut up, and the workspace that takes.  The forward's tiles
+// are 16 waves where that leaves kMany of them: half as many turns of the chain (us at
+// 16 / 8 waves, bf16: 8 x 4096 x 1024 67.5 / 71, 1 x 32768 x 2048 117 / 138; but 1 x 4096 x
+// 256, 32 tiles, 16.7 / 13.3).  The backward's are 8 (136 against 156 and 267 against
+// 288 us for the first two: at 16 a CU holds one workgroup, and nothing moves while it
+// computes).
+constexpr int64_t kMany = 512;
 struct Cut {
-  int64_t tiles, chains, tickets, words;
+  int64_t tiles, chains, tickets, words, waves;
   bool shared;
 };
-Cut cut_of(const ssm_gated_dims* dims, int64_t steps, int64_t V) {
+Cut cut_of(const ssm_gated_dims* dims, int64_t steps, int64_t V, int64_t most_waves) {
   Cut c;
-  c.tiles = (dims->seqlen + steps - 1) / steps;
   c.chains = dims->batch * ((dims->dim + 64 * V - 1) / (64 * V));
-  c.tickets = c.tiles * c.chains;
+  for (c.waves = most_waves;; c.waves = 8) {
+    c.tiles = (dims->seqlen + steps * c.waves - 1) / (steps * c.waves);
+    c.tickets = c.tiles * c.chains;
+    if (c.waves == 8 || c.tickets >= kMany) break;
+  }
   c.shared = c.tiles >= 2 && c.tickets < (1 << 30);
   c.words = c.shared ? 4 + 64 * V * c.chains * (2 * c.tiles + c.tiles / kSpan + 1) : 0;
   return c;
 }
-Cut fwd_cut(const ssm_gated_dims* dims) {
-  return cut_of(dims, kFwdSteps * kFwdWaves, dims->dim <= kNarrow ? 1 : kFwdWide);
-}
+Cut fwd_cut(const ssm_gated_dims* dims) { return cut_of(dims, kFwdSteps, dims->dim <= kNarrow ? 1 : kFwdWide, 16); }
+Cut bwd_cut(const ssm_gated_dims* dims) { return cut_of(dims, kBwdSteps, dims->dim <= kNarrow ? 1 : kBwdWide, 8); }
 
-Cut bwd_cut(const ssm_gated_dims* dims) {
-  return cut_of(dims, kBwdSteps * kBwdWaves, dims->dim <= kNarrow ? 1 : kBwdWide);
+// Workgroups that take tiles: as many as the GPU holds at 128 registers a lane, 16
+// waves a CU.  More start only when others end, to find no tile left (three times
+// as many: 74 us where these take 72).
+int64_t takers(const Cut& c, int64_t cus) {
+  const int64_t held = 16 / c.waves * cus;
+  return c.tickets < held ? c.tickets : held;
 }
 
 ChainSpace chain_space(void* workspace, const Cut& c, int64_t V) {
@@ -1053,10 +1068,10 @@ int ssm_gated_recurrence_fwd(ssm_scan_t handle, const ssm_gated_dims* dims, cons
   for_gated<kFwdWide>(dims, [&]<typename IO, int V>() {
     p.n_cg = static_cast<int32_t>((nd + 64 * V - 1) / (64 * V));
     if (cut.shared) {
-      const int64_t resident = 6 * handle->cu_count;
-      hipLaunchKernelGGL((gated_fwd_chain_kernel<IO, V, kFwdSteps, kFwdWaves>),
-                         dim3(static_cast<unsigned>(cut.tickets < resident ? cut.tickets : resident)),
-                         dim3(64 * kFwdWaves), 0, s, p, chain_space(io->workspace, cut, V),
+      const auto kernel = cut.waves == 16 ? gated_fwd_chain_kernel<IO, V, kFwdSteps, 16>
+                                          : gated_fwd_chain_kernel<IO, V, kFwdSteps, 8>;
+      hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>(takers(cut, handle->cu_count))),
+                         dim3(static_cast<unsigned>(64 * cut.waves)), 0, s, p, chain_space(io->workspace, cut, V),
                          static_cast<uint32_t>(cut.tickets));
       return;
     }
@@ -1141,10 +1156,9 @@ int ssm_gated_recurrence_bwd(ssm_scan_t handle, const ssm_gated_dims* dims, cons
   for_gated<kBwdWide>(dims, [&]<typename IO, int V>() {
     p.n_cg = static_cast<int32_t>((nd + 64 * V - 1) / (64 * V));
     if (cut.shared) {
-      const int64_t resident = 6 * handle->cu_count;
-      hipLaunchKernelGGL((gated_bwd_chain_kernel<IO, V, kBwdSteps, kBwdWaves>),
-                         dim3(static_cast<unsigned>(cut.tickets < resident ? cut.tickets : resident)),
-                         dim3(64 * kBwdWaves), 0, s, p, chain_space(io->workspace, cut, V),
+      const auto kernel = gated_bwd_chain_kernel<IO, V, kBwdSteps, 8>;
+      hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>(takers(cut, handle->cu_count))),
+                         dim3(static_cast<unsigned>(64 * cut.waves)), 0, s, p, chain_space(io->workspace, cut, V),
                          static_cast<uint32_t>(cut.tickets), static_cast<uint32_t>(cut.tiles));
       return;
     }
