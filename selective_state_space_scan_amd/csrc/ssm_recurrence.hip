@@ -153,7 +153,7 @@ __device__ __forceinline__ int wave_index() { return __builtin_amdgcn_readfirstl
 // (their values are not used).
 template <typename IO, int V, bool FULL>
 struct Feed {
-  const IO* p;  // the same for the wave
+  const IO* p;  // the same for the wave, where all its lanes take the same steps
   int64_t ts;
   int32_t left;
   __device__ __forceinline__ Feed(const void* base, int64_t bs, int64_t step, int32_t b, int32_t t0, int32_t last)
@@ -175,36 +175,6 @@ __device__ __forceinline__ void load_steps(const P& prm, int32_t b, int32_t t0, 
       fx(prm.x, prm.x_bs, prm.x_ts, b, t0, last);
 #pragma unroll
   for (int t = 0; t < T; ++t) ra[t] = fa.next(t, d), rg[t] = fg.next(t, d), rx[t] = fx.next(t, d);
-}
-
-// The states of a workgroup's waves in front of their steps: (P, S) of every
-// wave meet in LDS, and each composes those of the waves in front of it behind
-// `h`, the state in front of the workgroup.  `h` becomes the wave's; what the
-// whole workgroup leaves goes to `out`.
-template <int V, int W, bool REVERSE>
-__device__ __forceinline__ void join_waves(float (&lds)[W][2 * V][64], int wave, const float (&P)[V],
-                                           const float (&S)[V], float (&h)[V], float (&out)[V]) {
-  const int lane = threadIdx.x % 64;
-  // the state in front has arrived in every wave before any of them writes the
-  // one behind, which may go to the same place
-#pragma unroll
-  for (int v = 0; v < V; ++v) asm volatile("" : "+v"(h[v]));
-  __syncthreads();  // the last join has been read
-#pragma unroll
-  for (int v = 0; v < V; ++v) lds[wave][v][lane] = P[v], lds[wave][V + v][lane] = S[v];
-  __syncthreads();
-  float mine[V];
-#pragma unroll
-  for (int k = 0; k < W; ++k) {
-    const int w = REVERSE ? W - 1 - k : k;
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      if (w == wave) mine[v] = h[v];
-      h[v] = __builtin_fmaf(lds[w][v][lane], h[v], lds[w][V + v][lane]);
-    }
-  }
-#pragma unroll
-  for (int v = 0; v < V; ++v) out[v] = h[v], h[v] = mine[v];
 }
 
 // A kernel's parameters, read again where they are used: held in scalar registers
@@ -413,78 +383,154 @@ __global__ void chain_fill_kernel(uint32_t* p, int64_t n) {
   if (i < n) *reinterpret_cast<vec4*>(p + i) = i == 0 ? vec4(0u) : vec4(kEmpty);
 }
 
-// A workgroup takes 64 V channels of one row and walks their steps, W waves of T
-// steps side by side.  Lanes past the last channel repeat the last V of the row
-// (which a lane whose V would reach past it takes too: both compute and write
-// the same).
-template <typename IO, int V, int T, int W>
-__global__ __launch_bounds__(64 * W) void gated_fwd_kernel(const GatedParams prm) {
-  __shared__ float lds[W][2 * V][64];
-  const int wave = wave_index(), lane = threadIdx.x % 64;
-  const int32_t b = blockIdx.x / prm.n_cg, cg = blockIdx.x % prm.n_cg;
-  const int32_t first = (cg * 64 + lane) * V, d = first < prm.nd - V ? first : prm.nd - V;
-  const bool mine = first < prm.nd;
-  const int32_t n = length_of(prm.valid_len, b, prm.L);
-  IO* y = static_cast<IO*>(prm.y) + b * prm.y_bs;
-  float rate2[V], h[V] = {};
-#pragma unroll
-  for (int v = 0; v < V; ++v) rate2[v] = expf(prm.A_log[d + v]) * kLog2e;
-  if (prm.h0 != nullptr) VecIO<float>::load(prm.h0 + static_cast<int64_t>(b) * prm.nd + d, h);
-  int32_t tile = 0;
-  constexpr bool FULL = false;
-  for (; tile < n; tile += T * W) {
-    const int32_t t0 = tile + wave * T;
-    float a[T][V], u[T][V], P[V], S[V], out[V];
-    RawVec<IO, V> ra[T], rg[T], rx[T];
-    load_steps<FULL>(prm, b, t0, n - 1, d, ra, rg, rx);
+// ---- rows that one workgroup holds ----------------------------------------------
+//
+// Short rows: W waves of G groups of 64 / G lanes, each lane V channels and T steps, and
+// G W T steps hold the row.  With G = 1 rows are read 128 or 256 bytes at a time; with
+// G = 4 a few long rows are spread over four times as many workgroups, which are then
+// done sooner.
+
+// The pairs of the groups, and the states in front of them.
+template <int V, int G, int W>
+struct RowLds {
+  float pair[G * W][64 / G][2 * V];
+  float front[G * W][64 / G][V];
+};
+
+// From the pairs, in the order of the steps (REVERSE: from the last), to the states;
+// `h`, the state in front of all, becomes the one behind.  By one wave, each row of
+// 64 / G lanes W groups; all rows hold h.
+template <int V, int G, int W, bool REVERSE>
+__device__ __forceinline__ void scan_groups(RowLds<V, G, W>& lds, float (&h)[V]) {
+  static_assert(G == 1 || G == 4, "the whole wave, or rows of 16 lanes");
+  const int lane = threadIdx.x % 64, sub = lane / (64 / G), cl = lane % (64 / G);
+  const auto at = [&](int k) { return REVERSE ? G * W - 1 - (sub * W + k) : sub * W + k; };
+  if constexpr (G == 4) {
+    float P[V], S[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) P[v] = 1.0f, S[v] = 0.0f;
 #pragma unroll
-    for (int t = 0; t < T; ++t) {
-      float xv[V], av[V], gv[V];
-      rx[t].unpack(xv);
-      ra[t].unpack(av);
-      rg[t].unpack(gv);
-      const bool valid = t0 + t < n;
+    for (int k = 0; k < W; ++k) {
+      const float* g = lds.pair[at(k)][cl];
 #pragma unroll
-      for (int v = 0; v < V; ++v) {
-        const Gate g = gate_of<IO>(av[v], gv[v], rate2[v]);
-        a[t][v] = valid ? g.a : 1.0f;
-        u[t][v] = valid ? g.c * g.i * xv[v] : 0.0f;
-        P[v] *= a[t][v];
-        S[v] = __builtin_fmaf(a[t][v], S[v], u[t][v]);
-      }
+      for (int v = 0; v < V; ++v) S[v] = __builtin_fmaf(g[v], S[v], g[V + v]), P[v] *= g[v];
     }
-    join_waves<V, W, false>(lds, wave, P, S, h, out);
+    // rows 0, 1 and rows 2, 3 join, then the halves: what is in front of a row
 #pragma unroll
-    for (int t = 0; t < T; ++t) {
-      const bool valid = t0 + t < n;
-      float o[V];
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        h[v] = __builtin_fmaf(a[t][v], h[v], u[t][v]);
-        o[v] = valid ? h[v] : 0.0f;
-      }
-      if (mine && t0 + t < prm.L) VecIO<IO>::store(y + (t0 + t) * prm.y_ts + d, o);
+    for (int v = 0; v < V; ++v) {
+      float p0, p1, s0, s1, ph, sh, back;
+      rows_swap16(above_zero(P[v]), p0, p1);
+      rows_swap16(S[v], s0, s1);
+      rows_swap32(above_zero(p0 * p1), ph, back);
+      rows_swap32(__builtin_fmaf(p1, s0, s1), sh, back);
+      if (sub >= 2) h[v] = __builtin_fmaf(ph, h[v], sh);
+      if (sub % 2 == 1) h[v] = __builtin_fmaf(p0, h[v], s0);
     }
-    // a chunk ends with a wave's last step
-    static_assert(kChunk % T == 0, "chunks are whole waves");
-    if (prm.states != nullptr && mine && (t0 + T) % kChunk == 0 && (t0 + T) / kChunk <= prm.n_states)
-      VecIO<float>::store(prm.states + (static_cast<int64_t>(b) * prm.n_states + (t0 + T) / kChunk - 1) * prm.nd + d, h);
+  }
 #pragma unroll
-    for (int v = 0; v < V; ++v) h[v] = out[v];
+  for (int k = 0; k < W; ++k) {
+    const float* g = lds.pair[at(k)][cl];
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      lds.front[at(k)][cl][v] = h[v];
+      h[v] = __builtin_fmaf(g[v], h[v], g[V + v]);
+    }
   }
-  if (wave == 0 && mine && prm.h_last != nullptr)
-    VecIO<float>::store(prm.h_last + static_cast<int64_t>(b) * prm.nd + d, h);
-  if (!mine) return;
-  // behind the row's end: steps that are padding, and states that stay
-  for (int64_t t = tile + wave; t < prm.L; t += W) {
-    const float zero[V] = {};
-    VecIO<IO>::store(y + t * prm.y_ts + d, zero);
+  if constexpr (G == 4) {  // the last row's to all
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      float lo, hi;
+      rows_swap32(h[v], lo, hi);
+      rows_swap16(hi, lo, h[v]);
+    }
   }
-  if (prm.states != nullptr)
-    for (int32_t c = tile / kChunk + wave; c < prm.n_states; c += W)
-      VecIO<float>::store(prm.states + (static_cast<int64_t>(b) * prm.n_states + c) * prm.nd + d, h);
+}
+
+// Where a lane works.  Lanes past the last channel repeat the last V of the row
+// (which a lane whose V would reach past it takes too: both compute and write the
+// same).
+struct RowAt {
+  int32_t b, d, q, t0;
+  bool mine;
+};
+template <int V, int G, int T>
+__device__ __forceinline__ RowAt row_place(int32_t nd, int32_t n_cg) {
+  constexpr int LPG = 64 / G;
+  RowAt at;
+  const int lane = threadIdx.x % 64;
+  at.b = blockIdx.x / n_cg;
+  const int32_t first = (static_cast<int32_t>(blockIdx.x % n_cg) * LPG + lane % LPG) * V;
+  at.d = first < nd - V ? first : nd - V;
+  at.mine = first < nd;
+  at.q = wave_index() * G + (G == 1 ? 0 : lane / LPG);
+  at.t0 = at.q * T;
+  return at;
+}
+
+template <typename IO, int V, int G, int T, int W>
+__global__ __launch_bounds__(64 * W) void gated_fwd_row_kernel(const GatedParams prm) {
+  __shared__ RowLds<V, G, W> lds;
+  static_assert(kChunk % T == 0, "chunks are whole groups of steps");
+  const RowAt at = row_place<V, G, T>(prm.nd, prm.n_cg);
+  const int cl = threadIdx.x % (64 / G);
+  const int32_t n = length_of(prm.valid_len, at.b, prm.L), d = at.d, t0 = at.t0;
+  const int64_t bd = static_cast<int64_t>(at.b) * prm.nd + d;
+  float al[V], rate2[V], a[T][V], u[T][V], P[V], S[V], h[V] = {};
+  VecIO<float>::load(prm.A_log + d, al);
+  if (wave_index() == 0 && prm.h0 != nullptr) VecIO<float>::load(prm.h0 + bd, h);
+  RawVec<IO, V> ra[T], rg[T], rx[T];
+  if (n > 0) load_steps<false>(prm, at.b, t0, n - 1, d, ra, rg, rx);
+#pragma unroll
+  for (int v = 0; v < V; ++v) rate2[v] = expf(al[v]) * kLog2e, P[v] = 1.0f, S[v] = 0.0f;
+#pragma unroll
+  for (int t = 0; t < T; ++t) {
+    float xv[V], av[V], gv[V];
+    rx[t].unpack(xv);
+    ra[t].unpack(av);
+    rg[t].unpack(gv);
+    const bool valid = t0 + t < n;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const Gate g = gate_of<IO>(av[v], gv[v], rate2[v]);
+      a[t][v] = valid ? g.a : 1.0f;
+      u[t][v] = valid ? g.c * g.i * xv[v] : 0.0f;
+      P[v] *= a[t][v];
+      S[v] = __builtin_fmaf(a[t][v], S[v], u[t][v]);
+    }
+  }
+#pragma unroll
+  for (int v = 0; v < V; ++v) lds.pair[at.q][cl][v] = above_zero(P[v]), lds.pair[at.q][cl][V + v] = S[v];
+  __syncthreads();
+  if (wave_index() == 0) {
+    scan_groups<V, G, W, false>(lds, h);
+    if (at.mine && threadIdx.x < 64 / G) {
+      if (prm.h_last != nullptr) VecIO<float>::store(prm.h_last + bd, h);
+      // chunks that end behind the last group
+      if (prm.states != nullptr)
+        for (int32_t c = G * W * T / kChunk; c < prm.n_states; ++c)
+          VecIO<float>::store(prm.states + (static_cast<int64_t>(at.b) * prm.n_states + c) * prm.nd + d, h);
+    }
+  }
+  __syncthreads();
+#pragma unroll
+  for (int v = 0; v < V; ++v) h[v] = lds.front[at.q][cl][v];
+  if (!at.mine) return;
+  const IO* out = static_cast<IO*>(prm.y) + at.b * prm.y_bs + t0 * prm.y_ts;
+#pragma unroll
+  for (int t = 0; t < T; ++t) {
+    const bool valid = t0 + t < n;
+    float o[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      h[v] = __builtin_fmaf(a[t][v], h[v], u[t][v]);
+      o[v] = valid ? h[v] : 0.0f;
+    }
+    if (t0 + t < prm.L)
+      VecIO<IO>::store(const_cast<IO*>(lane_at(out, static_cast<uint32_t>(d) * static_cast<uint32_t>(sizeof(IO)))), o);
+    out += prm.y_ts;
+  }
+  if (prm.states != nullptr && (t0 + T) % kChunk == 0 && (t0 + T) / kChunk <= prm.n_states)
+    VecIO<float>::store(prm.states + (static_cast<int64_t>(at.b) * prm.n_states + (t0 + T) / kChunk - 1) * prm.nd + d, h);
 }
 
 // The same with the row's tiles on different workgroups.
@@ -584,123 +630,114 @@ __global__ __launch_bounds__(64 * W, 4) void gated_fwd_chain_kernel(const GatedP
   }
 }
 
-// The same from the row's end.  A tile's states come again from the kept one in
-// front of it; its W T steps are whole chunks.
-template <typename IO, int V, int T, int W>
-__global__ __launch_bounds__(64 * W) void gated_bwd_kernel(const GatedBwdParams prm) {
-  static_assert(T * W % kChunk == 0, "a tile begins behind a kept state");
-  __shared__ float lds[W][2 * V][64];
-  const int wave = wave_index(), lane = threadIdx.x % 64;
-  const int32_t b = blockIdx.x / prm.n_cg, cg = blockIdx.x % prm.n_cg;
-  const int32_t first = (cg * 64 + lane) * V, d = first < prm.nd - V ? first : prm.nd - V;
-  const bool mine = first < prm.nd;
-  const int32_t n = length_of(prm.valid_len, b, prm.L);
-  const int64_t bd = static_cast<int64_t>(b) * prm.nd + d;
-  IO* dx = static_cast<IO*>(prm.dx) + b * prm.dx_bs;
-  IO* dag = static_cast<IO*>(prm.dag) + b * prm.dag_bs;
-  IO* dxg = static_cast<IO*>(prm.dxg) + b * prm.dxg_bs;
-  float rate2[V], g[V] = {}, dA[V] = {};
-#pragma unroll
-  for (int v = 0; v < V; ++v) rate2[v] = expf(prm.A_log[d + v]) * kLog2e;
-  if (prm.dh_last != nullptr) VecIO<float>::load(prm.dh_last + bd, g);
-  const int32_t tiles = (n + T * W - 1) / (T * W);
-  constexpr bool FULL = false;
-  for (int32_t at = tiles - 1; at >= 0; --at) {
-    const int32_t tile = at * T * W, t0 = tile + wave * T;
-    float a[T][V], u[T][V], kx[T][V], ki[T][V], k1[T][V], r[T][V], P[V], S[V], h[V] = {}, out[V];
-    RawVec<IO, V> ra[T], rg[T], rx[T], rd[T];
-    load_steps<FULL>(prm, b, t0, n - 1, d, ra, rg, rx);
-    Feed<IO, V, FULL> fd(prm.dy, prm.dy_bs, prm.dy_ts, b, t0, n - 1);
+// The same from the row's end; the states come again from the row's first.
+template <typename IO, int V, int G, int T, int W>
+__global__ __launch_bounds__(64 * W) void gated_bwd_row_kernel(const GatedBwdParams prm) {
+  __shared__ RowLds<V, G, W> lds, back;
+  const RowAt at = row_place<V, G, T>(prm.nd, prm.n_cg);
+  const int cl = threadIdx.x % (64 / G), wave = wave_index();
+  const int32_t n = length_of(prm.valid_len, at.b, prm.L), d = at.d, t0 = at.t0;
+  const int64_t bd = static_cast<int64_t>(at.b) * prm.nd + d;
+  float al[V], rate2[V], a[T][V], u[T][V], kx[T][V], ki[T][V], k1[T][V], r[T][V], P[V], S[V], h[V] = {}, g[V] = {};
+  VecIO<float>::load(prm.A_log + d, al);
+  if (wave == 0 && prm.h0 != nullptr) VecIO<float>::load(prm.h0 + bd, h);
+  if (wave == W - 1 && prm.dh_last != nullptr) VecIO<float>::load(prm.dh_last + bd, g);
+  RawVec<IO, V> ra[T], rg[T], rx[T], rd[T];
+  if (n > 0) {
+    load_steps<false>(prm, at.b, t0, n - 1, d, ra, rg, rx);
+    Feed<IO, V, false> fd(prm.dy, prm.dy_bs, prm.dy_ts, at.b, t0, n - 1);
 #pragma unroll
     for (int t = 0; t < T; ++t) rd[t] = fd.next(t, d);
-    if (tile > 0)
-      VecIO<float>::load(prm.states + (static_cast<int64_t>(b) * prm.n_states + tile / kChunk - 1) * prm.nd + d, h);
-    else if (prm.h0 != nullptr)
-      VecIO<float>::load(prm.h0 + bd, h);
-#pragma unroll
-    for (int v = 0; v < V; ++v) P[v] = 1.0f, S[v] = 0.0f;
-#pragma unroll
-    for (int t = 0; t < T; ++t) {
-      float xv[V], av[V], gv[V];
-      rx[t].unpack(xv);
-      ra[t].unpack(av);
-      rg[t].unpack(gv);
-      const bool valid = t0 + t < n;
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        const Back q = back_of<IO>(xv[v], av[v], gv[v], rate2[v]);
-        a[t][v] = valid ? q.a : 1.0f;
-        u[t][v] = valid ? q.u : 0.0f;
-        kx[t][v] = q.kx, ki[t][v] = q.ki, k1[t][v] = q.k1, r[t][v] = q.r;
-        P[v] *= a[t][v];
-        S[v] = __builtin_fmaf(a[t][v], S[v], u[t][v]);
-      }
-    }
-    join_waves<V, W, false>(lds, wave, P, S, h, out);
-    // k1 becomes k1 - k2 h
-#pragma unroll
-    for (int t = 0; t < T; ++t)
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        k1[t][v] = __builtin_fmaf(-k2_of(a[t][v], r[t][v], rate2[v]), h[v], k1[t][v]);
-        h[v] = __builtin_fmaf(a[t][v], h[v], u[t][v]);
-      }
-    // what comes into a wave from behind leaves it as a (dy + .) of its first step
-#pragma unroll
-    for (int v = 0; v < V; ++v) P[v] = 1.0f, S[v] = 0.0f;
-#pragma unroll
-    for (int t = T - 1; t >= 0; --t) {
-      float dv[V];
-      rd[t].unpack(dv);
-      const bool valid = t0 + t < n;
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        P[v] *= a[t][v];
-        S[v] = a[t][v] * (S[v] + (valid ? dv[v] : 0.0f));
-      }
-    }
-    join_waves<V, W, true>(lds, wave, P, S, g, out);
-#pragma unroll
-    for (int t = T - 1; t >= 0; --t) {
-      float dv[V], ox[V], oa[V], og[V];
-      rd[t].unpack(dv);
-      const bool valid = t0 + t < n;
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        const float gt = g[v] + dv[v], q = gt * k1[t][v];
-        ox[v] = valid ? gt * kx[t][v] : 0.0f;
-        og[v] = valid ? gt * u[t][v] * ki[t][v] : 0.0f;
-        oa[v] = valid ? q * (1.0f - r[t][v]) : 0.0f;
-        dA[v] += valid ? q : 0.0f;
-        g[v] = valid ? gt * a[t][v] : g[v];
-      }
-      if (mine && t0 + t < prm.L) {
-        VecIO<IO>::store(dx + (t0 + t) * prm.dx_ts + d, ox);
-        VecIO<IO>::store(dag + (t0 + t) * prm.dag_ts + d, oa);
-        VecIO<IO>::store(dxg + (t0 + t) * prm.dxg_ts + d, og);
-      }
-    }
-#pragma unroll
-    for (int v = 0; v < V; ++v) g[v] = out[v];
   }
-  if (wave == 0 && mine && prm.dh0 != nullptr) VecIO<float>::store(prm.dh0 + bd, g);
-  if (mine) {
-    for (int64_t t = static_cast<int64_t>(tiles) * T * W + wave; t < prm.L; t += W) {
-      const float zero[V] = {};
-      VecIO<IO>::store(dx + t * prm.dx_ts + d, zero);
-      VecIO<IO>::store(dag + t * prm.dag_ts + d, zero);
-      VecIO<IO>::store(dxg + t * prm.dxg_ts + d, zero);
+#pragma unroll
+  for (int v = 0; v < V; ++v) rate2[v] = expf(al[v]) * kLog2e, P[v] = 1.0f, S[v] = 0.0f;
+#pragma unroll
+  for (int t = 0; t < T; ++t) {
+    float xv[V], av[V], gv[V];
+    rx[t].unpack(xv);
+    ra[t].unpack(av);
+    rg[t].unpack(gv);
+    const bool valid = t0 + t < n;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const Back q = back_of<IO>(xv[v], av[v], gv[v], rate2[v]);
+      a[t][v] = valid ? q.a : 1.0f;
+      u[t][v] = valid ? q.u : 0.0f;
+      kx[t][v] = q.kx, ki[t][v] = q.ki, k1[t][v] = q.k1, r[t][v] = q.r;
+      P[v] *= a[t][v];
+      S[v] = __builtin_fmaf(a[t][v], S[v], u[t][v]);
     }
   }
-  // the waves' sums of q, in order
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    lds.pair[at.q][cl][v] = back.pair[at.q][cl][v] = above_zero(P[v]);
+    lds.pair[at.q][cl][V + v] = S[v], S[v] = 0.0f;
+  }
+  // what comes into a group from behind leaves it as a (dy + .) of its first step
+#pragma unroll
+  for (int t = T - 1; t >= 0; --t) {
+    float dv[V];
+    rd[t].unpack(dv);
+    const bool valid = t0 + t < n;
+#pragma unroll
+    for (int v = 0; v < V; ++v) S[v] = a[t][v] * (S[v] + (valid ? dv[v] : 0.0f));
+  }
+#pragma unroll
+  for (int v = 0; v < V; ++v) back.pair[at.q][cl][V + v] = S[v];
+  __syncthreads();
+  if (wave == 0) scan_groups<V, G, W, false>(lds, h);
+  if (wave == W - 1) {
+    scan_groups<V, G, W, true>(back, g);
+    if (at.mine && threadIdx.x % 64 < 64 / G && prm.dh0 != nullptr) VecIO<float>::store(prm.dh0 + bd, g);
+  }
   __syncthreads();
 #pragma unroll
-  for (int v = 0; v < V; ++v) lds[wave][v][lane] = dA[v];
-  __syncthreads();
-  if (wave == 0 && mine) {
+  for (int v = 0; v < V; ++v) h[v] = lds.front[at.q][cl][v], g[v] = back.front[at.q][cl][v];
+  // k1 becomes k1 - k2 h
 #pragma unroll
-    for (int v = 0; v < V; ++v)
-      for (int w = 1; w < W; ++w) dA[v] += lds[w][v][lane];
+  for (int t = 0; t < T; ++t)
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      k1[t][v] = __builtin_fmaf(-k2_of(a[t][v], r[t][v], rate2[v]), h[v], k1[t][v]);
+      h[v] = __builtin_fmaf(a[t][v], h[v], u[t][v]);
+    }
+  float dA[V] = {};
+  const uint32_t off = static_cast<uint32_t>(d) * static_cast<uint32_t>(sizeof(IO));
+  IO* px = static_cast<IO*>(prm.dx) + at.b * prm.dx_bs + (t0 + T - 1) * prm.dx_ts;
+  IO* pa = static_cast<IO*>(prm.dag) + at.b * prm.dag_bs + (t0 + T - 1) * prm.dag_ts;
+  IO* pg = static_cast<IO*>(prm.dxg) + at.b * prm.dxg_bs + (t0 + T - 1) * prm.dxg_ts;
+#pragma unroll
+  for (int t = T - 1; t >= 0; --t) {
+    float dv[V], ox[V], oa[V], og[V];
+    rd[t].unpack(dv);
+    const bool valid = t0 + t < n;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const float gt = g[v] + dv[v], q = gt * k1[t][v];
+      ox[v] = valid ? gt * kx[t][v] : 0.0f;
+      og[v] = valid ? gt * u[t][v] * ki[t][v] : 0.0f;
+      oa[v] = valid ? q * (1.0f - r[t][v]) : 0.0f;
+      dA[v] += valid ? q : 0.0f;
+      g[v] = valid ? gt * a[t][v] : g[v];
+    }
+    if (at.mine && t0 + t < prm.L) {
+      VecIO<IO>::store(lane_at(px, off), ox);
+      VecIO<IO>::store(lane_at(pa, off), oa);
+      VecIO<IO>::store(lane_at(pg, off), og);
+    }
+    px -= prm.dx_ts, pa -= prm.dag_ts, pg -= prm.dxg_ts;
+  }
+  // the groups' sums of q, in order (every group has read its states by now, from
+  // places of its own)
+#pragma unroll
+  for (int v = 0; v < V; ++v) lds.front[at.q][cl][v] = dA[v];
+  __syncthreads();
+  if (at.mine && threadIdx.x < 64 / G) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      dA[v] = 0.0f;
+      for (int q = 0; q < G * W; ++q) dA[v] += lds.front[q][cl][v];
+    }
     VecIO<float>::store(prm.ws + bd, dA);
   }
 }
@@ -937,50 +974,83 @@ int check_gated_dims(const ssm_gated_dims* dims) {
 
 int64_t n_states(const ssm_gated_dims* dims) { return (dims->seqlen + kChunk - 1) / kChunk; }
 
-// Channels of a workgroup: two a lane, one where two would leave half of a wave
-// idle.
-constexpr int64_t kNarrow = 64;
-
-template <int WIDE, typename F>
-void for_gated(const ssm_gated_dims* dims, const F& f) {
-  const bool narrow = dims->dim <= kNarrow;
-  if (dims->io_dtype == SSM_IO_BF16)
-    narrow ? f.template operator()<uint16_t, 1>() : f.template operator()<uint16_t, WIDE>();
-  else
-    narrow ? f.template operator()<float, 1>() : f.template operator()<float, WIDE>();
-}
-
-constexpr int kSteps = 8, kWaves = 8;          // of the kernels that walk
-// Of those whose workgroups share a row: steps of a wave, and the most channels of a
-// lane.
+// Steps of a lane, and the most channels of one.
 constexpr int kFwdSteps = 16, kFwdWide = 2;
 constexpr int kBwdSteps = 8, kBwdWide = 1;
 
-// How a row's steps are cut up, and the workspace that takes.  The forward's tiles
-// are 16 waves where that leaves kMany of them: half as many turns of the chain (us at
-// 16 / 8 waves, bf16: 8 x 4096 x 1024 67.5 / 71, 1 x 32768 x 2048 117 / 138; but 1 x 4096 x
-// 256, 32 tiles, 16.7 / 13.3).  The backward's are 8 (136 against 156 and 267 against
-// 288 us for the first two: at 16 a CU holds one workgroup, and nothing moves while it
-// computes).
-constexpr int64_t kMany = 512;
+// How a call is cut up, and the workspace that takes.
 struct Cut {
-  int64_t tiles, chains, tickets, words, waves;
+  int64_t V, groups, chains, waves, tiles, tickets, words;
   bool shared;
 };
-Cut cut_of(const ssm_gated_dims* dims, int64_t steps, int64_t V, int64_t most_waves) {
+
+// Up to kFew workgroups of 16 channels take whole short rows (us forward / backward:
+// 1 x 512 x 64 6.4 / 12.7 where tiles of a chain take 9.7 / 15.3, 1 x 512 x 2048 8.9 / 15.8
+// and 11.1 / 16.3; at 1024 of them, 8 x 512 x 2048, their 32-byte pieces cost 44 / 80
+// where tiles take 23.5 / 44).  Wider ones take rows of up to 16 waves' steps (256 x 129
+// x 512 forward 45.6, tiles 54).  Two channels a lane read twice as long pieces, 69 us
+// for 72 at 8 x 4096 x 1024 bf16, but for kFill tiles of 128 x 128 and more.
+// Tiles of 16 waves halve the chain's length where there are kMany of them at least (us
+// at 16 / 8 waves, bf16: 8 x 4096 x 1024 67.5 / 71, 1 x 32768 x 2048 117 / 138, but 1 x
+// 4096 x 256 16.7 / 13.3); backward, their registers leave one workgroup a CU (156 us for
+// 136 and 288 for 267).
+constexpr int64_t kFew = 512, kFill = 512, kMany = 512;
+Cut cut_of(const ssm_gated_dims* dims, int64_t steps, int64_t wide, int64_t most_waves) {
   Cut c;
-  c.chains = dims->batch * ((dims->dim + 64 * V - 1) / (64 * V));
+  const int64_t nb = dims->batch, L = dims->seqlen, nd = dims->dim;
+  c.tiles = 1, c.tickets = 0, c.words = 0, c.waves = 1, c.shared = false;
+  if (L <= 4 * 16 * 8 && nb * ((nd + 15) / 16) <= kFew) {
+    c.groups = 4, c.V = 1, c.chains = nb * ((nd + 15) / 16);
+    while (c.waves < 16 && 4 * 8 * c.waves < L) c.waves *= 2;
+    return c;
+  }
+  c.groups = 1;
+  // one channel a lane where two would leave half of a wave idle, or half of the GPU, or
+  // make two workgroups share a channel
+  const int64_t blocks = nb * ((nd + 127) / 128) * ((L + 127) / 128);
+  c.V = nd <= 64 || nd % 128 == 1 || blocks < kFill ? 1 : wide;
+  c.chains = nb * ((nd + 64 * c.V - 1) / (64 * c.V));
+  if (L <= 16 * steps) {
+    while (c.waves < 16 && steps * c.waves < L) c.waves *= 2;
+    return c;
+  }
+  c.shared = true;
   for (c.waves = most_waves;; c.waves = 8) {
-    c.tiles = (dims->seqlen + steps * c.waves - 1) / (steps * c.waves);
+    c.tiles = (L + steps * c.waves - 1) / (steps * c.waves);
     c.tickets = c.tiles * c.chains;
     if (c.waves == 8 || c.tickets >= kMany) break;
   }
-  c.shared = c.tiles >= 2 && c.tickets < (1 << 30);
-  c.words = c.shared ? 4 + 64 * V * c.chains * (2 * c.tiles + c.tiles / kSpan + 1) : 0;
+  c.words = 4 + 64 * c.V * c.chains * (2 * c.tiles + c.tiles / kSpan + 1);
   return c;
 }
-Cut fwd_cut(const ssm_gated_dims* dims) { return cut_of(dims, kFwdSteps, dims->dim <= kNarrow ? 1 : kFwdWide, 16); }
-Cut bwd_cut(const ssm_gated_dims* dims) { return cut_of(dims, kBwdSteps, dims->dim <= kNarrow ? 1 : kBwdWide, 8); }
+Cut fwd_cut(const ssm_gated_dims* dims) { return cut_of(dims, kFwdSteps, kFwdWide, 16); }
+Cut bwd_cut(const ssm_gated_dims* dims) { return cut_of(dims, kBwdSteps, kBwdWide, 8); }
+
+// Calls f.template operator()<IO, V>().
+template <int WIDE, typename F>
+void for_gated(const ssm_gated_dims* dims, int64_t V, const F& f) {
+  if (dims->io_dtype == SSM_IO_BF16)
+    V == 1 ? f.template operator()<uint16_t, 1>() : f.template operator()<uint16_t, WIDE>();
+  else
+    V == 1 ? f.template operator()<float, 1>() : f.template operator()<float, WIDE>();
+}
+
+// Calls f.template operator()<W>().
+template <typename F>
+void for_waves(int64_t waves, const F& f) {
+  switch (waves) {
+    case 1:
+      return f.template operator()<1>();
+    case 2:
+      return f.template operator()<2>();
+    case 4:
+      return f.template operator()<4>();
+    case 8:
+      return f.template operator()<8>();
+    default:
+      return f.template operator()<16>();
+  }
+}
 
 // Workgroups that take tiles: as many as the GPU holds at 128 registers a lane, 16
 // waves a CU.  More start only when others end, to find no tile left (three times
@@ -1062,11 +1132,12 @@ int ssm_gated_recurrence_fwd(ssm_scan_t handle, const ssm_gated_dims* dims, cons
   p.ag_ts = io->a_gate_time_stride, p.xg_bs = io->x_gate_batch_stride, p.xg_ts = io->x_gate_time_stride;
   p.y_bs = io->y_batch_stride, p.y_ts = io->y_time_stride;
   p.L = L, p.nd = static_cast<int32_t>(nd), p.n_states = static_cast<int32_t>(ns);
-  bool fits = true;
   const Cut cut = fwd_cut(dims);
+  if (!cut.shared && !grid_fits(cut.chains, 64 * 16)) return SSM_ERR_UNSUPPORTED;
+  if (cut.shared && cut.tickets >= (1 << 30)) return SSM_ERR_UNSUPPORTED;
+  p.n_cg = static_cast<int32_t>(cut.chains / nb);
   if (cut.shared) launch_fill(io->workspace, cut, s);
-  for_gated<kFwdWide>(dims, [&]<typename IO, int V>() {
-    p.n_cg = static_cast<int32_t>((nd + 64 * V - 1) / (64 * V));
+  for_gated<kFwdWide>(dims, cut.V, [&]<typename IO, int V>() {
     if (cut.shared) {
       const auto kernel = cut.waves == 16 ? gated_fwd_chain_kernel<IO, V, kFwdSteps, 16>
                                           : gated_fwd_chain_kernel<IO, V, kFwdSteps, 8>;
@@ -1075,12 +1146,12 @@ int ssm_gated_recurrence_fwd(ssm_scan_t handle, const ssm_gated_dims* dims, cons
                          static_cast<uint32_t>(cut.tickets));
       return;
     }
-    fits = grid_fits(nb * p.n_cg, 64 * kWaves);
-    if (fits)
-      hipLaunchKernelGGL((gated_fwd_kernel<IO, V, kSteps, kWaves>), dim3(static_cast<unsigned>(nb * p.n_cg)),
-                         dim3(64 * kWaves), 0, s, p);
+    for_waves(cut.waves, [&]<int W>() {
+      const auto kernel = cut.groups == 4 ? gated_fwd_row_kernel<IO, 1, 4, 8, W> : gated_fwd_row_kernel<IO, V, 1, kFwdSteps, W>;
+      hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>(cut.chains)), dim3(64 * W), 0, s, p);
+    });
   });
-  return fits ? launched() : SSM_ERR_UNSUPPORTED;
+  return launched();
 }
 
 int64_t ssm_gated_recurrence_bwd_workspace_bytes(const ssm_gated_dims* dims) {
@@ -1149,12 +1220,13 @@ int ssm_gated_recurrence_bwd(ssm_scan_t handle, const ssm_gated_dims* dims, cons
   p.dx_ts = io->dx_time_stride, p.dag_bs = io->da_gate_batch_stride, p.dag_ts = io->da_gate_time_stride;
   p.dxg_bs = io->dx_gate_batch_stride, p.dxg_ts = io->dx_gate_time_stride;
   p.L = L, p.nd = static_cast<int32_t>(nd), p.n_states = static_cast<int32_t>(ns);
-  bool fits = true;
   const Cut cut = bwd_cut(dims);
   p.ws += cut.words;
+  if (!cut.shared && !grid_fits(cut.chains, 64 * 16)) return SSM_ERR_UNSUPPORTED;
+  if (cut.shared && cut.tickets >= (1 << 30)) return SSM_ERR_UNSUPPORTED;
+  p.n_cg = static_cast<int32_t>(cut.chains / nb);
   if (cut.shared) launch_fill(io->workspace, cut, s);
-  for_gated<kBwdWide>(dims, [&]<typename IO, int V>() {
-    p.n_cg = static_cast<int32_t>((nd + 64 * V - 1) / (64 * V));
+  for_gated<kBwdWide>(dims, cut.V, [&]<typename IO, int V>() {
     if (cut.shared) {
       const auto kernel = gated_bwd_chain_kernel<IO, V, kBwdSteps, 8>;
       hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>(takers(cut, handle->cu_count))),
@@ -1162,12 +1234,11 @@ int ssm_gated_recurrence_bwd(ssm_scan_t handle, const ssm_gated_dims* dims, cons
                          static_cast<uint32_t>(cut.tickets), static_cast<uint32_t>(cut.tiles));
       return;
     }
-    fits = grid_fits(nb * p.n_cg, 64 * kWaves);
-    if (fits)
-      hipLaunchKernelGGL((gated_bwd_kernel<IO, V, kSteps, kWaves>), dim3(static_cast<unsigned>(nb * p.n_cg)),
-                         dim3(64 * kWaves), 0, s, p);
+    for_waves(cut.waves, [&]<int W>() {
+      const auto kernel = cut.groups == 4 ? gated_bwd_row_kernel<IO, 1, 4, 8, W> : gated_bwd_row_kernel<IO, V, 1, kBwdSteps, W>;
+      hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>(cut.chains)), dim3(64 * W), 0, s, p);
+    });
   });
-  if (!fits) return SSM_ERR_UNSUPPORTED;
   if (launched() != SSM_OK) return SSM_ERR_HIP;
   launch_reduce(p.ws, (cut.shared ? cut.tiles : 1) * nb, nd, GatedGrads{io->dA_log}, s);
   return launched();

@@ -116,6 +116,41 @@ def test_gated_large(io, B, L, D, lens):
         assert np.array_equal(bits(a), bits(b))
 
 
+@pytest.mark.parametrize("io,B,L,D,lens", [
+    ("bf16", 8, 8197, 130, [8197, 8197, 0, 1, 256, 4096, 4097, 8190]),  # tiles of 16 waves, two channels a lane
+    ("f32", 8, 8197, 130, None),
+    ("bf16", 17, 8200, 63, [8200 - 511 * b for b in range(17)]),        # the same, one channel
+    ("f32", 8, 4100, 129, [4100, 0, 0, 0, 0, 0, 0, 4099]),              # of eight, rows of padding alone between
+    ("bf16", 8, 4100, 130, None),
+    ("bf16", 1, 20000, 18, None),                                       # more than nine spans
+    *[("bf16", 530, L, 66, None) for L in (3, 17, 100)],                # whole rows, two channels a lane
+    ("f32", 530, 40, 66, [b % 43 - 1 for b in range(530)]),
+    ("bf16", 130, 250, 66, [b * 2 for b in range(130)]),
+    *[("f32", 513, L, 3, None) for L in (16, 31, 64, 120)],             # one
+    *[(io, 2, L, 19, None) for L in (32, 33, 65, 129, 257, 511, 512) for io in ("f32", "bf16")],  # sixteen channels
+])
+def test_gated_every_cut(io, B, L, D, lens):
+    """Every way that rows are cut up, in full and with rows that end early, run to run the same bits."""
+    c = gated_inputs(io, B, L, D, 161, carry=B != 8)
+    one, two = gated_both(c, i32(lens)), gated_both(c, i32(lens))
+    sync()
+    check_gated(io, c, lens, *one)
+    for a, b in zip((*one[:3], *one[3].values()), (*two[:3], *two[3].values())):
+        assert a is b is None or np.array_equal(bits(a), bits(b))
+
+
+@pytest.mark.parametrize("B,L,D", [(600, 20, 129), (5, 600, 257), (9, 4100, 129), (2, 100, 17), (520, 100, 67)])
+def test_gated_state_in_place(B, L, D):
+    """h_last in h0's place: read before it is written, also where lanes share a channel."""
+    import selective_state_space_scan_amd as ssm
+    c = gated_inputs("bf16", B, L, D, 162)
+    y, last = ssm.gated_recurrence_fwd(c["x"], c["ag"], c["xg"], c["A"], h0=c["h0"])[:2]
+    h = c["h0"].clone()
+    y2, last2 = ssm.gated_recurrence_fwd(c["x"], c["ag"], c["xg"], c["A"], h0=h, h_last=h)[:2]
+    assert last2.data_ptr() == h.data_ptr()
+    assert np.array_equal(bits(y), bits(y2)) and np.array_equal(bits(last), bits(h))
+
+
 @pytest.mark.parametrize("io", ["f32", "bf16"])
 def test_gated_lengths_around_every_edge(io):
     """A row for every length around waves, chunks and tiles."""
