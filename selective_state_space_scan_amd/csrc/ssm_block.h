@@ -144,7 +144,7 @@ struct VecIO<uint16_t> {
 };
 
 // V elements as they stand in memory: what a lane keeps of a load in flight,
-// unpacked when it is used.
+// unpacked when it is used.  load_once: past the caches, for what is not read again.
 template <typename IO, int V>
 struct RawVec;
 
@@ -152,6 +152,15 @@ template <int V>
 struct RawVec<float, V> {
   float v[V];
   __device__ __forceinline__ void load(const float* p) { VecIO<float>::load(p, v); }
+  __device__ __forceinline__ void load_once(const float* p) {
+    if constexpr (V == 4) {
+      const auto w = __builtin_nontemporal_load(reinterpret_cast<const VecIO<float>::vec4*>(p));
+      v[0] = w.x, v[1] = w.y, v[2] = w.z, v[3] = w.w;
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; ++i) v[i] = __builtin_nontemporal_load(p + i);
+    }
+  }
   __device__ __forceinline__ void unpack(float (&o)[V]) const {
 #pragma unroll
     for (int i = 0; i < V; ++i) o[i] = v[i];
@@ -163,6 +172,9 @@ struct RawVec<uint16_t, V> {
   typedef uint32_t vec __attribute__((ext_vector_type(V / 2), aligned(2)));
   vec v;
   __device__ __forceinline__ void load(const uint16_t* p) { v = *reinterpret_cast<const vec*>(p); }
+  __device__ __forceinline__ void load_once(const uint16_t* p) {
+    v = __builtin_nontemporal_load(reinterpret_cast<const vec*>(p));
+  }
   __device__ __forceinline__ void unpack(float (&o)[V]) const {
 #pragma unroll
     for (int i = 0; i < V / 2; ++i) o[2 * i] = VecIO<uint16_t>::lo(v[i]), o[2 * i + 1] = VecIO<uint16_t>::hi(v[i]);
@@ -175,6 +187,9 @@ struct RawVec<uint16_t, 2> {
   __device__ __forceinline__ void load(const uint16_t* p) {
     v = *reinterpret_cast<const VecIO<uint16_t>::vec1*>(p);
   }
+  __device__ __forceinline__ void load_once(const uint16_t* p) {
+    v = __builtin_nontemporal_load(reinterpret_cast<const VecIO<uint16_t>::vec1*>(p));
+  }
   __device__ __forceinline__ void unpack(float (&o)[2]) const {
     o[0] = VecIO<uint16_t>::lo(v), o[1] = VecIO<uint16_t>::hi(v);
   }
@@ -184,6 +199,7 @@ template <>
 struct RawVec<uint16_t, 1> {
   uint16_t v;
   __device__ __forceinline__ void load(const uint16_t* p) { v = *p; }
+  __device__ __forceinline__ void load_once(const uint16_t* p) { v = __builtin_nontemporal_load(p); }
   __device__ __forceinline__ void unpack(float (&o)[1]) const { o[0] = VecIO<uint16_t>::lo(v); }
 };
 

@@ -15,10 +15,10 @@
 //
 // 10 to 30 operations an element on 4 to 20 bytes: bound by memory.  A group is
 // held in registers between its one read and its one write, by as few lanes as
-// hold it at 16 bytes a lane (4 to 64 of a wave, several groups side by side;
-// wider ones at eight elements a lane, by up to 1024 lanes).  A lane keeps its
-// channels from row to row, so weights are read once and dw, db stay in
-// registers.
+// hold it at 16 bytes a lane (1 to 64 of a wave, several groups side by side), then
+// at 16 elements a lane, by up to 512 lanes.  A lane keeps its channels from row
+// to row, so weights are read once and dw, db stay in registers, and it asks for
+// its next row before it works on the one it has.
 
 #include <hip/hip_runtime.h>
 
@@ -76,17 +76,16 @@ template <int TPL, int K>
 __device__ __forceinline__ void lane_sums(float (&v)[K], float* lds) {
 #pragma unroll
   for (int k = 0; k < K; ++k) {
-    if constexpr (TPL <= 16) {
-      v[k] = group_sum<TPL>(v[k]);
-    } else {
-      float a, b;
-      v[k] = group_sum<16>(v[k]);
+    float a, b;
+    if constexpr (TPL == 2) v[k] += dpp_move<0xB1>(v[k]);
+    if constexpr (TPL >= 4) v[k] = group_sum<(TPL < 16 ? TPL : 16)>(v[k]);
+    if constexpr (TPL >= 32) {
       rows_swap16(v[k], a, b);
       v[k] = a + b;
-      if constexpr (TPL > 32) {
-        rows_swap32(v[k], a, b);
-        v[k] = a + b;
-      }
+    }
+    if constexpr (TPL >= 64) {
+      rows_swap32(v[k], a, b);
+      v[k] = a + b;
     }
   }
   if constexpr (TPL > 64) {
@@ -100,6 +99,7 @@ __device__ __forceinline__ void lane_sums(float (&v)[K], float* lds) {
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       v[k] = 0.0f;
+#pragma unroll
       for (int w = 0; w < TPL / 64; ++w) v[k] += lds[w * K + k];
     }
   }
@@ -122,8 +122,31 @@ __device__ __forceinline__ void act_slope(float u, bool silu, float& act, float&
   }
 }
 
-// Row `row` of a strided tensor.
-__device__ __forceinline__ int64_t row_at(const Strides& s, uint32_t b, uint32_t t) { return b * s.batch + t * s.time; }
+// A lane's rows, one after another at equal distances, as steps of rows of L.
+struct Walk {
+  uint32_t row, b, t, by, by_b, by_t, L;
+  __device__ __forceinline__ Walk(uint32_t first, uint32_t step, uint32_t len)
+      : row(first), b(first / len), t(first - first / len * len), by(step), by_b(step / len),
+        by_t(step - step / len * len), L(len) {}
+  // Whether the step passed one end of a row more than by_b.
+  __device__ __forceinline__ bool next() {
+    row += by, b += by_b, t += by_t;
+    const bool over = t >= L;
+    t -= over ? L : 0;
+    b += over ? 1 : 0;
+    return over;
+  }
+};
+// A strided tensor along them.
+template <typename IO>
+struct Along {
+  IO* p;
+  int64_t by, over;
+  __device__ __forceinline__ Along(const void* base, const Strides& s, const Walk& w, int64_t c0)
+      : p(static_cast<IO*>(const_cast<void*>(base)) + w.b * s.batch + w.t * s.time + c0),
+        by(w.by_b * s.batch + w.by_t * s.time), over(s.batch - w.L * s.time) {}
+  __device__ __forceinline__ void next(bool o) { p += by + (o ? over : 0); }
+};
 
 // Where a lane works: its group (of the row), its place in it, and the first of
 // its rows; workgroups take gpb groups of rpb rows at once.
@@ -143,47 +166,89 @@ __device__ __forceinline__ Place place(int32_t gpb, int32_t rpb, int32_t groups)
 }
 
 template <int TPL>
-constexpr int block_of = TPL > 256 ? TPL : 256;
+constexpr int block_of = TPL > 256 ? TPL : (TPL > 64 ? TPL : 256);
 
-// Piece k of a lane is the group's piece k * TPL + lane.
-template <typename IO, int TPL, int NV, int GATE>
+// A lane's pieces: piece k of it is the group's piece k * TPL + lane, moved back to
+// the last V elements where it would reach past the group's end.  Its first `skip`
+// elements are another's then: both compute and write the same for them, and they
+// count in one's sums.  A piece behind the end (skip = V) writes nothing.
+template <int V, int TPL, int NV>
+struct Pieces {
+  int32_t d[NV], skip[NV];
+  __device__ __forceinline__ Pieces(int lane, int32_t n) {
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      const int32_t first = (k * TPL + lane) * V;
+      d[k] = first < n - V ? first : n - V;
+      skip[k] = first - d[k] < V ? first - d[k] : V;
+    }
+  }
+};
+
+// Whether the row at w, whose length has been read, is not padding.
+__device__ __forceinline__ int32_t length_at(const int32_t* valid_len, const Walk& w, bool have) {
+  return valid_len == nullptr ? INT32_MAX : (have ? valid_len[w.b] : 0);
+}
+
+template <typename IO, int V, int TPL, int NV, int GATE>
 __global__ __launch_bounds__(block_of<TPL>) void group_fwd_kernel(const GroupParams prm) {
-  constexpr int V = VecIO<IO>::kWide, BLOCK = block_of<TPL>;
+  constexpr int BLOCK = block_of<TPL>;
   __shared__ float lds[BLOCK / 64 * 2];
   const Place at = place<TPL>(prm.gpb, prm.rpb, prm.groups);
   const int64_t c0 = static_cast<int64_t>(at.g) * prm.n;
-  int n[NV];
-  float w[NV][V], bias[NV][V];
+  const Pieces<V, TPL, NV> pc(at.lane, prm.n);
+  const uint32_t step = gridDim.y * prm.rpb;
+  Walk walk(blockIdx.y * prm.rpb + at.rs, step, prm.L), far = walk;
+  Along<const IO> x(prm.x, prm.xs, walk, c0), z(prm.z, prm.zs, walk, c0);
+  Along<IO> y(prm.y, prm.ys, walk, c0);
+  // the row to work on has been asked for, and the next one's length
+  RawVec<IO, V> rx[NV], rz[NV];
+  const auto ask = [&](bool valid) __attribute__((always_inline)) {
+    if (!valid || prm.n == 0) return;
 #pragma unroll
-  for (int k = 0; k < NV; ++k) {
-    const int d = (k * TPL + at.lane) * V;
-    n[k] = !at.active || d >= prm.n ? 0 : (prm.n - d < V ? prm.n - d : V);
-    load_n<float, V>(prm.w + c0 + d, n[k], w[k]);
-    load_n<float, V>(prm.bias + c0 + d, prm.bias == nullptr ? 0 : n[k], bias[k]);
+    for (int k = 0; k < NV; ++k) {
+      rx[k].load(x.p + pc.d[k]);
+      if constexpr (GATE != SSM_GATE_NONE) rz[k].load(z.p + pc.d[k]);
+    }
+  };
+  bool have = at.active && walk.row < prm.rows;
+  bool valid = have && static_cast<int32_t>(walk.t) < length_at(prm.valid_len, walk, have);
+  ask(valid);
+  far.next();
+  int32_t len = length_at(prm.valid_len, far, at.active && far.row < prm.rows);
+  float w[NV][V], bias[NV][V] = {};
+  if (at.active && prm.n > 0) {
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      VecIO<float>::load(prm.w + c0 + pc.d[k], w[k]);
+      if (prm.bias != nullptr) VecIO<float>::load(prm.bias + c0 + pc.d[k], bias[k]);
+    }
   }
   const bool silu = prm.silu != 0;
-  const uint32_t step = gridDim.y * prm.rpb;
   // every lane of a workgroup makes the same number of turns
   for (uint32_t base = blockIdx.y * prm.rpb; base < prm.rows; base += step) {
-    const uint32_t row = base + at.rs;
-    const bool have = at.active && row < prm.rows;
-    const uint32_t b = row / prm.L, t = row - b * prm.L;
-    const bool valid = have && (prm.valid_len == nullptr || static_cast<int64_t>(t) < prm.valid_len[b]);
-    const IO* x = static_cast<const IO*>(prm.x) + row_at(prm.xs, b, t) + c0;
-    const IO* z = static_cast<const IO*>(prm.z) + row_at(prm.zs, b, t) + c0;
-    IO* y = static_cast<IO*>(prm.y) + row_at(prm.ys, b, t) + c0;
     float v[NV][V], zv[NV][V];
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-      const int d = (k * TPL + at.lane) * V, m = valid ? n[k] : 0;
-      load_n<IO, V>(x + d, m, v[k]);
-      if constexpr (GATE != SSM_GATE_NONE) load_n<IO, V>(z + d, m, zv[k]);
+      rx[k].unpack(v[k]);
+      if constexpr (GATE != SSM_GATE_NONE) rz[k].unpack(zv[k]);
     }
-    if constexpr (GATE == SSM_GATE_BEFORE) {
+    const uint32_t row = walk.row;
+    const bool had = have, was = valid, over = walk.next();
+    x.next(over), z.next(over);
+    have = at.active && walk.row < prm.rows;
+    valid = have && static_cast<int32_t>(walk.t) < len;
+    ask(valid);
+    far.next();
+    len = length_at(prm.valid_len, far, at.active && far.row < prm.rows);
+    if constexpr (GATE != SSM_GATE_NONE) {
 #pragma unroll
       for (int k = 0; k < NV; ++k)
 #pragma unroll
-        for (int i = 0; i < V; ++i) v[k][i] *= act_of<IO>(zv[k][i], silu);
+        for (int i = 0; i < V; ++i) {
+          zv[k][i] = act_of<IO>(zv[k][i], silu);
+          if constexpr (GATE == SSM_GATE_BEFORE) v[k][i] *= zv[k][i];
+        }
     }
     float mean = 0.0f;
     if (!prm.rms) {
@@ -191,7 +256,7 @@ __global__ __launch_bounds__(block_of<TPL>) void group_fwd_kernel(const GroupPar
 #pragma unroll
       for (int k = 0; k < NV; ++k)
 #pragma unroll
-        for (int i = 0; i < V; ++i) s[0] += v[k][i];
+        for (int i = 0; i < V; ++i) s[0] += i >= pc.skip[k] ? v[k][i] : 0.0f;
       lane_sums<TPL>(s, lds);
       mean = s[0] * prm.inv_n;
     }
@@ -200,9 +265,8 @@ __global__ __launch_bounds__(block_of<TPL>) void group_fwd_kernel(const GroupPar
     for (int k = 0; k < NV; ++k)
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        // elements past the group's end stay zero
-        const float c = i < n[k] ? v[k][i] - mean : 0.0f;
-        v[k][i] = c;
+        v[k][i] -= mean;
+        const float c = i >= pc.skip[k] ? v[k][i] : 0.0f;
         s[0] += c;
         s[1] = __builtin_fmaf(c, c, s[1]);
       }
@@ -213,68 +277,89 @@ __global__ __launch_bounds__(block_of<TPL>) void group_fwd_kernel(const GroupPar
     float var = __builtin_fmaf(-off, off, s[1] * prm.inv_n);
     var = var < 0.0f ? 0.0f : var;
     const float rstd = 1.0f / __builtin_sqrtf(var + prm.eps);
-    if (!have) continue;
-    if (at.lane == 0) {
-      const int64_t st = static_cast<int64_t>(row) * prm.groups + at.g;
-      if (prm.mean != nullptr) prm.mean[st] = valid ? mean + off : 0.0f;
-      if (prm.rstd != nullptr) prm.rstd[st] = valid ? rstd : 0.0f;
-    }
-#pragma unroll
-    for (int k = 0; k < NV; ++k) {
-      const int d = (k * TPL + at.lane) * V;
-      float o[V];
-#pragma unroll
-      for (int i = 0; i < V; ++i) {
-        float p = __builtin_fmaf((v[k][i] - off) * rstd, w[k][i], bias[k][i]);
-        if constexpr (GATE == SSM_GATE_NONE) p = act_of<IO>(p, silu);
-        if constexpr (GATE == SSM_GATE_AFTER) p *= act_of<IO>(zv[k][i], silu);
-        o[i] = valid ? p : 0.0f;
+    if (had) {
+      if (at.lane == 0) {
+        const int64_t st = static_cast<int64_t>(row) * prm.groups + at.g;
+        if (prm.mean != nullptr) prm.mean[st] = was ? mean + off : 0.0f;
+        if (prm.rstd != nullptr) prm.rstd[st] = was ? rstd : 0.0f;
       }
-      store_n<IO, V>(y + d, n[k], o);
+#pragma unroll
+      for (int k = 0; k < NV; ++k) {
+        float o[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          float p = __builtin_fmaf((v[k][i] - off) * rstd, w[k][i], bias[k][i]);
+          if constexpr (GATE == SSM_GATE_NONE) p = act_of<IO>(p, silu);
+          if constexpr (GATE == SSM_GATE_AFTER) p *= zv[k][i];
+          o[i] = was ? p : 0.0f;
+        }
+        if (pc.skip[k] < V) VecIO<IO>::store(y.p + pc.d[k], o);
+      }
     }
+    y.next(over);
   }
 }
 
 // Each workgroup leaves one row of [dw | db] for its groups, the second pass
 // adds them.
-template <typename IO, int TPL, int NV, int GATE>
+template <typename IO, int V, int TPL, int NV, int GATE>
 __global__ __launch_bounds__(block_of<TPL>) void group_bwd_kernel(const GroupBwdParams prm) {
-  constexpr int V = VecIO<IO>::kWide, BLOCK = block_of<TPL>;
+  constexpr int BLOCK = block_of<TPL>;
   __shared__ float lds[BLOCK / 64 * 2];
   __shared__ float join[TPL < BLOCK ? BLOCK * V : 1];
   const Place at = place<TPL>(prm.gpb, prm.rpb, prm.groups);
   const int64_t c0 = static_cast<int64_t>(at.g) * prm.n, nd = static_cast<int64_t>(prm.groups) * prm.n;
-  int n[NV];
-  float w[NV][V], bias[NV][V], dw[NV][V] = {}, db[NV][V] = {};
+  const Pieces<V, TPL, NV> pc(at.lane, prm.n);
+  const uint32_t step = gridDim.y * prm.rpb;
+  Walk walk(blockIdx.y * prm.rpb + at.rs, step, prm.L), far = walk;
+  Along<const IO> x(prm.x, prm.xs, walk, c0), z(prm.z, prm.zs, walk, c0), dy(prm.dy, prm.dys, walk, c0);
+  Along<IO> dx(prm.dx, prm.dxs, walk, c0), dz(prm.dz, prm.dzs, walk, c0);
+  RawVec<IO, V> rx[NV], rz[NV], rg[NV];
+  float rm = 0.0f, rr = 0.0f;
+  const auto ask = [&](bool valid) __attribute__((always_inline)) {
+    rm = rr = 0.0f;
+    if (!valid) return;
+    const int64_t st = static_cast<int64_t>(walk.row) * prm.groups + at.g;
+    if (!prm.rms) rm = prm.mean[st];
+    rr = prm.rstd[st];
 #pragma unroll
-  for (int k = 0; k < NV; ++k) {
-    const int d = (k * TPL + at.lane) * V;
-    n[k] = !at.active || d >= prm.n ? 0 : (prm.n - d < V ? prm.n - d : V);
-    load_n<float, V>(prm.w + c0 + d, n[k], w[k]);
-    if constexpr (GATE != SSM_GATE_BEFORE)  // p is not wanted there
-      load_n<float, V>(prm.bias + c0 + d, prm.bias == nullptr ? 0 : n[k], bias[k]);
+    for (int k = 0; k < NV; ++k) {
+      rx[k].load_once(x.p + pc.d[k]);
+      if constexpr (GATE != SSM_GATE_NONE) rz[k].load_once(z.p + pc.d[k]);
+      rg[k].load_once(dy.p + pc.d[k]);
+    }
+  };
+  bool have = at.active && walk.row < prm.rows;
+  bool valid = have && static_cast<int32_t>(walk.t) < length_at(prm.valid_len, walk, have);
+  ask(valid);
+  far.next();
+  int32_t len = length_at(prm.valid_len, far, at.active && far.row < prm.rows);
+  float w[NV][V], bias[NV][V] = {}, dw[NV][V] = {}, db[NV][V] = {};
+  if (at.active) {
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      VecIO<float>::load(prm.w + c0 + pc.d[k], w[k]);
+      if constexpr (GATE != SSM_GATE_BEFORE)  // p is not wanted there
+        if (prm.bias != nullptr) VecIO<float>::load(prm.bias + c0 + pc.d[k], bias[k]);
+    }
   }
   const bool silu = prm.silu != 0;
-  const uint32_t step = gridDim.y * prm.rpb;
   for (uint32_t base = blockIdx.y * prm.rpb; base < prm.rows; base += step) {
-    const uint32_t row = base + at.rs;
-    const bool have = at.active && row < prm.rows;
-    const uint32_t b = row / prm.L, t = row - b * prm.L;
-    const bool valid = have && (prm.valid_len == nullptr || static_cast<int64_t>(t) < prm.valid_len[b]);
-    const IO* x = static_cast<const IO*>(prm.x) + row_at(prm.xs, b, t) + c0;
-    const IO* z = static_cast<const IO*>(prm.z) + row_at(prm.zs, b, t) + c0;
-    const IO* dy = static_cast<const IO*>(prm.dy) + row_at(prm.dys, b, t) + c0;
-    const int64_t st = static_cast<int64_t>(row) * prm.groups + at.g;
-    const float mean = valid && !prm.rms ? prm.mean[st] : 0.0f;
-    const float rstd = valid ? prm.rstd[st] : 0.0f;
     float xv[NV][V], zv[NV][V], g[NV][V], h[NV][V];
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-      const int d = (k * TPL + at.lane) * V, m = valid ? n[k] : 0;
-      load_n<IO, V>(x + d, m, xv[k]);
-      if constexpr (GATE != SSM_GATE_NONE) load_n<IO, V>(z + d, m, zv[k]);
-      load_n<IO, V>(dy + d, m, g[k]);
+      rx[k].unpack(xv[k]);
+      if constexpr (GATE != SSM_GATE_NONE) rz[k].unpack(zv[k]);
+      rg[k].unpack(g[k]);
     }
+    const float mean = rm, rstd = rr;
+    const bool had = have, was = valid, over = walk.next();
+    x.next(over), z.next(over), dy.next(over);
+    have = at.active && walk.row < prm.rows;
+    valid = have && static_cast<int32_t>(walk.t) < len;
+    ask(valid);
+    far.next();
+    len = length_at(prm.valid_len, far, at.active && far.row < prm.rows);
     float s[2] = {0.0f, 0.0f};
 #pragma unroll
     for (int k = 0; k < NV; ++k)
@@ -282,9 +367,8 @@ __global__ __launch_bounds__(block_of<TPL>) void group_bwd_kernel(const GroupBwd
       for (int i = 0; i < V; ++i) {
         float v = xv[k][i];
         if constexpr (GATE == SSM_GATE_BEFORE) v *= act_of<IO>(zv[k][i], silu);
-        // past the group's end h is 0, whatever the mean; a row that is not valid
-        // has rstd = 0 on zeros: both add nothing
-        const float xh = i < n[k] ? (v - mean) * rstd : 0.0f;
+        // what a row of padding finds in the registers counts as nothing
+        const float xh = was ? (v - mean) * rstd : 0.0f;
         h[k][i] = xh;
         float dp = g[k][i];
         if constexpr (GATE != SSM_GATE_BEFORE) {
@@ -298,38 +382,40 @@ __global__ __launch_bounds__(block_of<TPL>) void group_bwd_kernel(const GroupBwd
             zv[k][i] = dp * p * slope;  // dz
             dp *= act;
           }
-          if (!valid) dp = 0.0f;  // weights that are not finite
         }
+        dp = was ? dp : 0.0f;
         dw[k][i] = __builtin_fmaf(dp, xh, dw[k][i]);
         db[k][i] += dp;
         g[k][i] = dp * w[k][i];
-        s[0] = __builtin_fmaf(g[k][i], xh, s[0]);
-        s[1] += g[k][i];
+        const float k1 = i >= pc.skip[k] ? g[k][i] : 0.0f;
+        s[0] = __builtin_fmaf(k1, xh, s[0]);
+        s[1] += k1;
       }
     lane_sums<TPL>(s, lds);
-    if (!have) continue;
-    const float along = s[0] * prm.inv_n, off = prm.rms ? 0.0f : s[1] * prm.inv_n;
-    IO* dx = static_cast<IO*>(prm.dx) + row_at(prm.dxs, b, t) + c0;
-    IO* dz = static_cast<IO*>(prm.dz) + row_at(prm.dzs, b, t) + c0;
+    if (had) {
+      const float along = s[0] * prm.inv_n, off = prm.rms ? 0.0f : s[1] * prm.inv_n;
 #pragma unroll
-    for (int k = 0; k < NV; ++k) {
-      const int d = (k * TPL + at.lane) * V;
-      float o[V], oz[V];
+      for (int k = 0; k < NV; ++k) {
+        float o[V], oz[V];
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        float dv = (g[k][i] - off - h[k][i] * along) * rstd;
-        if constexpr (GATE == SSM_GATE_AFTER) oz[i] = valid ? zv[k][i] : 0.0f;
-        if constexpr (GATE == SSM_GATE_BEFORE) {
-          float act, slope;
-          act_slope<IO>(zv[k][i], silu, act, slope);
-          oz[i] = valid ? dv * xv[k][i] * slope : 0.0f;
-          dv *= act;
+        for (int i = 0; i < V; ++i) {
+          float dv = (g[k][i] - off - h[k][i] * along) * rstd;
+          if constexpr (GATE == SSM_GATE_AFTER) oz[i] = was ? zv[k][i] : 0.0f;
+          if constexpr (GATE == SSM_GATE_BEFORE) {
+            float act, slope;
+            act_slope<IO>(zv[k][i], silu, act, slope);
+            oz[i] = was ? dv * xv[k][i] * slope : 0.0f;
+            dv *= act;
+          }
+          o[i] = was ? dv : 0.0f;
         }
-        o[i] = valid ? dv : 0.0f;
+        if (pc.skip[k] < V) {
+          VecIO<IO>::store(dx.p + pc.d[k], o);
+          if constexpr (GATE != SSM_GATE_NONE) VecIO<IO>::store(dz.p + pc.d[k], oz);
+        }
       }
-      store_n<IO, V>(dx + d, n[k], o);
-      if constexpr (GATE != SSM_GATE_NONE) store_n<IO, V>(dz + d, n[k], oz);
     }
+    dx.next(over), dz.next(over);
   }
   // One row of sums a workgroup: [dw | db].
   float* out = prm.ws + static_cast<int64_t>(blockIdx.y) * (prm.with_bias ? 2 : 1) * nd + c0;
@@ -338,7 +424,6 @@ __global__ __launch_bounds__(block_of<TPL>) void group_bwd_kernel(const GroupBwd
     if (q == 1 && !prm.with_bias) break;
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-      const int d = (k * TPL + at.lane) * V;
       float sum[V];
 #pragma unroll
       for (int i = 0; i < V; ++i) sum[i] = q == 0 ? dw[k][i] : db[k][i];
@@ -355,7 +440,7 @@ __global__ __launch_bounds__(block_of<TPL>) void group_bwd_kernel(const GroupBwd
           }
         }
       }
-      if (at.rs == 0) store_n<float, V>(out + q * nd + d, n[k], sum);
+      if (at.active && at.rs == 0 && pc.skip[k] < V) VecIO<float>::store(out + q * nd + pc.d[k], sum);
     }
   }
 }
@@ -394,39 +479,54 @@ int check_group_dims(const ssm_group_norm_dims* dims) {
   return SSM_OK;
 }
 
-// Calls f.template operator()<IO, TPL, NV>(): the fewest lanes that hold a group at
-// one piece (16 bytes) a lane, up to a wave, and from there at eight elements.
+// Calls f.template operator()<IO, V, TPL, NV>(): the fewest lanes that hold a group at
+// one piece (16 bytes, or as much of it as a group has) a lane, up to a wave, and from
+// there at 16 elements.
 template <typename IO, typename F>
 void for_lanes(int64_t n, const F& f) {
-  constexpr int V = VecIO<IO>::kWide, E = 8;
-  if (n <= 4 * V)
-    f.template operator()<IO, 4, 1>();
+  constexpr int V = VecIO<IO>::kWide, E = 16;
+  if (n == 1)
+    f.template operator()<IO, 1, 1, 1>();
+  else if (n < 4)
+    f.template operator()<IO, 2, 2, 1>();
+  else if (n < V)
+    f.template operator()<IO, 4, 2, 1>();
+  else if (n == V)
+    f.template operator()<IO, V, 1, 1>();
+  else if (n <= 2 * V)
+    f.template operator()<IO, V, 2, 1>();
+  else if (n <= 4 * V)
+    f.template operator()<IO, V, 4, 1>();
   else if (n <= 8 * V)
-    f.template operator()<IO, 8, 1>();
+    f.template operator()<IO, V, 8, 1>();
   else if (n <= 16 * V)
-    f.template operator()<IO, 16, 1>();
+    f.template operator()<IO, V, 16, 1>();
   else if (n <= 32 * V)
-    f.template operator()<IO, 32, 1>();
+    f.template operator()<IO, V, 32, 1>();
   else if (n <= 64 * V)
-    f.template operator()<IO, 64, 1>();
+    f.template operator()<IO, V, 64, 1>();
+  else if (n <= 128 * V)
+    f.template operator()<IO, V, 64, 2>();
   else if (n <= 64 * E)
-    f.template operator()<IO, 64, E / V>();
+    f.template operator()<IO, V, 64, E / V>();
+  else if (n <= 128 * E)
+    f.template operator()<IO, V, 128, E / V>();
   else if (n <= 256 * E)
-    f.template operator()<IO, 256, E / V>();
+    f.template operator()<IO, V, 256, E / V>();
   else
-    f.template operator()<IO, 1024, E / V>();
+    f.template operator()<IO, V, 512, E / V>();
 }
 
 template <typename F>
 void for_group(const ssm_group_norm_dims* dims, const F& f) {
   const int64_t n = dims->dim / dims->groups;
-  const auto gated = [&]<typename IO, int TPL, int NV>() {
+  const auto gated = [&]<typename IO, int V, int TPL, int NV>() {
     if (dims->gate == SSM_GATE_NONE)
-      f.template operator()<IO, TPL, NV, SSM_GATE_NONE>();
+      f.template operator()<IO, V, TPL, NV, SSM_GATE_NONE>();
     else if (dims->gate == SSM_GATE_AFTER)
-      f.template operator()<IO, TPL, NV, SSM_GATE_AFTER>();
+      f.template operator()<IO, V, TPL, NV, SSM_GATE_AFTER>();
     else
-      f.template operator()<IO, TPL, NV, SSM_GATE_BEFORE>();
+      f.template operator()<IO, V, TPL, NV, SSM_GATE_BEFORE>();
   };
   if (dims->io_dtype == SSM_IO_BF16)
     for_lanes<uint16_t>(n, gated);
@@ -451,15 +551,20 @@ Cover cover(int64_t units, int64_t groups, int64_t rows, int64_t most) {
   return c;
 }
 
-constexpr int64_t kFwdGroups = 256 * 8, kBwdGroups = 256 * 3;
+// Waves, each lane with its row in flight: 24 a CU forward, 8 backward (us, 32768 x 1024
+// bf16 with a gate behind: 38 forward at 24, 40 at 12; backward 63 at 8, 67 at 12, 85
+// with 16 and loads through the caches, which hold what nothing reads again: 73 at 8;
+// 8192 channels a group 65 and 80).  Groups of up to four channels are bound by their
+// loads' latency rather: 65536 x 128 groups of 4 takes 103 at 16, 131 at 8.
+constexpr int64_t kFwdWaves = 256 * 24, kBwdWaves = 256 * 8, kSmallBwdWaves = 256 * 16;
 
 template <int TPL>
 Cover fwd_cover(const ssm_group_norm_dims* dims) {
-  return cover(block_of<TPL> / TPL, dims->groups, dims->batch * dims->seqlen, kFwdGroups);
+  return cover(block_of<TPL> / TPL, dims->groups, dims->batch * dims->seqlen, kFwdWaves * 64 / block_of<TPL>);
 }
-template <int TPL>
+template <int V, int TPL, int NV>
 Cover bwd_cover(const ssm_group_norm_dims* dims) {
-  return cover(block_of<TPL> / TPL, dims->groups, dims->batch * dims->seqlen, kBwdGroups);
+  return cover(block_of<TPL> / TPL, dims->groups, dims->batch * dims->seqlen, (V * NV <= 4 && TPL <= 2 ? kSmallBwdWaves : kBwdWaves) * 64 / block_of<TPL>);
 }
 
 }  // namespace
@@ -504,10 +609,10 @@ int ssm_group_norm_fwd(ssm_scan_t handle, const ssm_group_norm_dims* dims, const
   p.rows = static_cast<uint32_t>(rows), p.L = static_cast<uint32_t>(L);
   p.n = static_cast<int32_t>(nd / dims->groups), p.groups = static_cast<int32_t>(dims->groups);
   p.rms = dims->rms, p.silu = dims->silu, p.eps = dims->eps, p.inv_n = nd > 0 ? 1.0f / static_cast<float>(p.n) : 0.0f;
-  for_group(dims, [&]<typename IO, int TPL, int NV, int GATE>() {
+  for_group(dims, [&]<typename IO, int V, int TPL, int NV, int GATE>() {
     const Cover c = fwd_cover<TPL>(dims);
     p.gpb = static_cast<int32_t>(c.gpb), p.rpb = static_cast<int32_t>(c.rpb);
-    hipLaunchKernelGGL((group_fwd_kernel<IO, TPL, NV, GATE>),
+    hipLaunchKernelGGL((group_fwd_kernel<IO, V, TPL, NV, GATE>),
                        dim3(static_cast<unsigned>(c.columns), static_cast<unsigned>(c.stripes)), dim3(block_of<TPL>), 0,
                        static_cast<hipStream_t>(stream), p);
   });
@@ -517,8 +622,8 @@ int ssm_group_norm_fwd(ssm_scan_t handle, const ssm_group_norm_dims* dims, const
 int64_t ssm_group_norm_bwd_workspace_bytes(const ssm_group_norm_dims* dims) {
   if (check_group_dims(dims) != SSM_OK) return -1;
   int64_t bytes = 0;
-  for_group(dims, [&]<typename IO, int TPL, int NV, int GATE>() {
-    bytes = bwd_cover<TPL>(dims).stripes * 2 * dims->dim * 4;
+  for_group(dims, [&]<typename IO, int V, int TPL, int NV, int GATE>() {
+    bytes = bwd_cover<V, TPL, NV>(dims).stripes * 2 * dims->dim * 4;
   });
   return bytes;
 }
@@ -577,11 +682,11 @@ int ssm_group_norm_bwd(ssm_scan_t handle, const ssm_group_norm_dims* dims, const
   p.n = static_cast<int32_t>(nd / dims->groups), p.groups = static_cast<int32_t>(dims->groups);
   p.rms = dims->rms, p.silu = dims->silu, p.with_bias = io->dbias != nullptr, p.inv_n = 1.0f / static_cast<float>(p.n);
   int64_t stripes = 0;
-  for_group(dims, [&]<typename IO, int TPL, int NV, int GATE>() {
-    const Cover c = bwd_cover<TPL>(dims);
+  for_group(dims, [&]<typename IO, int V, int TPL, int NV, int GATE>() {
+    const Cover c = bwd_cover<V, TPL, NV>(dims);
     stripes = c.stripes;
     p.gpb = static_cast<int32_t>(c.gpb), p.rpb = static_cast<int32_t>(c.rpb);
-    hipLaunchKernelGGL((group_bwd_kernel<IO, TPL, NV, GATE>),
+    hipLaunchKernelGGL((group_bwd_kernel<IO, V, TPL, NV, GATE>),
                        dim3(static_cast<unsigned>(c.columns), static_cast<unsigned>(c.stripes)), dim3(block_of<TPL>), 0,
                        s, p);
   });
