@@ -150,8 +150,8 @@ __device__ __forceinline__ int wave_index() { return __builtin_amdgcn_readfirstl
 
 // V channels of a wave's steps of one tensor, loaded one step after another.  Unless
 // all of them are steps of the row (FULL), those past the last one read it again
-// (their values are not used).
-template <typename IO, int V, bool FULL>
+// (their values are not used).  ONCE: past the caches, where pieces are whole lines.
+template <typename IO, int V, bool FULL, bool ONCE>
 struct Feed {
   const IO* p;  // the same for the wave, where all its lanes take the same steps
   int64_t ts;
@@ -160,7 +160,11 @@ struct Feed {
       : p(static_cast<const IO*>(base) + b * bs + (FULL || t0 < last ? t0 : last) * step), ts(step), left(last - t0) {}
   __device__ __forceinline__ RawVec<IO, V> next(int t, int32_t d) {
     RawVec<IO, V> raw;
-    raw.load(lane_at(p, static_cast<uint32_t>(d) * static_cast<uint32_t>(sizeof(IO))));
+    const IO* at = lane_at(p, static_cast<uint32_t>(d) * static_cast<uint32_t>(sizeof(IO)));
+    if constexpr (ONCE)
+      raw.load_once(at);
+    else
+      raw.load(at);
     p += FULL || t < left ? ts : 0;
     return raw;
   }
@@ -168,10 +172,10 @@ struct Feed {
 
 // A wave's steps of both gates and x.  Loads come back in order: what the first step
 // takes is asked for first.
-template <bool FULL, typename IO, int V, int T, typename P>
+template <bool FULL, bool ONCE, typename IO, int V, int T, typename P>
 __device__ __forceinline__ void load_steps(const P& prm, int32_t b, int32_t t0, int32_t last, int32_t d,
                                            RawVec<IO, V> (&ra)[T], RawVec<IO, V> (&rg)[T], RawVec<IO, V> (&rx)[T]) {
-  Feed<IO, V, FULL> fa(prm.ag, prm.ag_bs, prm.ag_ts, b, t0, last), fg(prm.xg, prm.xg_bs, prm.xg_ts, b, t0, last),
+  Feed<IO, V, FULL, ONCE> fa(prm.ag, prm.ag_bs, prm.ag_ts, b, t0, last), fg(prm.xg, prm.xg_bs, prm.xg_ts, b, t0, last),
       fx(prm.x, prm.x_bs, prm.x_ts, b, t0, last);
 #pragma unroll
   for (int t = 0; t < T; ++t) ra[t] = fa.next(t, d), rg[t] = fg.next(t, d), rx[t] = fx.next(t, d);
@@ -479,7 +483,7 @@ __global__ __launch_bounds__(64 * W) void gated_fwd_row_kernel(const GatedParams
   VecIO<float>::load(prm.A_log + d, al);
   if (wave_index() == 0 && prm.h0 != nullptr) VecIO<float>::load(prm.h0 + bd, h);
   RawVec<IO, V> ra[T], rg[T], rx[T];
-  if (n > 0) load_steps<false>(prm, at.b, t0, n - 1, d, ra, rg, rx);
+  if (n > 0) load_steps<false, false>(prm, at.b, t0, n - 1, d, ra, rg, rx);
 #pragma unroll
   for (int v = 0; v < V; ++v) rate2[v] = expf(al[v]) * kLog2e, P[v] = 1.0f, S[v] = 0.0f;
 #pragma unroll
@@ -534,7 +538,7 @@ __global__ __launch_bounds__(64 * W) void gated_fwd_row_kernel(const GatedParams
 }
 
 // The same with the row's tiles on different workgroups.
-template <typename IO, int V, int T, int W>
+template <typename IO, int V, int T, int W, bool ONCE>
 __global__ __launch_bounds__(64 * W, 4) void gated_fwd_chain_kernel(const GatedParams, const ChainSpace sp,
                                                                  uint32_t tickets) {
   __shared__ ChainLds<V, W> lds;
@@ -558,7 +562,7 @@ __global__ __launch_bounds__(64 * W, 4) void gated_fwd_chain_kernel(const GatedP
       float al[V], rate2[V], a[T][V], u[T][V], P[V], S[V];
       RawVec<IO, V> ra[T], rg[T], rx[T];
       VecIO<float>::load(prm.A_log + d, al);
-      load_steps<FULL>(prm, b, t0, n - 1, d, ra, rg, rx);
+      load_steps<FULL, ONCE>(prm, b, t0, n - 1, d, ra, rg, rx);
 #pragma unroll
       for (int v = 0; v < V; ++v) rate2[v] = expf(al[v]) * kLog2e, P[v] = 1.0f, S[v] = 0.0f;
 #pragma unroll
@@ -644,8 +648,8 @@ __global__ __launch_bounds__(64 * W) void gated_bwd_row_kernel(const GatedBwdPar
   if (wave == W - 1 && prm.dh_last != nullptr) VecIO<float>::load(prm.dh_last + bd, g);
   RawVec<IO, V> ra[T], rg[T], rx[T], rd[T];
   if (n > 0) {
-    load_steps<false>(prm, at.b, t0, n - 1, d, ra, rg, rx);
-    Feed<IO, V, false> fd(prm.dy, prm.dy_bs, prm.dy_ts, at.b, t0, n - 1);
+    load_steps<false, false>(prm, at.b, t0, n - 1, d, ra, rg, rx);
+    Feed<IO, V, false, false> fd(prm.dy, prm.dy_bs, prm.dy_ts, at.b, t0, n - 1);
 #pragma unroll
     for (int t = 0; t < T; ++t) rd[t] = fd.next(t, d);
   }
@@ -745,7 +749,7 @@ __global__ __launch_bounds__(64 * W) void gated_bwd_row_kernel(const GatedBwdPar
 // The same with the row's tiles on different workgroups, the last ones first.  What
 // a step needs of the forward pass comes from its own tile alone; the chain carries
 // the state's gradient.  A wave's product of decays is one for both directions.
-template <typename IO, int V, int T, int W>
+template <typename IO, int V, int T, int W, bool ONCE>
 __global__ __launch_bounds__(64 * W, 4) void gated_bwd_chain_kernel(const GatedBwdParams, const ChainSpace sp,
                                                                  uint32_t tickets, uint32_t tiles) {
   static_assert(T * W % kChunk == 0, "a tile begins behind a kept state");
@@ -786,8 +790,8 @@ __global__ __launch_bounds__(64 * W, 4) void gated_bwd_chain_kernel(const GatedB
       float al[V], rate2[V], a[T][V], u[T][V], kx[T][V], ki[T][V], k1[T][V], r[T][V], P[V], S[V], h[V] = {};
       RawVec<IO, V> ra[T], rg[T], rx[T], rd[T];
       VecIO<float>::load(prm.A_log + d, al);
-      load_steps<FULL>(prm, b, t0, n - 1, d, ra, rg, rx);
-      Feed<IO, V, FULL> fd(prm.dy, prm.dy_bs, prm.dy_ts, b, t0, n - 1);
+      load_steps<FULL, ONCE>(prm, b, t0, n - 1, d, ra, rg, rx);
+      Feed<IO, V, FULL, ONCE> fd(prm.dy, prm.dy_bs, prm.dy_ts, b, t0, n - 1);
 #pragma unroll
       for (int t = 0; t < T; ++t) rd[t] = fd.next(t, d);
       if (tile > 0)
@@ -978,6 +982,15 @@ int64_t n_states(const ssm_gated_dims* dims) { return (dims->seqlen + kChunk - 1
 constexpr int kFwdSteps = 16, kFwdWide = 2;
 constexpr int kBwdSteps = 8, kBwdWide = 1;
 
+// Whether every piece of 64 channels begins and ends with a line of 128 bytes.  Tiles
+// read those past the caches (us, bf16 but for the last: 8 x 4096 x 1024 forward 66.2 for
+// 67.5 and backward 128 for 134, 16 x 8192 x 512 ragged 81 for 86, 8 x 4096 x 512 f32 58
+// for 62 and 97 for 110); a line that two pieces share is better kept (16 x 2048 x 1001:
+// 71.5 and 166 for 75 and 184).
+bool whole_lines(const Rows& r) {
+  return aligned(r.p, 128) && (r.n1 == 1 || r.s1 * r.e % 128 == 0) && (r.n0 == 1 || r.s0 * r.e % 128 == 0);
+}
+
 // How a call is cut up, and the workspace that takes.
 struct Cut {
   int64_t V, groups, chains, waves, tiles, tickets, words;
@@ -1092,6 +1105,7 @@ int ssm_gated_recurrence_fwd(ssm_scan_t handle, const ssm_gated_dims* dims, cons
   const int64_t e = dims->io_dtype == SSM_IO_BF16 ? 2 : 4;
   const int64_t need = ssm_gated_recurrence_fwd_workspace_bytes(dims);
   const bool empty = nb == 0 || nd == 0;
+  bool lines = false;
   if (!empty) {
     if (L > 0 && (io->x == nullptr || io->a_gate == nullptr || io->x_gate == nullptr || io->A_log == nullptr ||
                   io->y == nullptr))
@@ -1106,6 +1120,7 @@ int ssm_gated_recurrence_fwd(ssm_scan_t handle, const ssm_gated_dims* dims, cons
         !aligned(io->A_log, 4) || !aligned(io->valid_len, 4) || !aligned(io->h0, 4) || !aligned(io->h_last, 4) ||
         !aligned(io->chunk_states, 4) || !aligned(io->workspace, 8))
       return SSM_ERR_UNSUPPORTED;
+    lines = whole_lines(x) && whole_lines(ag) && whole_lines(xg);
     // the state may be updated in place: it is read before it is written
     const Rows in[] = {x, ag, xg, flat(io->A_log, nd * 4), flat(io->valid_len, nb * 4),
                        flat(io->h0, io->h0 == io->h_last ? 0 : nb * nd * 4)};
@@ -1139,8 +1154,10 @@ int ssm_gated_recurrence_fwd(ssm_scan_t handle, const ssm_gated_dims* dims, cons
   if (cut.shared) launch_fill(io->workspace, cut, s);
   for_gated<kFwdWide>(dims, cut.V, [&]<typename IO, int V>() {
     if (cut.shared) {
-      const auto kernel = cut.waves == 16 ? gated_fwd_chain_kernel<IO, V, kFwdSteps, 16>
-                                          : gated_fwd_chain_kernel<IO, V, kFwdSteps, 8>;
+      const auto kernel = cut.waves == 16 ? (lines ? gated_fwd_chain_kernel<IO, V, kFwdSteps, 16, true>
+                                                   : gated_fwd_chain_kernel<IO, V, kFwdSteps, 16, false>)
+                                          : (lines ? gated_fwd_chain_kernel<IO, V, kFwdSteps, 8, true>
+                                                   : gated_fwd_chain_kernel<IO, V, kFwdSteps, 8, false>);
       hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>(takers(cut, handle->cu_count))),
                          dim3(static_cast<unsigned>(64 * cut.waves)), 0, s, p, chain_space(io->workspace, cut, V),
                          static_cast<uint32_t>(cut.tickets));
@@ -1169,6 +1186,7 @@ int ssm_gated_recurrence_bwd(ssm_scan_t handle, const ssm_gated_dims* dims, cons
   const int64_t e = dims->io_dtype == SSM_IO_BF16 ? 2 : 4;
   const int64_t need = ssm_gated_recurrence_bwd_workspace_bytes(dims);
   const bool some = nb > 0 && L > 0;
+  bool lines = false;
   if (nd > 0) {
     if (io->dA_log == nullptr) return SSM_ERR_INVALID_ARG;
     if (some && (io->x == nullptr || io->a_gate == nullptr || io->x_gate == nullptr || io->A_log == nullptr ||
@@ -1190,6 +1208,7 @@ int ssm_gated_recurrence_bwd(ssm_scan_t handle, const ssm_gated_dims* dims, cons
     if (!aligned(io->A_log, 4) || !aligned(io->valid_len, 4) || !aligned(io->h0, 4) || !aligned(io->dh_last, 4) ||
         !aligned(io->chunk_states, 4) || !aligned(io->dA_log, 4) || !aligned(io->dh0, 4) || !aligned(io->workspace, 8))
       return SSM_ERR_UNSUPPORTED;
+    lines = whole_lines(x) && whole_lines(ag) && whole_lines(xg) && whole_lines(dy);
     const Rows in[] = {x, ag, xg, dy, flat(io->A_log, nd * 4), flat(io->valid_len, nb * 4), flat(io->h0, nb * nd * 4),
                        flat(io->dh_last, nb * nd * 4), flat(io->chunk_states, nb * ns * nd * 4)};
     const Rows out[] = {dx, dag, dxg, flat(io->dA_log, nd * 4), flat(io->dh0, nb * nd * 4),
@@ -1228,7 +1247,8 @@ int ssm_gated_recurrence_bwd(ssm_scan_t handle, const ssm_gated_dims* dims, cons
   if (cut.shared) launch_fill(io->workspace, cut, s);
   for_gated<kBwdWide>(dims, cut.V, [&]<typename IO, int V>() {
     if (cut.shared) {
-      const auto kernel = gated_bwd_chain_kernel<IO, V, kBwdSteps, 8>;
+      const auto kernel =
+          lines ? gated_bwd_chain_kernel<IO, V, kBwdSteps, 8, true> : gated_bwd_chain_kernel<IO, V, kBwdSteps, 8, false>;
       hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>(takers(cut, handle->cu_count))),
                          dim3(static_cast<unsigned>(64 * cut.waves)), 0, s, p, chain_space(io->workspace, cut, V),
                          static_cast<uint32_t>(cut.tickets), static_cast<uint32_t>(cut.tiles));
