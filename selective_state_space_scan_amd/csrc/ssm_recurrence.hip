@@ -101,28 +101,30 @@ __device__ __forceinline__ Gate gate_of(float ag, float xg, float rate2) {
   return g;
 }
 
-// What the backward takes of a step besides a and u: with g the state's gradient
-// and h the state in front,
-//     dx = g kx,  dx_gate = g u ki,  q = g (k1 - k2 h),  da_gate = q (1 - r)
-// k1 = s a^2 i x / c and k2 = s a go to 0 with s, and, where a is 0, for large s.
+// A channel's rate2.  Finite, so that it times r = 0, or s2 times a = 0, is no NaN.
+__device__ __forceinline__ float rate2_of(float a_log) {
+  const float r = expf(a_log) * kLog2e;
+  return r > 0x1p127f ? 0x1p127f : r;
+}
+
+// What the backward takes of a step besides a and u: with g the state's gradient, h the
+// state in front and rate = exp(A_log),
+//     dx = g kx,  dx_gate = g u ki,  q = rate g (k1 - r a h),  da_gate = q (1 - r)
+// k1 = r a^2 i x / c: where c is 0, so is rate.
 struct Back {
   float a, u, kx, ki, k1, r;
 };
-// k2
-__device__ __forceinline__ float k2_of(float a, float r, float rate2) {
-  return __builtin_fminf(rate2 * r, 0x1p127f) * kLn2 * a;
-}
 template <typename IO>
 __device__ __forceinline__ Back back_of(float x, float ag, float xg, float rate2) {
   Back b;
   const float r = gate_sigmoid<IO>(ag), i = gate_sigmoid<IO>(xg), s2 = rate2 * r;
   b.a = fast_exp2(-s2);
   const float c2 = one_minus_square(b.a, s2);
-  const float rc = c2 > 0.0f ? __builtin_amdgcn_rsqf(c2) : c2 * 0.0f, c = c2 * rc, ix = i * x;
+  const float rc = __builtin_amdgcn_rsqf(__builtin_fmaxf(c2, 0x1p-126f)), c = c2 * rc, ix = i * x;
   b.u = c * ix;
   b.kx = c * i;
   b.ki = 1.0f - i;
-  b.k1 = k2_of(b.a, r, rate2) * b.a * (rc * ix);
+  b.k1 = r * b.a * b.a * (rc * ix);
   b.r = r;
   return b;
 }
@@ -293,8 +295,8 @@ struct ChainLds {
 // every wave's pair (P, S) and publishes the tile's; it is called with the chain's
 // initial state in `h` for its first tile, which takes it into its pair, and zero
 // for the others.  The second waits for the pairs in front and the span's state, and
-// leaves in `h` the state in front of the wave's steps and in `out` the one behind
-// the tile.  pos: the tile's place in its chain; more: whether another follows.  The
+// leaves in `h` the state in front of the wave's steps and, in the wave of the tile's
+// last ones, in `out` the one behind the tile.  pos: the tile's place in its chain; more: whether another follows.  The
 // workgroup's next ticket is drawn here, where all wait anyway.
 template <int V, int W, bool REVERSE>
 __device__ __forceinline__ void join_begin(ChainLds<V, W>& lds, const ChainSpace& sp, int buf, int wave, uint32_t pos,
@@ -364,20 +366,32 @@ __device__ __forceinline__ void join_end(ChainLds<V, W>& lds, const ChainSpace& 
 #pragma unroll
     for (int v = 0; v < V; ++v) h[v] = __builtin_fmaf(lds.front[j][v][lane], h[v], lds.front[j][V + v][lane]);
   }
-  float own[V];
+  // through the waves in front, four pairs read at a time
+  const int mine_at = REVERSE ? W - 1 - wave : wave;
 #pragma unroll
-  for (int k = 0; k < W; ++k) {
-    const int w = REVERSE ? W - 1 - k : k;
+  for (int k0 = 0; k0 < W; k0 += 4) {
+    if (k0 >= mine_at) break;
+    float a[4][V], u[4][V];
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      if (w == wave) own[v] = h[v];
-      h[v] = __builtin_fmaf(mine[w][v][lane], h[v], mine[w][V + v][lane]);
+    for (int k = 0; k < 4; ++k) {
+      const int w = REVERSE ? W - 1 - (k0 + k) : k0 + k;
+#pragma unroll
+      for (int v = 0; v < V; ++v) a[k][v] = mine[w][v][lane], u[k][v] = mine[w][V + v][lane];
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (k0 + k < mine_at) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) h[v] = __builtin_fmaf(a[k][v], h[v], u[k][v]);
+      }
     }
   }
-  __builtin_amdgcn_s_setprio(0);
-  if (wave == 0 && more && before == kSpan - 1) publish<V>(sp.state<V>(span + 1, chain), h);
+  if (mine_at == W - 1) {
 #pragma unroll
-  for (int v = 0; v < V; ++v) out[v] = h[v], h[v] = own[v];
+    for (int v = 0; v < V; ++v) out[v] = __builtin_fmaf(mine[wave][v][lane], h[v], mine[wave][V + v][lane]);
+    if (more && before == kSpan - 1) publish<V>(sp.state<V>(span + 1, chain), out);
+  }
+  __builtin_amdgcn_s_setprio(0);
 }
 
 __global__ void chain_fill_kernel(uint32_t* p, int64_t n) {
@@ -485,7 +499,7 @@ __global__ __launch_bounds__(64 * W) void gated_fwd_row_kernel(const GatedParams
   RawVec<IO, V> ra[T], rg[T], rx[T];
   if (n > 0) load_steps<false, false>(prm, at.b, t0, n - 1, d, ra, rg, rx);
 #pragma unroll
-  for (int v = 0; v < V; ++v) rate2[v] = expf(al[v]) * kLog2e, P[v] = 1.0f, S[v] = 0.0f;
+  for (int v = 0; v < V; ++v) rate2[v] = rate2_of(al[v]), P[v] = 1.0f, S[v] = 0.0f;
 #pragma unroll
   for (int t = 0; t < T; ++t) {
     float xv[V], av[V], gv[V];
@@ -553,7 +567,6 @@ __global__ __launch_bounds__(64 * W, 4) void gated_fwd_chain_kernel(const GatedP
     const int32_t b = chain / prm.n_cg, cg = chain % prm.n_cg, tile = pos * (T * W), t0 = tile + wave * T;
     const int32_t first = (cg * 64 + lane) * V, d = first < prm.nd - V ? first : prm.nd - V;
     const bool mine = first < prm.nd;
-    const uint32_t off = static_cast<uint32_t>(d) * static_cast<uint32_t>(sizeof(IO));
     const int32_t n = length_of(prm.valid_len, b, prm.L);
     const int64_t bd = static_cast<int64_t>(b) * prm.nd + d;
     float h[V] = {}, out[V];
@@ -564,7 +577,7 @@ __global__ __launch_bounds__(64 * W, 4) void gated_fwd_chain_kernel(const GatedP
       VecIO<float>::load(prm.A_log + d, al);
       load_steps<FULL, ONCE>(prm, b, t0, n - 1, d, ra, rg, rx);
 #pragma unroll
-      for (int v = 0; v < V; ++v) rate2[v] = expf(al[v]) * kLog2e, P[v] = 1.0f, S[v] = 0.0f;
+      for (int v = 0; v < V; ++v) rate2[v] = rate2_of(al[v]), P[v] = 1.0f, S[v] = 0.0f;
 #pragma unroll
       for (int t = 0; t < T; ++t) {
         float xv[V], av[V], gv[V];
@@ -585,6 +598,10 @@ __global__ __launch_bounds__(64 * W, 4) void gated_fwd_chain_kernel(const GatedP
       join_end<V, W, false>(lds, sp, buf, wave, pos, chain, tile + T * W < n, h, out, ticket);
       buf ^= 1;
       const auto& prm = params_again<GatedParams>();
+      if (!mine) return;
+      // a new value, zero-extended here: stores at scalar addresses
+      uint32_t off = static_cast<uint32_t>(d) * static_cast<uint32_t>(sizeof(IO));
+      asm volatile("" : "+v"(off));
       IO* y = static_cast<IO*>(prm.y) + b * prm.y_bs + t0 * prm.y_ts;
 #pragma unroll
       for (int t = 0; t < T; ++t) {
@@ -595,10 +612,10 @@ __global__ __launch_bounds__(64 * W, 4) void gated_fwd_chain_kernel(const GatedP
           h[v] = __builtin_fmaf(a[t][v], h[v], u[t][v]);
           o[v] = valid ? h[v] : 0.0f;
         }
-        if (mine && (FULL || t0 + t < prm.L)) VecIO<IO>::store(lane_at(y, off), o);
+        if (FULL || t0 + t < prm.L) VecIO<IO>::store(lane_at(y, off), o);
         y += prm.y_ts;
       }
-      if (prm.states != nullptr && mine && (t0 + T) % kChunk == 0 && (t0 + T) / kChunk <= prm.n_states)
+      if (prm.states != nullptr && (t0 + T) % kChunk == 0 && (t0 + T) / kChunk <= prm.n_states)
         VecIO<float>::store(prm.states + (static_cast<int64_t>(b) * prm.n_states + (t0 + T) / kChunk - 1) * prm.nd + d, h);
     };
     if (tile + T * W <= n) {
@@ -623,11 +640,10 @@ __global__ __launch_bounds__(64 * W, 4) void gated_fwd_chain_kernel(const GatedP
     }
     const auto& end = params_again<GatedParams>();
     // the row's last tile (its first where it has no step) leaves the state
-    if (mine && (tile < n ? tile + T * W >= n : tile == 0)) {
-      if (wave == 0 && end.h_last != nullptr) VecIO<float>::store(end.h_last + bd, out);
+    if (wave == W - 1 && mine && (tile < n ? tile + T * W >= n : tile == 0)) {
+      if (end.h_last != nullptr) VecIO<float>::store(end.h_last + bd, out);
       if (end.states != nullptr) {
-        const int32_t c0 = tile < n ? (tile + T * W) / kChunk : 0;
-        for (int32_t c = c0 + wave; c < end.n_states; c += W)
+        for (int32_t c = tile < n ? (tile + T * W) / kChunk : 0; c < end.n_states; ++c)
           VecIO<float>::store(end.states + (static_cast<int64_t>(b) * end.n_states + c) * end.nd + d, out);
       }
     }
@@ -654,7 +670,7 @@ __global__ __launch_bounds__(64 * W) void gated_bwd_row_kernel(const GatedBwdPar
     for (int t = 0; t < T; ++t) rd[t] = fd.next(t, d);
   }
 #pragma unroll
-  for (int v = 0; v < V; ++v) rate2[v] = expf(al[v]) * kLog2e, P[v] = 1.0f, S[v] = 0.0f;
+  for (int v = 0; v < V; ++v) rate2[v] = rate2_of(al[v]), P[v] = 1.0f, S[v] = 0.0f;
 #pragma unroll
   for (int t = 0; t < T; ++t) {
     float xv[V], av[V], gv[V];
@@ -697,15 +713,17 @@ __global__ __launch_bounds__(64 * W) void gated_bwd_row_kernel(const GatedBwdPar
   __syncthreads();
 #pragma unroll
   for (int v = 0; v < V; ++v) h[v] = lds.front[at.q][cl][v], g[v] = back.front[at.q][cl][v];
-  // k1 becomes k1 - k2 h
+  // k1 becomes k1 - r a h
 #pragma unroll
   for (int t = 0; t < T; ++t)
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      k1[t][v] = __builtin_fmaf(-k2_of(a[t][v], r[t][v], rate2[v]), h[v], k1[t][v]);
+      k1[t][v] = __builtin_fmaf(-(r[t][v] * a[t][v]), h[v], k1[t][v]);
       h[v] = __builtin_fmaf(a[t][v], h[v], u[t][v]);
     }
-  float dA[V] = {};
+  float dA[V] = {}, rate[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) rate[v] = rate2[v] * kLn2;
   const uint32_t off = static_cast<uint32_t>(d) * static_cast<uint32_t>(sizeof(IO));
   IO* px = static_cast<IO*>(prm.dx) + at.b * prm.dx_bs + (t0 + T - 1) * prm.dx_ts;
   IO* pa = static_cast<IO*>(prm.dag) + at.b * prm.dag_bs + (t0 + T - 1) * prm.dag_ts;
@@ -720,7 +738,7 @@ __global__ __launch_bounds__(64 * W) void gated_bwd_row_kernel(const GatedBwdPar
       const float gt = g[v] + dv[v], q = gt * k1[t][v];
       ox[v] = valid ? gt * kx[t][v] : 0.0f;
       og[v] = valid ? gt * u[t][v] * ki[t][v] : 0.0f;
-      oa[v] = valid ? q * (1.0f - r[t][v]) : 0.0f;
+      oa[v] = valid ? q * __builtin_fmaf(-rate[v], r[t][v], rate[v]) : 0.0f;
       dA[v] += valid ? q : 0.0f;
       g[v] = valid ? gt * a[t][v] : g[v];
     }
@@ -734,7 +752,7 @@ __global__ __launch_bounds__(64 * W) void gated_bwd_row_kernel(const GatedBwdPar
   // the groups' sums of q, in order (every group has read its states by now, from
   // places of its own)
 #pragma unroll
-  for (int v = 0; v < V; ++v) lds.front[at.q][cl][v] = dA[v];
+  for (int v = 0; v < V; ++v) lds.front[at.q][cl][v] = dA[v] * rate[v];
   __syncthreads();
   if (at.mine && threadIdx.x < 64 / G) {
 #pragma unroll
@@ -780,7 +798,6 @@ __global__ __launch_bounds__(64 * W, 4) void gated_bwd_chain_kernel(const GatedB
     const int32_t b = chain / prm.n_cg, cg = chain % prm.n_cg, tile = k * (T * W), t0 = tile + wave * T;
     const int32_t first = (cg * 64 + lane) * V, d = first < prm.nd - V ? first : prm.nd - V;
     const bool mine = first < prm.nd;
-    const uint32_t off = static_cast<uint32_t>(d) * static_cast<uint32_t>(sizeof(IO));
     const int32_t n = length_of(prm.valid_len, b, prm.L);
     const int64_t bd = static_cast<int64_t>(b) * prm.nd + d;
     const uint32_t pos = (n + T * W - 1) / (T * W) - 1 - k;  // from the row's last tile with a step
@@ -799,7 +816,7 @@ __global__ __launch_bounds__(64 * W, 4) void gated_bwd_chain_kernel(const GatedB
       else if (prm.h0 != nullptr)
         VecIO<float>::load(prm.h0 + bd, h);
 #pragma unroll
-      for (int v = 0; v < V; ++v) rate2[v] = expf(al[v]) * kLog2e, P[v] = 1.0f, S[v] = 0.0f;
+      for (int v = 0; v < V; ++v) rate2[v] = rate2_of(al[v]), P[v] = 1.0f, S[v] = 0.0f;
 #pragma unroll
       for (int t = 0; t < T; ++t) {
         float xv[V], av[V], gv[V];
@@ -835,20 +852,27 @@ __global__ __launch_bounds__(64 * W, 4) void gated_bwd_chain_kernel(const GatedB
 #pragma unroll
         for (int v = 0; v < V; ++v) h[v] = __builtin_fmaf(lds.waves[buf][w][v][lane], h[v], sums[buf][w][v][lane]);
       }
-      // k1 becomes k1 - k2 h
+      // k1 becomes k1 - r a h
 #pragma unroll
       for (int t = 0; t < T; ++t)
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-          k1[t][v] = __builtin_fmaf(-k2_of(a[t][v], r[t][v], rate2[v]), h[v], k1[t][v]);
+          k1[t][v] = __builtin_fmaf(-(r[t][v] * a[t][v]), h[v], k1[t][v]);
           h[v] = __builtin_fmaf(a[t][v], h[v], u[t][v]);
         }
       join_end<V, W, true>(lds, sp, buf, wave, pos, chain, k > 0, g, out, ticket);
       buf ^= 1;
       const auto& prm = params_again<GatedBwdParams>();
+      if (!mine) return;
+      // a new value, zero-extended here: stores at scalar addresses
+      uint32_t off = static_cast<uint32_t>(d) * static_cast<uint32_t>(sizeof(IO));
+      asm volatile("" : "+v"(off));
       IO* px = static_cast<IO*>(prm.dx) + b * prm.dx_bs + (t0 + T - 1) * prm.dx_ts;
       IO* pa = static_cast<IO*>(prm.dag) + b * prm.dag_bs + (t0 + T - 1) * prm.dag_ts;
       IO* pg = static_cast<IO*>(prm.dxg) + b * prm.dxg_bs + (t0 + T - 1) * prm.dxg_ts;
+      float rate[V];
+#pragma unroll
+      for (int v = 0; v < V; ++v) rate[v] = rate2[v] * kLn2;
 #pragma unroll
       for (int t = T - 1; t >= 0; --t) {
         float dv[V], ox[V], oa[V], og[V];
@@ -859,18 +883,19 @@ __global__ __launch_bounds__(64 * W, 4) void gated_bwd_chain_kernel(const GatedB
           const float gt = g[v] + dv[v], q = gt * k1[t][v];
           ox[v] = valid ? gt * kx[t][v] : 0.0f;
           og[v] = valid ? gt * u[t][v] * ki[t][v] : 0.0f;
-          oa[v] = valid ? q * (1.0f - r[t][v]) : 0.0f;
+          oa[v] = valid ? q * __builtin_fmaf(-rate[v], r[t][v], rate[v]) : 0.0f;
           dA[v] += valid ? q : 0.0f;
           g[v] = valid ? gt * a[t][v] : g[v];
         }
-        if (mine && (FULL || t0 + t < prm.L)) {
+        if (FULL || t0 + t < prm.L) {
           VecIO<IO>::store(lane_at(px, off), ox);
           VecIO<IO>::store(lane_at(pa, off), oa);
           VecIO<IO>::store(lane_at(pg, off), og);
         }
         px -= prm.dx_ts, pa -= prm.dag_ts, pg -= prm.dxg_ts;
-
       }
+#pragma unroll
+      for (int v = 0; v < V; ++v) dA[v] *= rate[v];
     };
     if (tile + T * W <= n) {
       body.template operator()<true>();
@@ -954,7 +979,7 @@ __global__ __launch_bounds__(256) void gated_step_kernel(const GatedStepParams p
   float o[V];
 #pragma unroll
   for (int v = 0; v < V; ++v) {
-    const Gate g = gate_of<IO>(ag[v], xg[v], expf(al[v]) * kLog2e);
+    const Gate g = gate_of<IO>(ag[v], xg[v], rate2_of(al[v]));
     h[v] = __builtin_fmaf(g.a, h[v], g.c * g.i * x[v]);
     o[v] = active[0] ? h[v] : 0.0f;
   }
