@@ -205,9 +205,10 @@ __device__ __forceinline__ const __attribute__((address_space(4))) P& params_aga
 // on when the others come, so results are the same bits from run to run, and only
 // every kSpan-th tile is a step of the serial chain.
 //
-// Tiles are dealt by a counter, all chains' first tiles first: a tile waits only for
-// tiles with smaller numbers, a workgroup takes its own in order, so the smallest
-// unfinished one is always at work and never waits for one that is not: every wait ends.
+// Tiles are dealt by a counter, in runs of one or more, all chains' first tiles first: a
+// tile waits only for tiles with smaller numbers, a workgroup takes its own in order, so
+// the smallest unfinished one is always at work and never waits for one that is not:
+// every wait ends.
 //
 // Published words tell by themselves that they are there: a fill kernel sets all
 // to kEmpty, a NaN that is never published (it is replaced by another), and words
@@ -272,6 +273,9 @@ struct ChainSpace {
   float* pairs;   // [tile][chain][P, S][64 V]
   float* states;  // [span][chain][64 V]
   uint32_t chains;
+  uint32_t run;  // the logarithm of the tickets drawn at once
+  __device__ __forceinline__ bool last_of_run(uint32_t ticket) const { return (ticket + 1) >> run << run == ticket + 1; }
+  __device__ __forceinline__ uint32_t draw() const { return atomicAdd(counter, 1u) << run; }
   template <int V>
   __device__ __forceinline__ float* pair(uint32_t pos, uint32_t chain) const {
     return pairs + ((static_cast<int64_t>(pos) * chains + chain) * 2 * 64 + threadIdx.x % 64) * V;
@@ -339,7 +343,8 @@ __device__ __forceinline__ void join_end(ChainLds<V, W>& lds, const ChainSpace& 
   auto& mine = lds.waves[buf];
   const uint32_t span = pos / kSpan;
   const int before = static_cast<int>(pos % kSpan);  // tiles of the span in front of this one
-  if (threadIdx.x == 0) lds.ticket = atomicAdd(sp.counter, 1u);
+  const bool draw = sp.last_of_run(ticket);
+  if (draw && threadIdx.x == 0) lds.ticket = sp.draw();
   for (int j = wave; j <= before; j += W) {
     if (j < before) {
       const float* at = sp.pair<V>(span * kSpan + j, chain);
@@ -357,7 +362,7 @@ __device__ __forceinline__ void join_end(ChainLds<V, W>& lds, const ChainSpace& 
     }
   }
   __syncthreads();
-  ticket = __builtin_amdgcn_readfirstlane(lds.ticket);
+  ticket = draw ? __builtin_amdgcn_readfirstlane(lds.ticket) : ticket + 1;
   if (span > 0) {
 #pragma unroll
     for (int v = 0; v < V; ++v) h[v] = lds.state[v][lane];
@@ -392,6 +397,18 @@ __device__ __forceinline__ void join_end(ChainLds<V, W>& lds, const ChainSpace& 
     if (more && before == kSpan - 1) publish<V>(sp.state<V>(span + 1, chain), out);
   }
   __builtin_amdgcn_s_setprio(0);
+}
+
+// Zeros in the 64 V channels (`left` are there) of some rows, 16 bytes a lane, by
+// WAVES waves from the second on.
+template <typename IO, int V, int WAVES>
+__device__ __forceinline__ void zero_rows(IO* p, int64_t ts, int64_t rows, int64_t left) {
+  constexpr int K = VecIO<IO>::kWide, kPieces = 64 * V / K;
+  for (int i = threadIdx.x - 64; i < rows * kPieces; i += 64 * WAVES) {
+    const int c = i % kPieces * K;
+    const float zero[K] = {};
+    store_n<IO, K>(p + i / kPieces * ts + c, left - c < K ? static_cast<int>(left - c) : K, zero);
+  }
 }
 
 __global__ void chain_fill_kernel(uint32_t* p, int64_t n) {
@@ -557,7 +574,7 @@ __global__ __launch_bounds__(64 * W, 4) void gated_fwd_chain_kernel(const GatedP
                                                                  uint32_t tickets) {
   __shared__ ChainLds<V, W> lds;
   const int wave = wave_index(), lane = threadIdx.x % 64;
-  if (threadIdx.x == 0) lds.ticket = atomicAdd(sp.counter, 1u);
+  if (threadIdx.x == 0) lds.ticket = sp.draw();
   __syncthreads();
   uint32_t ticket = __builtin_amdgcn_readfirstlane(lds.ticket);
   __syncthreads();
@@ -625,18 +642,15 @@ __global__ __launch_bounds__(64 * W, 4) void gated_fwd_chain_kernel(const GatedP
     } else {
 #pragma unroll
       for (int v = 0; v < V; ++v) out[v] = h[v];
-      if (mine) {
-        IO* y = static_cast<IO*>(prm.y) + b * prm.y_bs;
-        const int32_t end = tile + T * W < prm.L ? tile + T * W : static_cast<int32_t>(prm.L);
-        for (int32_t t = t0; t < t0 + T && t < end; ++t) {
-          const float zero[V] = {};
-          VecIO<IO>::store(y + t * prm.y_ts + d, zero);
-        }
-      }
+      const int64_t at = static_cast<int64_t>(cg) * (64 * V);
       __syncthreads();  // this turn's ticket has been read
-      if (threadIdx.x == 0) lds.ticket = atomicAdd(sp.counter, 1u);
+      const bool draw = sp.last_of_run(ticket);
+      if (draw && threadIdx.x == 0) lds.ticket = sp.draw();
+      if (wave > 0)  // the first one would wait for its stores before it knows the ticket
+        zero_rows<IO, V, W - 1>(static_cast<IO*>(prm.y) + b * prm.y_bs + tile * prm.y_ts + at, prm.y_ts,
+                                prm.L - tile < T * W ? prm.L - tile : T * W, prm.nd - at);
       __syncthreads();
-      ticket = __builtin_amdgcn_readfirstlane(lds.ticket);
+      ticket = draw ? __builtin_amdgcn_readfirstlane(lds.ticket) : ticket + 1;
     }
     const auto& end = params_again<GatedParams>();
     // the row's last tile (its first where it has no step) leaves the state
@@ -774,12 +788,12 @@ __global__ __launch_bounds__(64 * W, 4) void gated_bwd_chain_kernel(const GatedB
   __shared__ ChainLds<V, W> lds;
   __shared__ float sums[2][W][V][64], dsum[2][W][V][64];
   const int wave = wave_index(), lane = threadIdx.x % 64;
-  // A tile's sums of q, one a wave, wait for the next barrier; then the first wave
+  // A tile's sums of q, one a wave, wait for the next barrier; then the last wave
   // adds them in order.
   float* sum_to = nullptr;
   int sum_buf = 0;
   const auto flush = [&]() __attribute__((always_inline)) {
-    if (wave == 0 && sum_to != nullptr) {
+    if (wave == W - 1 && sum_to != nullptr) {
       float t[V] = {};
 #pragma unroll
       for (int w = 0; w < W; ++w)
@@ -788,7 +802,7 @@ __global__ __launch_bounds__(64 * W, 4) void gated_bwd_chain_kernel(const GatedB
       VecIO<float>::store(sum_to, t);
     }
   };
-  if (threadIdx.x == 0) lds.ticket = atomicAdd(sp.counter, 1u);
+  if (threadIdx.x == 0) lds.ticket = sp.draw();
   __syncthreads();
   uint32_t ticket = __builtin_amdgcn_readfirstlane(lds.ticket);
   __syncthreads();
@@ -904,23 +918,21 @@ __global__ __launch_bounds__(64 * W, 4) void gated_bwd_chain_kernel(const GatedB
     } else {
 #pragma unroll
       for (int v = 0; v < V; ++v) out[v] = g[v];
-      if (mine) {
-        IO* dx = static_cast<IO*>(prm.dx) + b * prm.dx_bs;
-        IO* dag = static_cast<IO*>(prm.dag) + b * prm.dag_bs;
-        IO* dxg = static_cast<IO*>(prm.dxg) + b * prm.dxg_bs;
-        const int32_t end = tile + T * W < prm.L ? tile + T * W : static_cast<int32_t>(prm.L);
-        for (int32_t t = t0; t < t0 + T && t < end; ++t) {
-          const float zero[V] = {};
-          VecIO<IO>::store(dx + t * prm.dx_ts + d, zero);
-          VecIO<IO>::store(dag + t * prm.dag_ts + d, zero);
-          VecIO<IO>::store(dxg + t * prm.dxg_ts + d, zero);
-        }
-      }
+      const int64_t at = static_cast<int64_t>(cg) * (64 * V), rows = prm.L - tile < T * W ? prm.L - tile : T * W;
       __syncthreads();  // this turn's ticket has been read
       flush();
-      if (threadIdx.x == 0) lds.ticket = atomicAdd(sp.counter, 1u);
+      const bool draw = sp.last_of_run(ticket);
+      if (draw && threadIdx.x == 0) lds.ticket = sp.draw();
+      if (wave > 0) {  // the first one would wait for its stores before it knows the ticket
+        zero_rows<IO, V, W - 1>(static_cast<IO*>(prm.dx) + b * prm.dx_bs + tile * prm.dx_ts + at, prm.dx_ts, rows,
+                                prm.nd - at);
+        zero_rows<IO, V, W - 1>(static_cast<IO*>(prm.dag) + b * prm.dag_bs + tile * prm.dag_ts + at, prm.dag_ts, rows,
+                                prm.nd - at);
+        zero_rows<IO, V, W - 1>(static_cast<IO*>(prm.dxg) + b * prm.dxg_bs + tile * prm.dxg_ts + at, prm.dxg_ts, rows,
+                                prm.nd - at);
+      }
       __syncthreads();
-      ticket = __builtin_amdgcn_readfirstlane(lds.ticket);
+      ticket = draw ? __builtin_amdgcn_readfirstlane(lds.ticket) : ticket + 1;
     }
     const auto& end = params_again<GatedBwdParams>();
     if (wave == 0 && mine && k == 0 && end.dh0 != nullptr) VecIO<float>::store(end.dh0 + bd, out);
@@ -1018,7 +1030,7 @@ bool whole_lines(const Rows& r) {
 
 // How a call is cut up, and the workspace that takes.
 struct Cut {
-  int64_t V, groups, chains, waves, tiles, tickets, words;
+  int64_t V, groups, chains, waves, tiles, tickets, run, words;
   bool shared;
 };
 
@@ -1036,7 +1048,7 @@ constexpr int64_t kFew = 512, kFill = 512, kMany = 512;
 Cut cut_of(const ssm_gated_dims* dims, int64_t steps, int64_t wide, int64_t most_waves) {
   Cut c;
   const int64_t nb = dims->batch, L = dims->seqlen, nd = dims->dim;
-  c.tiles = 1, c.tickets = 0, c.words = 0, c.waves = 1, c.shared = false;
+  c.tiles = 1, c.tickets = 0, c.run = 0, c.words = 0, c.waves = 1, c.shared = false;
   if (L <= 4 * 16 * 8 && nb * ((nd + 15) / 16) <= kFew) {
     c.groups = 4, c.V = 1, c.chains = nb * ((nd + 15) / 16);
     while (c.waves < 16 && 4 * 8 * c.waves < L) c.waves *= 2;
@@ -1062,7 +1074,14 @@ Cut cut_of(const ssm_gated_dims* dims, int64_t steps, int64_t wide, int64_t most
   return c;
 }
 Cut fwd_cut(const ssm_gated_dims* dims) { return cut_of(dims, kFwdSteps, kFwdWide, 16); }
-Cut bwd_cut(const ssm_gated_dims* dims) { return cut_of(dims, kBwdSteps, kBwdWide, 8); }
+Cut bwd_cut(const ssm_gated_dims* dims) {
+  Cut c = cut_of(dims, kBwdSteps, kBwdWide, 8);
+  // One counter deals a run every 13 ns, whatever the tiles take: many are dealt in
+  // pairs (us, bf16: 1 x 32768 x 2048 234 for 256, 16 x 8192 x 512 ragged 169 for 220; with
+  // fewer, 8 x 4096 x 512 f32 97 for 96, 16 x 2048 x 1001 174 for 164).
+  c.run = c.tickets > 8192 ? 1 : 0;
+  return c;
+}
 
 // Calls f.template operator()<IO, V>().
 template <int WIDE, typename F>
@@ -1094,8 +1113,8 @@ void for_waves(int64_t waves, const F& f) {
 // waves a CU.  More start only when others end, to find no tile left (three times
 // as many: 74 us where these take 72).
 int64_t takers(const Cut& c, int64_t cus) {
-  const int64_t held = 16 / c.waves * cus;
-  return c.tickets < held ? c.tickets : held;
+  const int64_t held = 16 / c.waves * cus, runs = ((c.tickets - 1) >> c.run) + 1;
+  return runs < held ? runs : held;
 }
 
 ChainSpace chain_space(void* workspace, const Cut& c, int64_t V) {
@@ -1104,6 +1123,7 @@ ChainSpace chain_space(void* workspace, const Cut& c, int64_t V) {
   sp.pairs = static_cast<float*>(workspace) + 4;
   sp.states = sp.pairs + 2 * 64 * V * c.chains * c.tiles;
   sp.chains = static_cast<uint32_t>(c.chains);
+  sp.run = static_cast<uint32_t>(c.run);
   return sp;
 }
 void launch_fill(void* workspace, const Cut& c, hipStream_t s) {
@@ -1174,7 +1194,7 @@ int ssm_gated_recurrence_fwd(ssm_scan_t handle, const ssm_gated_dims* dims, cons
   p.L = L, p.nd = static_cast<int32_t>(nd), p.n_states = static_cast<int32_t>(ns);
   const Cut cut = fwd_cut(dims);
   if (!cut.shared && !grid_fits(cut.chains, 64 * 16)) return SSM_ERR_UNSUPPORTED;
-  if (cut.shared && cut.tickets >= (1 << 30)) return SSM_ERR_UNSUPPORTED;
+  if (cut.shared && cut.tickets >= (1 << 28)) return SSM_ERR_UNSUPPORTED;
   p.n_cg = static_cast<int32_t>(cut.chains / nb);
   if (cut.shared) launch_fill(io->workspace, cut, s);
   for_gated<kFwdWide>(dims, cut.V, [&]<typename IO, int V>() {
@@ -1267,7 +1287,7 @@ int ssm_gated_recurrence_bwd(ssm_scan_t handle, const ssm_gated_dims* dims, cons
   const Cut cut = bwd_cut(dims);
   p.ws += cut.words;
   if (!cut.shared && !grid_fits(cut.chains, 64 * 16)) return SSM_ERR_UNSUPPORTED;
-  if (cut.shared && cut.tickets >= (1 << 30)) return SSM_ERR_UNSUPPORTED;
+  if (cut.shared && cut.tickets >= (1 << 28)) return SSM_ERR_UNSUPPORTED;
   p.n_cg = static_cast<int32_t>(cut.chains / nb);
   if (cut.shared) launch_fill(io->workspace, cut, s);
   for_gated<kBwdWide>(dims, cut.V, [&]<typename IO, int V>() {

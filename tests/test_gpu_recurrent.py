@@ -123,6 +123,8 @@ def test_gated_large(io, B, L, D, lens):
     ("f32", 8, 4100, 129, [4100, 0, 0, 0, 0, 0, 0, 4099]),              # of eight, rows of padding alone between
     ("bf16", 8, 4100, 130, None),
     ("bf16", 1, 20000, 18, None),                                       # more than nine spans
+    ("bf16", 1, 2101, 16385, [1500]),                                   # backward tiles dealt in pairs, an odd number
+    ("f32", 2, 2090, 8200, [2090, 33]),
     *[("bf16", 530, L, 66, None) for L in (3, 17, 100)],                # whole rows, two channels a lane
     ("f32", 530, 40, 66, [b % 43 - 1 for b in range(530)]),
     ("bf16", 130, 250, 66, [b * 2 for b in range(130)]),
