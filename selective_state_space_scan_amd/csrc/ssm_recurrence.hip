@@ -1035,15 +1035,16 @@ struct Cut {
 };
 
 // Up to kFew workgroups of 16 channels take whole short rows (us forward / backward:
-// 1 x 512 x 64 6.4 / 12.7 where tiles of a chain take 9.7 / 15.3, 1 x 512 x 2048 8.9 / 15.8
+// 1 x 512 x 64 7.2 / 12.8 where tiles of a chain take 11 / 15.9, 1 x 512 x 2048 9.0 / 15.5
 // and 11.1 / 16.3; at 1024 of them, 8 x 512 x 2048, their 32-byte pieces cost 44 / 80
-// where tiles take 23.5 / 44).  Wider ones take rows of up to 16 waves' steps (256 x 129
-// x 512 forward 45.6, tiles 54).  Two channels a lane read twice as long pieces, 69 us
-// for 72 at 8 x 4096 x 1024 bf16, but for kFill tiles of 128 x 128 and more.
+// where tiles take 23 / 44).  Wider ones take rows of up to 16 waves' steps (256 x 129
+// x 512 forward 45.3, tiles 54).  Two bf16 channels a lane read pieces of 256 bytes, 65 us
+// for 78.5 at 8 x 4096 x 1024, but for kFill tiles of 128 x 128 and more; two of fp32
+// cost more registers than they give (102 us at one, 107 at two).
 // Tiles of 16 waves halve the chain's length where there are kMany of them at least (us
-// at 16 / 8 waves, bf16: 8 x 4096 x 1024 67.5 / 71, 1 x 32768 x 2048 117 / 138, but 1 x
-// 4096 x 256 16.7 / 13.3); backward, their registers leave one workgroup a CU (156 us for
-// 136 and 288 for 267).
+// at 16 / 8 waves, bf16: 8 x 4096 x 1024 65 / 68, 1 x 32768 x 2048 108 / 132; but with
+// 256 of them, 1 x 4096 x 256, 16.7 / 13.3).  Backward, their registers leave one
+// workgroup a CU, which took 15 and 8 % longer.
 constexpr int64_t kFew = 512, kFill = 512, kMany = 512;
 Cut cut_of(const ssm_gated_dims* dims, int64_t steps, int64_t wide, int64_t most_waves) {
   Cut c;
@@ -1058,7 +1059,7 @@ Cut cut_of(const ssm_gated_dims* dims, int64_t steps, int64_t wide, int64_t most
   // one channel a lane where two would leave half of a wave idle, or half of the GPU, or
   // make two workgroups share a channel
   const int64_t blocks = nb * ((nd + 127) / 128) * ((L + 127) / 128);
-  c.V = nd <= 64 || nd % 128 == 1 || blocks < kFill ? 1 : wide;
+  c.V = dims->io_dtype == SSM_IO_F32 || nd <= 64 || nd % 128 == 1 || blocks < kFill ? 1 : wide;
   c.chains = nb * ((nd + 64 * c.V - 1) / (64 * c.V));
   if (L <= 16 * steps) {
     while (c.waves < 16 && steps * c.waves < L) c.waves *= 2;
@@ -1086,10 +1087,10 @@ Cut bwd_cut(const ssm_gated_dims* dims) {
 // Calls f.template operator()<IO, V>().
 template <int WIDE, typename F>
 void for_gated(const ssm_gated_dims* dims, int64_t V, const F& f) {
-  if (dims->io_dtype == SSM_IO_BF16)
-    V == 1 ? f.template operator()<uint16_t, 1>() : f.template operator()<uint16_t, WIDE>();
+  if (dims->io_dtype == SSM_IO_F32)
+    f.template operator()<float, 1>();
   else
-    V == 1 ? f.template operator()<float, 1>() : f.template operator()<float, WIDE>();
+    V == 1 ? f.template operator()<uint16_t, 1>() : f.template operator()<uint16_t, WIDE>();
 }
 
 // Calls f.template operator()<W>().
@@ -1111,7 +1112,7 @@ void for_waves(int64_t waves, const F& f) {
 
 // Workgroups that take tiles: as many as the GPU holds at 128 registers a lane, 16
 // waves a CU.  More start only when others end, to find no tile left (three times
-// as many: 74 us where these take 72).
+// as many: backward 132 us where these take 125, 8 x 4096 x 1024 bf16).
 int64_t takers(const Cut& c, int64_t cus) {
   const int64_t held = 16 / c.waves * cus, runs = ((c.tickets - 1) >> c.run) + 1;
   return runs < held ? runs : held;
@@ -1193,7 +1194,7 @@ int ssm_gated_recurrence_fwd(ssm_scan_t handle, const ssm_gated_dims* dims, cons
   p.y_bs = io->y_batch_stride, p.y_ts = io->y_time_stride;
   p.L = L, p.nd = static_cast<int32_t>(nd), p.n_states = static_cast<int32_t>(ns);
   const Cut cut = fwd_cut(dims);
-  if (!cut.shared && !grid_fits(cut.chains, 64 * 16)) return SSM_ERR_UNSUPPORTED;
+  if (!cut.shared && !grid_fits(cut.chains, 64 * cut.waves)) return SSM_ERR_UNSUPPORTED;
   if (cut.shared && cut.tickets >= (1 << 28)) return SSM_ERR_UNSUPPORTED;
   p.n_cg = static_cast<int32_t>(cut.chains / nb);
   if (cut.shared) launch_fill(io->workspace, cut, s);
@@ -1286,7 +1287,7 @@ int ssm_gated_recurrence_bwd(ssm_scan_t handle, const ssm_gated_dims* dims, cons
   p.L = L, p.nd = static_cast<int32_t>(nd), p.n_states = static_cast<int32_t>(ns);
   const Cut cut = bwd_cut(dims);
   p.ws += cut.words;
-  if (!cut.shared && !grid_fits(cut.chains, 64 * 16)) return SSM_ERR_UNSUPPORTED;
+  if (!cut.shared && !grid_fits(cut.chains, 64 * cut.waves)) return SSM_ERR_UNSUPPORTED;
   if (cut.shared && cut.tickets >= (1 << 28)) return SSM_ERR_UNSUPPORTED;
   p.n_cg = static_cast<int32_t>(cut.chains / nb);
   if (cut.shared) launch_fill(io->workspace, cut, s);
