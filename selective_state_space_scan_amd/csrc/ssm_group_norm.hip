@@ -18,7 +18,9 @@
 // hold it at 16 bytes a lane (1 to 64 of a wave, several groups side by side), then
 // at 16 elements a lane, by up to 512 lanes.  A lane keeps its channels from row
 // to row, so weights are read once and dw, db stay in registers, and it asks for
-// its next row before it works on the one it has.
+// its next row before it works on the one it has (us, 32768 x 1024 bf16 with a gate:
+// forward 38 to 45, 52 without that; backward 61 to 65, with the sums' pass of 5; the
+// bytes of a copy's rate 40 and 66).
 
 #include <hip/hip_runtime.h>
 

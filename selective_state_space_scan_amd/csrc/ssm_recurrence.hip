@@ -19,6 +19,11 @@
 // behind (P', S') is (P P', P S' + S).  A lane folds the steps it holds into
 // one pair, a workgroup's waves join theirs in LDS, and every step is then
 // known from the state in front of its lane.
+//
+// 40 vector operations a step and channel forward and 75 backward, 6 of them
+// transcendental, on 8 and 14 bytes of bf16: about as long as the bytes take (us, 8 x
+// 4096 x 1024 bf16: 61 to 65 forward for 53 of bytes, 123 backward for 92; 1 x 32768 x
+// 2048: 108 for 104, 233 for 183; 8 x 4096 x 512 f32: 55 for 53, 95.5 for 92).
 
 #include <hip/hip_runtime.h>
 

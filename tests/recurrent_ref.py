@@ -31,7 +31,7 @@ def _gates(ag, xg, A_log, io):
     # exp(A_log) 2 U, its products with log2(e), r and ln 2, and the constants' own rounding
     es = er + 7 * U
     ea = s * es + 3 * U
-    # the series: q's error (condition at most 1), eight terms and what is left out; the difference: a^2's error
+    # the polynomial: its argument's error (condition at most 1), its steps and its distance; the difference: a^2's error
     near = es + 9 * U
     with np.errstate(divide="ignore", invalid="ignore"):
         far = np.where(c2 > 0, 2 * a * a / c2 * ea, 0) + 2 * U
