@@ -1042,7 +1042,9 @@ struct Cut {
 // Up to kFew workgroups of 16 channels take whole short rows (us forward / backward:
 // 1 x 512 x 64 7.2 / 12.8 where tiles of a chain take 11 / 15.9, 1 x 512 x 2048 9.0 / 15.5
 // and 11.1 / 16.3; at 1024 of them, 8 x 512 x 2048, their 32-byte pieces cost 44 / 80
-// where tiles take 23 / 44).  Wider ones take rows of up to 16 waves' steps (256 x 129
+// where tiles take 23 / 44); forward, half as many take rows of up to 1024 steps, 16 a lane
+// (1 x 600 x 64 8.1 for 11.8, 4 x 1024 x 1024 f32 20.8 for 23.7; 504 of them, 8 x 1000 x
+// 1000, 41 for 24.6).  Wider ones take rows of up to 16 waves' steps (256 x 129
 // x 512 forward 45.3, tiles 54).  Two bf16 channels a lane read pieces of 256 bytes, 65 us
 // for 78.5 at 8 x 4096 x 1024, but for kFill tiles of 128 x 128 and more; two of fp32
 // cost more registers than they give (102 us at one, 107 at two).
@@ -1055,7 +1057,7 @@ Cut cut_of(const ssm_gated_dims* dims, int64_t steps, int64_t wide, int64_t most
   Cut c;
   const int64_t nb = dims->batch, L = dims->seqlen, nd = dims->dim;
   c.tiles = 1, c.tickets = 0, c.run = 0, c.words = 0, c.waves = 1, c.shared = false;
-  if (L <= 4 * 16 * 8 && nb * ((nd + 15) / 16) <= kFew) {
+  if (nb * ((nd + 15) / 16) <= (L <= 4 * 16 * 8 ? kFew : (L <= 4 * 16 * steps ? kFew / 2 : 0))) {
     c.groups = 4, c.V = 1, c.chains = nb * ((nd + 15) / 16);
     while (c.waves < 16 && 4 * 8 * c.waves < L) c.waves *= 2;
     return c;
@@ -1215,7 +1217,9 @@ int ssm_gated_recurrence_fwd(ssm_scan_t handle, const ssm_gated_dims* dims, cons
       return;
     }
     for_waves(cut.waves, [&]<int W>() {
-      const auto kernel = cut.groups == 4 ? gated_fwd_row_kernel<IO, 1, 4, 8, W> : gated_fwd_row_kernel<IO, V, 1, kFwdSteps, W>;
+      auto kernel = cut.groups == 4 ? gated_fwd_row_kernel<IO, 1, 4, 8, W> : gated_fwd_row_kernel<IO, V, 1, kFwdSteps, W>;
+      if constexpr (W == 16)
+        if (cut.groups == 4 && L > 4 * 16 * 8) kernel = gated_fwd_row_kernel<IO, 1, 4, kFwdSteps, W>;
       hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>(cut.chains)), dim3(64 * W), 0, s, p);
     });
   });

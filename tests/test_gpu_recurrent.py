@@ -130,6 +130,7 @@ def test_gated_large(io, B, L, D, lens):
     ("bf16", 130, 250, 66, [b * 2 for b in range(130)]),
     *[("f32", 513, L, 3, None) for L in (16, 31, 64, 120)],             # one
     *[(io, 2, L, 19, None) for L in (32, 33, 65, 129, 257, 511, 512) for io in ("f32", "bf16")],  # sixteen channels
+    *[(io, 2, L, 35, [L, 530]) for L in (513, 1000, 1024) for io in ("f32", "bf16")],   # sixteen steps a lane
 ])
 def test_gated_every_cut(io, B, L, D, lens):
     """Every way that rows are cut up, in full and with rows that end early, run to run the same bits."""
