@@ -1040,7 +1040,7 @@ struct Cut {
 };
 
 // Up to kFew workgroups of 16 channels take whole short rows (us forward / backward:
-// 1 x 512 x 64 7.2 / 12.8 where tiles of a chain take 11 / 15.9, 1 x 512 x 2048 9.0 / 15.5
+// 1 x 512 x 64 7.2 / 9.1 where tiles of a chain take 11 / 15.9, 1 x 512 x 2048 9.0 / 13.1
 // and 11.1 / 16.3; at 1024 of them, 8 x 512 x 2048, their 32-byte pieces cost 44 / 80
 // where tiles take 23 / 44); forward, half as many take rows of up to 1024 steps, 16 a lane
 // (1 x 600 x 64 8.1 for 11.8, 4 x 1024 x 1024 f32 20.8 for 23.7; 504 of them, 8 x 1000 x
@@ -1295,7 +1295,10 @@ int ssm_gated_recurrence_bwd(ssm_scan_t handle, const ssm_gated_dims* dims, cons
   p.dxg_bs = io->dx_gate_batch_stride, p.dxg_ts = io->dx_gate_time_stride;
   p.L = L, p.nd = static_cast<int32_t>(nd), p.n_states = static_cast<int32_t>(ns);
   const Cut cut = bwd_cut(dims);
-  p.ws += cut.words;
+  // a workgroup that holds a whole row has all of its sums: with one row, they are the
+  // result (1 x 512 x 64 bf16 9.1 us, with the second pass 12.6)
+  const bool sums = cut.shared || nb > 1;
+  p.ws = sums ? p.ws + cut.words : io->dA_log;
   if (!cut.shared && !grid_fits(cut.chains, 64 * cut.waves)) return SSM_ERR_UNSUPPORTED;
   if (cut.shared && cut.tickets >= (1 << 28)) return SSM_ERR_UNSUPPORTED;
   p.n_cg = static_cast<int32_t>(cut.chains / nb);
@@ -1315,6 +1318,7 @@ int ssm_gated_recurrence_bwd(ssm_scan_t handle, const ssm_gated_dims* dims, cons
     });
   });
   if (launched() != SSM_OK) return SSM_ERR_HIP;
+  if (!sums) return SSM_OK;
   launch_reduce(p.ws, (cut.shared ? cut.tiles : 1) * nb, nd, GatedGrads{io->dA_log}, s);
   return launched();
 }
