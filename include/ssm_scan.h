@@ -574,7 +574,8 @@ int ssm_layer_norm_bwd(ssm_scan_t handle, const ssm_norm_dims* dims, const ssm_n
  *               need hold anything before the call.  NULL allowed where that
  *               is 0.  Calls that may run at the same time must not share it.
  *
- * Sizes are below 2^31, dim below 2^29 (SSM_ERR_UNSUPPORTED).  The conventions
+ * batch is below 2^31, seqlen below 2^31 - 65536 and dim below 2^29
+ * (SSM_ERR_UNSUPPORTED, as where a grid would be too large).  The conventions
  * are the scan's: host-side checks first, asynchronous, nothing allocated,
  * bitwise reproducible, fp32 arithmetic rounded once to the io dtype. */
 typedef struct ssm_gated_dims {
@@ -627,6 +628,8 @@ int ssm_gated_recurrence_fwd(ssm_scan_t handle, const ssm_gated_dims* dims, cons
  *  chunk_states the forward's (only the first ceil(seqlen / chunk) - 1 of a
  *               row are read; NULL allowed when seqlen <= chunk).
  *  dA_log       [dim] fp32;  dh0 [batch, dim] fp32 or NULL.
+ *               dim is at most 2^26 - 16 (SSM_ERR_UNSUPPORTED), unless batch
+ *               is 1 and seqlen at most 128.
  *  workspace    at least ssm_gated_recurrence_bwd_workspace_bytes(dims) bytes
  *               of device scratch (8-byte aligned), as for the forward. */
 typedef struct ssm_gated_bwd_io {
@@ -754,7 +757,8 @@ int ssm_group_norm_fwd(ssm_scan_t handle, const ssm_group_norm_dims* dims, const
  *               rms) and rstd as it returned them.
  *  dy           like y;  dx, dz like x and z with strides of their own (dz
  *               with a gate, required, and NULL without): +0 past valid_len.
- *  dweight      [dim] fp32;  dbias [dim] fp32 or NULL.
+ *  dweight      [dim] fp32;  dbias [dim] fp32 or NULL; both together of at
+ *               most 2^26 - 16 elements (SSM_ERR_UNSUPPORTED).
  *  workspace    at least ssm_group_norm_bwd_workspace_bytes(dims) bytes of
  *               device scratch (4-byte aligned), overwritten. */
 typedef struct ssm_group_norm_bwd_io {

@@ -489,6 +489,11 @@ __global__ __launch_bounds__(kReduceCols * kReduceLanes) void reduce_partials_ke
   }
 }
 
+// Whether that pass's grid takes so many columns.
+inline bool reduce_fits(int64_t cols) {
+  return grid_fits((cols + kReduceCols - 1) / kReduceCols, kReduceCols * kReduceLanes);
+}
+
 template <typename Out>
 inline void launch_reduce(const float* ws, int64_t parts, int64_t cols, const Out& out, hipStream_t s) {
   hipLaunchKernelGGL(reduce_partials_kernel<Out>, dim3(static_cast<unsigned>((cols + kReduceCols - 1) / kReduceCols)),

@@ -661,8 +661,7 @@ int ssm_causal_conv_bwd(ssm_scan_t handle, const ssm_conv_dims* dims, const ssm_
   if (all > kMaxSize) return SSM_ERR_UNSUPPORTED;
   const int64_t blocks = static_cast<int64_t>(all);
   const int64_t cols = (W + 1) * nd;
-  if (!grid_fits(blocks, 256) || !grid_fits((cols + kReduceCols - 1) / kReduceCols, kReduceCols * kReduceLanes))
-    return SSM_ERR_UNSUPPORTED;
+  if (!grid_fits(blocks, 256) || !reduce_fits(cols)) return SSM_ERR_UNSUPPORTED;
   for_conv(dims, [&]<typename IO, int TAPS, bool SILU>() {
     const auto kernel = t.V == 1 ? conv_bwd_kernel<IO, 1, TAPS, SILU> : conv_bwd_kernel<IO, kBwdVec, TAPS, SILU>;
     hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, s, p);

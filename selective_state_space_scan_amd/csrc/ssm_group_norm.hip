@@ -639,6 +639,7 @@ int ssm_group_norm_bwd(ssm_scan_t handle, const ssm_group_norm_dims* dims, const
   const int64_t e = dims->io_dtype == SSM_IO_BF16 ? 2 : 4;
   const int64_t need = ssm_group_norm_bwd_workspace_bytes(dims);
   const bool gated = dims->gate != SSM_GATE_NONE;
+  if (rows > 0 && nd > 0 && !reduce_fits((io->dbias != nullptr ? 2 : 1) * nd)) return SSM_ERR_UNSUPPORTED;
   if (nd > 0) {
     if (io->weight == nullptr || io->dweight == nullptr) return SSM_ERR_INVALID_ARG;
     if (rows > 0 && (gated != (io->z != nullptr) || gated != (io->dz != nullptr))) return SSM_ERR_INVALID_ARG;

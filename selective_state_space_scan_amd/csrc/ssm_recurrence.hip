@@ -1241,6 +1241,11 @@ int ssm_gated_recurrence_bwd(ssm_scan_t handle, const ssm_gated_dims* dims, cons
   const int64_t e = dims->io_dtype == SSM_IO_BF16 ? 2 : 4;
   const int64_t need = ssm_gated_recurrence_bwd_workspace_bytes(dims);
   const bool some = nb > 0 && L > 0;
+  const Cut cut = bwd_cut(dims);
+  // a workgroup that holds a whole row has all of its sums: with one row, they are the
+  // result (1 x 512 x 64 bf16 9.1 us, with the second pass 12.6)
+  const bool sums = cut.shared || nb > 1;
+  if (some && nd > 0 && sums && !reduce_fits(nd)) return SSM_ERR_UNSUPPORTED;
   bool lines = false;
   if (nd > 0) {
     if (io->dA_log == nullptr) return SSM_ERR_INVALID_ARG;
@@ -1294,10 +1299,6 @@ int ssm_gated_recurrence_bwd(ssm_scan_t handle, const ssm_gated_dims* dims, cons
   p.dx_ts = io->dx_time_stride, p.dag_bs = io->da_gate_batch_stride, p.dag_ts = io->da_gate_time_stride;
   p.dxg_bs = io->dx_gate_batch_stride, p.dxg_ts = io->dx_gate_time_stride;
   p.L = L, p.nd = static_cast<int32_t>(nd), p.n_states = static_cast<int32_t>(ns);
-  const Cut cut = bwd_cut(dims);
-  // a workgroup that holds a whole row has all of its sums: with one row, they are the
-  // result (1 x 512 x 64 bf16 9.1 us, with the second pass 12.6)
-  const bool sums = cut.shared || nb > 1;
   p.ws = sums ? p.ws + cut.words : io->dA_log;
   if (!cut.shared && !grid_fits(cut.chains, 64 * cut.waves)) return SSM_ERR_UNSUPPORTED;
   if (cut.shared && cut.tickets >= (1 << 28)) return SSM_ERR_UNSUPPORTED;

@@ -251,6 +251,39 @@ def test_rms_needs_no_mean():
     assert group_bwd(group_dims(rms=1), mean=None, **ODD["group_bwd"]) == UNSUPPORTED
 
 
+# Sizes at a limit, behind pointers so far apart that nothing overlaps: a call whose sizes are taken meets the NULL
+# handle (-1), the others -2.
+def far(op, dims, **kw):
+    n = dims.seqlen * dims.dim
+    names = dict(gated_fwd=("x", "a_gate", "x_gate", "y"), group_fwd=("x", "z", "y"), group_bwd=("dy", "x", "z", "dx", "dz"),
+                 gated_bwd=("x", "a_gate", "x_gate", "dy", "dx", "da_gate", "dx_gate"), gated_step=())[op]
+    io = {k: (i + 1) << 42 for i, k in enumerate(OPTIONAL[op] + REQUIRED[op] + ("workspace",))}
+    for k in names:
+        io.update({k + "_batch_stride": n, k + "_time_stride": dims.dim})
+    if "workspace" not in REQUIRED[op] + (("workspace",) if op == "gated_fwd" else ()):
+        del io["workspace"]
+    else:
+        io["workspace_bytes"] = 1 << 41
+    return CALLS[op](dims, **{**io, **kw})
+
+
+def test_columns_of_the_sums_fit_their_grid():
+    """A weight's gradient is summed by 1024 work-items for 16 columns, and a launch counts them in 32 bits."""
+    most = 2**26 - 16
+    for kw in (dict(batch=2, seqlen=1), dict(batch=1, seqlen=129)):
+        for dim, code in ((most, INVALID), (most + 1, UNSUPPORTED), (2**29 - 1, UNSUPPORTED)):
+            assert far("gated_bwd", gated_dims(dim=dim, **kw)) == code, (dim, kw)
+    # one short row has its sums without a second pass
+    assert far("gated_bwd", gated_dims(batch=1, seqlen=128, dim=most + 16)) == INVALID
+    for dim, dbias, code in ((most, None, INVALID), (most + 1, None, UNSUPPORTED), (most // 2, 1 << 52, INVALID),
+                             (most // 2 + 1, 1 << 52, UNSUPPORTED), (2**29 - 1, None, UNSUPPORTED)):
+        d = group_dims(batch=1, seqlen=1, dim=dim, groups=dim)
+        assert far("group_bwd", d, dbias=dbias) == code, (dim, dbias)
+    # sums over nothing take another pass
+    assert far("gated_bwd", gated_dims(batch=0, dim=most + 1)) == INVALID
+    assert far("group_bwd", group_dims(batch=0, dim=most + 1, groups=1 + most)) == INVALID
+
+
 def test_short_sequences_need_no_kept_states():
     n = ssm.gated_chunk_len()
     assert n == 64
