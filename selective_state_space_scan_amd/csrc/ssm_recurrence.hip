@@ -1134,9 +1134,16 @@ ChainSpace chain_space(void* workspace, const Cut& c, int64_t V) {
   sp.run = static_cast<uint32_t>(c.run);
   return sp;
 }
+int64_t fill_blocks(const Cut& c) { return (c.words / 4 + 255) / 256; }
 void launch_fill(void* workspace, const Cut& c, hipStream_t s) {
-  hipLaunchKernelGGL(chain_fill_kernel, dim3(static_cast<unsigned>((c.words / 4 + 255) / 256)), dim3(256), 0, s,
+  hipLaunchKernelGGL(chain_fill_kernel, dim3(static_cast<unsigned>(fill_blocks(c))), dim3(256), 0, s,
                      static_cast<uint32_t*>(workspace), c.words);
+}
+
+// Whether a call that is cut up like this can be launched: its grids, and tickets that
+// stay in 32 bits with those that are drawn behind the last.
+bool launchable(const Cut& c) {
+  return c.shared ? c.tickets < (1 << 28) && grid_fits(fill_blocks(c), 256) : grid_fits(c.chains, 64 * c.waves);
 }
 
 }  // namespace
@@ -1158,6 +1165,8 @@ int ssm_gated_recurrence_fwd(ssm_scan_t handle, const ssm_gated_dims* dims, cons
   const int64_t e = dims->io_dtype == SSM_IO_BF16 ? 2 : 4;
   const int64_t need = ssm_gated_recurrence_fwd_workspace_bytes(dims);
   const bool empty = nb == 0 || nd == 0;
+  const Cut cut = fwd_cut(dims);
+  if (!empty && L > 0 && !launchable(cut)) return SSM_ERR_UNSUPPORTED;
   bool lines = false;
   if (!empty) {
     if (L > 0 && (io->x == nullptr || io->a_gate == nullptr || io->x_gate == nullptr || io->A_log == nullptr ||
@@ -1200,9 +1209,6 @@ int ssm_gated_recurrence_fwd(ssm_scan_t handle, const ssm_gated_dims* dims, cons
   p.ag_ts = io->a_gate_time_stride, p.xg_bs = io->x_gate_batch_stride, p.xg_ts = io->x_gate_time_stride;
   p.y_bs = io->y_batch_stride, p.y_ts = io->y_time_stride;
   p.L = L, p.nd = static_cast<int32_t>(nd), p.n_states = static_cast<int32_t>(ns);
-  const Cut cut = fwd_cut(dims);
-  if (!cut.shared && !grid_fits(cut.chains, 64 * cut.waves)) return SSM_ERR_UNSUPPORTED;
-  if (cut.shared && cut.tickets >= (1 << 28)) return SSM_ERR_UNSUPPORTED;
   p.n_cg = static_cast<int32_t>(cut.chains / nb);
   if (cut.shared) launch_fill(io->workspace, cut, s);
   for_gated<kFwdWide>(dims, cut.V, [&]<typename IO, int V>() {
@@ -1245,7 +1251,7 @@ int ssm_gated_recurrence_bwd(ssm_scan_t handle, const ssm_gated_dims* dims, cons
   // a workgroup that holds a whole row has all of its sums: with one row, they are the
   // result (1 x 512 x 64 bf16 9.1 us, with the second pass 12.6)
   const bool sums = cut.shared || nb > 1;
-  if (some && nd > 0 && sums && !reduce_fits(nd)) return SSM_ERR_UNSUPPORTED;
+  if (some && nd > 0 && (!launchable(cut) || (sums && !reduce_fits(nd)))) return SSM_ERR_UNSUPPORTED;
   bool lines = false;
   if (nd > 0) {
     if (io->dA_log == nullptr) return SSM_ERR_INVALID_ARG;
@@ -1300,8 +1306,6 @@ int ssm_gated_recurrence_bwd(ssm_scan_t handle, const ssm_gated_dims* dims, cons
   p.dxg_bs = io->dx_gate_batch_stride, p.dxg_ts = io->dx_gate_time_stride;
   p.L = L, p.nd = static_cast<int32_t>(nd), p.n_states = static_cast<int32_t>(ns);
   p.ws = sums ? p.ws + cut.words : io->dA_log;
-  if (!cut.shared && !grid_fits(cut.chains, 64 * cut.waves)) return SSM_ERR_UNSUPPORTED;
-  if (cut.shared && cut.tickets >= (1 << 28)) return SSM_ERR_UNSUPPORTED;
   p.n_cg = static_cast<int32_t>(cut.chains / nb);
   if (cut.shared) launch_fill(io->workspace, cut, s);
   for_gated<kBwdWide>(dims, cut.V, [&]<typename IO, int V>() {

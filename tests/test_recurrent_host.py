@@ -284,6 +284,24 @@ def test_columns_of_the_sums_fit_their_grid():
     assert far("group_bwd", group_dims(batch=0, dim=most + 1, groups=1 + most)) == INVALID
 
 
+def test_tiles_and_the_words_between_them_fit_their_grids():
+    """Rows cut into tiles: a work-item clears four of the words that tiles publish, 64 or 128 channels of them also
+    where a row has one."""
+    for op, L, words in (("gated_fwd", 257, lambda B: 4 + 64 * B * 5),      # two tiles a row
+                         ("gated_bwd", 129, lambda B: 4 + 64 * B * 7)):     # three
+        most = max(B for B in range(2**34 // (words(1) - 4) - 8, 2**34 // (words(1) - 4) + 8)
+                   if (words(B) // 4 + 255) // 256 * 256 < 2**32)
+        for B, code in ((most, INVALID), (most + 1, UNSUPPORTED), (most * 2, UNSUPPORTED), (2**31 - 1, UNSUPPORTED)):
+            d = gated_dims(batch=B, seqlen=L, dim=1)
+            got = far(op, d, **{k: 0 for k in ("x_batch_stride", "a_gate_batch_stride", "x_gate_batch_stride")})
+            assert got == code, (op, B)
+    # whole rows: a workgroup each, and its work-items
+    for op in ("gated_fwd", "gated_bwd"):
+        for B, L, code in ((2**26 - 1, 2, INVALID), (2**26, 2, UNSUPPORTED), (2**31 - 1, 1, UNSUPPORTED),
+                           (2**22 - 1, 128, INVALID), (2**22, 128, INVALID if op == "gated_fwd" else UNSUPPORTED)):
+            assert far(op, gated_dims(batch=B, seqlen=L, dim=1)) == code, (op, B, L)
+
+
 def test_short_sequences_need_no_kept_states():
     n = ssm.gated_chunk_len()
     assert n == 64
