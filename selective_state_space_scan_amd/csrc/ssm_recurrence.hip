@@ -1167,6 +1167,9 @@ int ssm_gated_recurrence_fwd(ssm_scan_t handle, const ssm_gated_dims* dims, cons
   const bool empty = nb == 0 || nd == 0;
   const Cut cut = fwd_cut(dims);
   if (!empty && L > 0 && !launchable(cut)) return SSM_ERR_UNSUPPORTED;
+  // no steps: the state is copied
+  if (!empty && L == 0 && io->h_last != nullptr && io->h_last != io->h0 && !grid_fits((nb * nd + 255) / 256, 256))
+    return SSM_ERR_UNSUPPORTED;
   bool lines = false;
   if (!empty) {
     if (L > 0 && (io->x == nullptr || io->a_gate == nullptr || io->x_gate == nullptr || io->A_log == nullptr ||
@@ -1195,10 +1198,8 @@ int ssm_gated_recurrence_fwd(ssm_scan_t handle, const ssm_gated_dims* dims, cons
   hipStream_t s = static_cast<hipStream_t>(stream);
   if (L == 0) {
     if (io->h_last == nullptr || io->h_last == io->h0) return SSM_OK;
-    const int64_t blocks = (nb * nd + 255) / 256;
-    if (!grid_fits(blocks, 256)) return SSM_ERR_UNSUPPORTED;
-    hipLaunchKernelGGL(gated_copy_kernel, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, s, io->h0, io->h_last,
-                       nb * nd);
+    hipLaunchKernelGGL(gated_copy_kernel, dim3(static_cast<unsigned>((nb * nd + 255) / 256)), dim3(256), 0, s, io->h0,
+                       io->h_last, nb * nd);
     return launched();
   }
 
@@ -1252,6 +1253,8 @@ int ssm_gated_recurrence_bwd(ssm_scan_t handle, const ssm_gated_dims* dims, cons
   // result (1 x 512 x 64 bf16 9.1 us, with the second pass 12.6)
   const bool sums = cut.shared || nb > 1;
   if (some && nd > 0 && (!launchable(cut) || (sums && !reduce_fits(nd)))) return SSM_ERR_UNSUPPORTED;
+  if (nb > 0 && nd > 0 && L == 0 && io->dh0 != nullptr && !grid_fits((nb * nd + 255) / 256, 256))
+    return SSM_ERR_UNSUPPORTED;
   bool lines = false;
   if (nd > 0) {
     if (io->dA_log == nullptr) return SSM_ERR_INVALID_ARG;
@@ -1287,12 +1290,9 @@ int ssm_gated_recurrence_bwd(ssm_scan_t handle, const ssm_gated_dims* dims, cons
   if (!some) {  // sums over nothing; the state's gradient passes through
     hipLaunchKernelGGL(gated_copy_kernel, dim3(static_cast<unsigned>((nd + 255) / 256)), dim3(256), 0, s, nullptr,
                        io->dA_log, nd);
-    if (nb > 0 && io->dh0 != nullptr) {
-      const int64_t blocks = (nb * nd + 255) / 256;
-      if (!grid_fits(blocks, 256)) return SSM_ERR_UNSUPPORTED;
-      hipLaunchKernelGGL(gated_copy_kernel, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, s, io->dh_last, io->dh0,
-                         nb * nd);
-    }
+    if (nb > 0 && io->dh0 != nullptr)
+      hipLaunchKernelGGL(gated_copy_kernel, dim3(static_cast<unsigned>((nb * nd + 255) / 256)), dim3(256), 0, s,
+                         io->dh_last, io->dh0, nb * nd);
     return launched();
   }
   GatedBwdParams p;

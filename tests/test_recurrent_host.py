@@ -302,6 +302,17 @@ def test_tiles_and_the_words_between_them_fit_their_grids():
             assert far(op, gated_dims(batch=B, seqlen=L, dim=1)) == code, (op, B, L)
 
 
+def test_states_of_no_steps_fit_their_grid():
+    """Without steps the state, or its gradient, is copied by a work-item an element."""
+    for op in ("gated_fwd", "gated_bwd"):
+        for dim, code in ((2**22 - 256, INVALID), (2**22, UNSUPPORTED)):
+            assert far(op, gated_dims(batch=2**10, seqlen=0, dim=dim)) == code, (op, dim)
+    # nothing to copy
+    big = gated_dims(batch=2**10, seqlen=0, dim=2**22)
+    assert far("gated_fwd", big, h_last=None) == INVALID and far("gated_fwd", big, h0=1 << 50, h_last=1 << 50) == INVALID
+    assert far("gated_bwd", big, dh0=None) == INVALID
+
+
 def test_short_sequences_need_no_kept_states():
     n = ssm.gated_chunk_len()
     assert n == 64
