@@ -1091,6 +1091,11 @@ Cut bwd_cut(const ssm_gated_dims* dims) {
   return c;
 }
 
+// Whether the sums for dA_log take a second pass.  A workgroup that holds a whole row has
+// all of its sums: with one row, they are the result (1 x 512 x 64 bf16 9.1 us, with the
+// second pass 12.6).
+bool sums_apart(const Cut& c, const ssm_gated_dims* dims) { return c.shared || dims->batch > 1; }
+
 // Calls f.template operator()<IO, V>().
 template <int WIDE, typename F>
 void for_gated(const ssm_gated_dims* dims, int64_t V, const F& f) {
@@ -1237,7 +1242,7 @@ int64_t ssm_gated_recurrence_bwd_workspace_bytes(const ssm_gated_dims* dims) {
   if (check_gated_dims(dims) != SSM_OK) return -1;
   // the chains' words, then a row of sums for every tile that a workgroup took
   const Cut c = bwd_cut(dims);
-  return (c.words + (c.shared ? c.tiles : 1) * dims->batch * dims->dim) * 4;
+  return sums_apart(c, dims) ? (c.words + c.tiles * dims->batch * dims->dim) * 4 : 0;
 }
 
 int ssm_gated_recurrence_bwd(ssm_scan_t handle, const ssm_gated_dims* dims, const ssm_gated_bwd_io* io, void* stream) {
@@ -1249,9 +1254,7 @@ int ssm_gated_recurrence_bwd(ssm_scan_t handle, const ssm_gated_dims* dims, cons
   const int64_t need = ssm_gated_recurrence_bwd_workspace_bytes(dims);
   const bool some = nb > 0 && L > 0;
   const Cut cut = bwd_cut(dims);
-  // a workgroup that holds a whole row has all of its sums: with one row, they are the
-  // result (1 x 512 x 64 bf16 9.1 us, with the second pass 12.6)
-  const bool sums = cut.shared || nb > 1;
+  const bool sums = sums_apart(cut, dims);
   if (some && nd > 0 && (!launchable(cut) || (sums && !reduce_fits(nd)))) return SSM_ERR_UNSUPPORTED;
   if (nb > 0 && nd > 0 && L == 0 && io->dh0 != nullptr && !grid_fits((nb * nd + 255) / 256, 256))
     return SSM_ERR_UNSUPPORTED;
@@ -1260,7 +1263,8 @@ int ssm_gated_recurrence_bwd(ssm_scan_t handle, const ssm_gated_dims* dims, cons
     if (io->dA_log == nullptr) return SSM_ERR_INVALID_ARG;
     if (some && (io->x == nullptr || io->a_gate == nullptr || io->x_gate == nullptr || io->A_log == nullptr ||
                  io->dy == nullptr || io->dx == nullptr || io->da_gate == nullptr || io->dx_gate == nullptr ||
-                 (io->chunk_states == nullptr && L > kChunk) || io->workspace == nullptr || io->workspace_bytes < need))
+                 (io->chunk_states == nullptr && L > kChunk) ||
+                 (need > 0 && (io->workspace == nullptr || io->workspace_bytes < need))))
       return SSM_ERR_INVALID_ARG;
     const Rows x{io->x, nb, io->x_batch_stride, L, io->x_time_stride, nd, e};
     const Rows ag{io->a_gate, nb, io->a_gate_batch_stride, L, io->a_gate_time_stride, nd, e};
@@ -1324,7 +1328,7 @@ int ssm_gated_recurrence_bwd(ssm_scan_t handle, const ssm_gated_dims* dims, cons
   });
   if (launched() != SSM_OK) return SSM_ERR_HIP;
   if (!sums) return SSM_OK;
-  launch_reduce(p.ws, (cut.shared ? cut.tiles : 1) * nb, nd, GatedGrads{io->dA_log}, s);
+  launch_reduce(p.ws, cut.tiles * nb, nd, GatedGrads{io->dA_log}, s);
   return launched();
 }
 

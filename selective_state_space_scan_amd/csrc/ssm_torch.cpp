@@ -604,10 +604,12 @@ PyObject* gated_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const Tensor dA = fresh({nd}, at::kFloat, c.dev);
     Tensor d0;
     if (a[5] != Py_None) d0 = fresh({nb, nd}, at::kFloat, c.dev);
-    const Tensor ws = scratch(a[12], entry.gated_bwd_bytes(&c.dims), c.dev);
+    Tensor ws;
+    const int64_t bytes = entry.gated_bwd_bytes(&c.dims);
+    if (bytes != 0 || a[12] != Py_None) ws = scratch(a[12], bytes, c.dev);
     s.dy = dy.const_data_ptr(), s.dx = dx.data_ptr(), s.da_gate = dag.data_ptr(), s.dx_gate = dxg.data_ptr();
     s.dA_log = at_ptr<float>(dA), s.dh0 = at_ptr<float>(d0);
-    s.workspace = ws.data_ptr(), s.workspace_bytes = ws.numel();
+    s.workspace = at_ptr<void>(ws), s.workspace_bytes = ws.defined() ? ws.numel() : 0;
     s.dy_batch_stride = dy.stride(0), s.dy_time_stride = dy.stride(1);
     s.dx_batch_stride = dx.stride(0), s.dx_time_stride = dx.stride(1);
     s.da_gate_batch_stride = dag.stride(0), s.da_gate_time_stride = dag.stride(1);

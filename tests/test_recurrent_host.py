@@ -313,6 +313,20 @@ def test_states_of_no_steps_fit_their_grid():
     assert far("gated_bwd", big, dh0=None) == INVALID
 
 
+def test_one_short_row_takes_no_scratch_backward():
+    """Its sums are its gradient."""
+    need = ssm.lib().ssm_gated_recurrence_bwd_workspace_bytes
+    for L, dim in ((1, 1), (80, 24), (512, 64), (128, 9000), (0, 24)):
+        assert need(ctypes.byref(gated_dims(batch=1, seqlen=L, dim=dim))) == 0, (L, dim)
+    for B, L, dim in ((2, 80, 24), (1, 513, 64), (1, 129, 9000)):
+        assert need(ctypes.byref(gated_dims(batch=B, seqlen=L, dim=dim))) >= 4 * B * dim, (B, L, dim)
+    one = gated_dims(batch=1)
+    assert gated_bwd(one, workspace=None, workspace_bytes=0, **ODD["gated_bwd"]) == UNSUPPORTED
+    assert gated_bwd(one, workspace=None, workspace_bytes=0) == INVALID                   # the handle
+    assert gated_bwd(one, workspace=15 * MB + 4) == UNSUPPORTED                           # what is given is looked at
+    assert gated_bwd(one, workspace=1 * MB) == ALIAS
+
+
 def test_short_sequences_need_no_kept_states():
     n = ssm.gated_chunk_len()
     assert n == 64
