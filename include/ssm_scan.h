@@ -554,6 +554,10 @@ int ssm_layer_norm_bwd(ssm_scan_t handle, const ssm_norm_dims* dims, const ssm_n
  *
  *     a[t] = exp(-exp(A_log[d]) r[t]),   h[t] = a[t] h[t-1] + sqrt(1 - a[t]^2) i[t] x[t],   y[t] = h[t]
  *
+ * A sigmoid or 1 - a^2 below fp32's smallest normal number, 2^-126, counts as 0:
+ * the step keeps the state and lets nothing in, and no gradient reaches what it
+ * shuts out.  An infinite exp(A_log) counts as a finite one, 2^127 ln 2.
+ *
  *  x, a_gate, x_gate, y [batch, seqlen, dim] io dtype, dim fastest, rows and
  *               steps x_batch_stride and x_time_stride (...) elements apart
  *               (both gates are often the halves of one projection's output).
@@ -622,8 +626,7 @@ int ssm_gated_recurrence_fwd(ssm_scan_t handle, const ssm_gated_dims* dims, cons
  *  dy           like y;  dx, da_gate, dx_gate like x and the gates, with
  *               strides of their own; the gradients are +0 past valid_len.
  *               da_gate and dx_gate are those of the gates before their
- *               sigmoid.  Where s = exp(A_log) r underflows to 0 the decay's
- *               gradient is its limit 0.
+ *               sigmoid.
  *  dh_last      [batch, dim] fp32 or NULL (zero).
  *  chunk_states the forward's (only the first ceil(seqlen / chunk) - 1 of a
  *               row are read; NULL allowed when seqlen <= chunk).

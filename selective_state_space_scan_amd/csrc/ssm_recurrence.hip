@@ -115,7 +115,7 @@ __device__ __forceinline__ float rate2_of(float a_log) {
 // What the backward takes of a step besides a and u: with g the state's gradient, h the
 // state in front and rate = exp(A_log),
 //     dx = g kx,  dx_gate = g u ki,  q = rate g (k1 - r a h),  da_gate = q (1 - r)
-// k1 = r a^2 i x / c: where c is 0, so is rate.
+// k1 = r a^2 i x / c, and 0 where c is.
 struct Back {
   float a, u, kx, ki, k1, r;
 };
@@ -125,7 +125,8 @@ __device__ __forceinline__ Back back_of(float x, float ag, float xg, float rate2
   const float r = gate_sigmoid<IO>(ag), i = gate_sigmoid<IO>(xg), s2 = rate2 * r;
   b.a = fast_exp2(-s2);
   const float c2 = one_minus_square(b.a, s2);
-  const float rc = __builtin_amdgcn_rsqf(__builtin_fmaxf(c2, 0x1p-126f)), c = c2 * rc, ix = i * x;
+  // the forward's square root takes a subnormal c2 as 0
+  const float rc = c2 < 0x1p-126f ? 0.0f : __builtin_amdgcn_rsqf(c2), c = c2 * rc, ix = i * x;
   b.u = c * ix;
   b.kx = c * i;
   b.ki = 1.0f - i;
