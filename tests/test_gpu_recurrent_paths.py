@@ -73,6 +73,18 @@ def lens_of(B, L):
 
 # ---- against 64 bits -----------------------------------------------------------
 
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("L,lens", [(1, None), (9, [8]), (100, None), (128, [128]), (128, [0])])
+def test_one_short_row_of_many_channels(io, L, lens):
+    """A row that 64-channel workgroups hold: its sums are dA_log, without scratch."""
+    D = 8250
+    assert on_path("row64", io, 1, L, D) == "rows"
+    c = gated_inputs(io, 1, L, D, 302)
+    r = gated_both(c, i32(lens))
+    sync()
+    check_gated(io, c, lens, *r)
+
+
 @pytest.mark.parametrize("rate", [-82.0, -30.0, -12.0, 3.0, 20.0])
 @pytest.mark.parametrize("path,io,B,L,D", EDGES)
 def test_decays_of_every_size(path, io, B, L, D, rate):
@@ -114,3 +126,180 @@ def test_decays_at_their_ends(path, io, B, L, D):
     tol = (R.sig_err(xg, io) + 8 * R.U + (2.0**-8 if io == "bf16" else 0)) * np.abs(want)
     check("y", n64(y[..., ~keep]), want, tol)
     assert (g["dA_log"][~keep] == 0).all() and (g["da_gate"][..., ~keep] == 0).all()
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+def test_lengths_around_every_edge_of_tiles_and_spans(io):
+    lens = sorted({n + d for n in (0, 16, 64, 128, 256, 1024, 1088, 2048, 2112, 2176) for d in (-1, 0, 1) if n + d >= 0})
+    B, L, D = len(lens), 2200, 5
+    assert on_path((1, 8), io, B, L, D) == "tiles"
+    c = gated_inputs(io, B, L, D, 305)
+    r = gated_both(c, i32(lens))
+    sync()
+    check_gated(io, c, lens, *r)
+
+
+@pytest.mark.parametrize("path,io,B,L,D", [e for e in EDGES if isinstance(e[0], tuple)])
+def test_in_pieces(path, io, B, L, D):
+    """A sequence cut anywhere and carried on, the state updated in place, is the whole sequence within its counted
+    error."""
+    import torch
+    import selective_state_space_scan_amd as ssm
+    on_path(path, io, B, L, D)
+    c = gated_inputs(io, B, L, D, 306)
+    lens = lens_of(B, L)
+    (ry, rl, _), (ty, tl, _) = R.gated_fwd(n64(c["x"]), n64(c["ag"]), n64(c["xg"]), n64(c["A"]), lens, n64(c["h0"]), io)
+    for cut in (1, 64, 1100, L - 1):
+        h = c["h0"].clone()
+        ys = []
+        for part in (slice(0, cut), slice(cut, L)):
+            vl = i32([min(max(n - part.start, 0), part.stop - part.start) for n in lens])
+            before = h.clone()
+            ys.append(ssm.gated_recurrence_fwd(c["x"][:, part], c["ag"][:, part], c["xg"][:, part], c["A"], vl, h0=h,
+                                               h_last=h)[0])
+            assert all(same(h[b], before[b]) for b in range(B) if int(vl[b]) == 0)
+        sync()
+        check("y", n64(torch.cat(ys, 1)), ry, ty)
+        check("h_last", n64(h), rl, tl)
+
+
+# ---- bit by bit ----------------------------------------------------------------
+
+@pytest.mark.parametrize("path,io,B,L,D", EDGES)
+def test_padding_reaches_nothing(path, io, B, L, D):
+    """NaN, infinities and the type's lowest value past a row's end change no bit."""
+    import torch
+    on_path(path, io, B, L, D)
+    lens = lens_of(B, L) if B > 1 else [L // 2 - 10]
+    c = gated_inputs(io, B, L, D, 307)
+    want = outputs(gated_both(c, i32(lens)))
+    for b, n in enumerate(lens):
+        for t in (want[0], *want[3:6]):
+            assert not bits(t[b, n:]).any()   # +0
+    for bad in (float("nan"), float("inf"), torch.finfo(_dt(io)).min):
+        k = {n: t.clone() for n, t in c.items()}
+        for b, n in enumerate(lens):
+            for name in ("x", "ag", "xg", "dy"):
+                k[name][b, n:] = bad
+        assert all(same(a, b) for a, b in zip(outputs(gated_both(k, i32(lens))), want))
+
+
+@pytest.mark.parametrize("path,io,B,L,D", EDGES)
+def test_bad_values_stay_in_their_channel_and_row(path, io, B, L, D):
+    """NaNs, among them the one whose bits are all ones, which tiles never publish as it is, and infinities."""
+    import torch
+    on_path(path, io, B, L, D)
+    c = gated_inputs(io, B, L, D, 308)
+    good = outputs(gated_both(c))
+    at, cols = L // 2, (7, D - 1)
+    ok = torch.ones(D, dtype=torch.bool, device=DEV)
+    ok[list(cols)] = False
+    for name, value in [(n, v) for n in ("x", "ag", "xg", "dy", "h0", "dl") for v in ("nan", "ones")] + [
+            ("x", "inf"), ("h0", "inf")]:
+        k = {n: t.clone() for n, t in c.items()}
+        t = k[name]
+        where = t[0] if name in ("h0", "dl") else t[0, at]
+        if value == "ones":
+            where.view(torch.int32 if t.dtype == torch.float32 else torch.int16)[list(cols)] = -1
+        else:
+            where[list(cols)] = float(value)
+        r = outputs(gated_both(k))
+        for i, (a, b) in enumerate(zip(r, good)):
+            assert same(a[..., ok], b[..., ok]), (name, value, i)
+            if i != 6:   # dA_log has no rows
+                assert same(a[1:], b[1:]), (name, value, i)
+        y, dx = r[0][0][:, list(cols)], r[3][0][:, list(cols)]
+        first = 0 if name == "h0" else at
+        if name in ("x", "ag", "xg", "h0"):   # the state forgets none of them, and knows nothing of them before they come
+            assert (torch.isposinf(y[first:]) if value == "inf" else torch.isnan(y[first:])).all(), (name, value)
+            assert same(y[:first], good[0][0, :first][:, list(cols)]), (name, value)
+        if name in ("dy", "dl"):
+            assert torch.isnan(dx[:at + 1]).all() and same(y, good[0][0][:, list(cols)]), (name, value)
+
+
+@pytest.mark.parametrize("offset", [1, 3])
+@pytest.mark.parametrize("path,io,B,L,D", EDGES)
+def test_unaligned_views(path, io, B, L, D, offset):
+    on_path(path, io, B, L, D)
+    c = gated_inputs(io, B, L, D, 309)
+    o = {k: off(t, offset) for k, t in c.items()}
+    dx = off(c["x"], offset)
+    assert all(same(a, b) for a, b in zip(outputs(gated_both(c)), outputs(gated_both(o, dx=dx))))
+
+
+@pytest.mark.parametrize("path,io,B,L,D", EDGES)
+def test_time_major_and_repeated_inputs(path, io, B, L, D):
+    """Tensors as [L, B, D] buffers seen as [B, L, D]; inputs with stride 0."""
+    import torch
+    import selective_state_space_scan_amd as ssm
+    on_path(path, io, B, L, D)
+    c = gated_inputs(io, B, L, D, 310)
+    tm = lambda t: t.transpose(0, 1).contiguous().transpose(0, 1)  # noqa: E731
+    want = outputs(gated_both(c))
+    m = {k: tm(t) if t.dim() == 3 else t for k, t in c.items()}
+    assert all(same(a, b) for a, b in zip(outputs(gated_both(m, dx=tm(torch.zeros_like(c["x"])))), want))
+    y = tm(torch.zeros_like(c["x"]))
+    got = ssm.gated_recurrence_fwd(m["x"], m["ag"], m["xg"], m["A"], h0=m["h0"], y=y)
+    assert got[0] is y and same(y, want[0]) and same(got[1], want[1])
+    r = dict(c, x=c["x"][:1].expand(B, L, D), ag=c["ag"][:, :1].expand(B, L, D), dy=c["dy"][:1, :1].expand(B, L, D))
+    s = {k: t.contiguous() for k, t in r.items()}
+    assert all(same(a, b) for a, b in zip(outputs(gated_both(r)), outputs(gated_both(s))))
+
+
+def test_streams_of_tiles():
+    """Tiles on another stream, and on two at once."""
+    import torch
+    assert on_path((1, 8), "bf16", 3, 2500, 136) == "tiles"
+    sets = [_all_ops(311, 2500), _all_ops(321, 2500)]
+    want = [{k: [t.clone() for t in f()] for k, f in ops} for ops in sets]
+    sync()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for name, f in sets[0]:
+        for how in (streams[0], streams[0].cuda_stream):
+            got = f(how)
+            streams[0].synchronize()
+            assert all(torch.equal(a, b) for a, b in zip(got, want[0][name])), name
+    got = [{}, {}]
+    for _ in range(5):
+        for i in (0, 1):
+            for name, f in sets[i]:
+                got[i][name] = f(streams[i])
+    sync()
+    for i in (0, 1):
+        for name in want[i]:
+            assert all(torch.equal(a, b) for a, b in zip(got[i][name], want[i][name])), (i, name)
+
+
+# ---- limits --------------------------------------------------------------------
+
+def test_the_most_columns_that_are_summed():
+    """The backward's widest calls: their last columns are those of a call on them alone; one more is refused."""
+    import torch
+    import selective_state_space_scan_amd as ssm
+    D, n = 2**26 - 16, 48
+    x = torch.empty((1, 1, D), dtype=torch.bfloat16, device=DEV)
+    x.view(torch.int16).random_(0x3f00, 0x3fff)   # 0.5 to 2
+    A = torch.linspace(-5, 1, D, device=DEV)
+    two = x.expand(2, 1, D)
+    g = ssm.gated_recurrence_bwd(two, two, two, A, None, two, None)
+    last = two[..., D - n:]
+    r = ssm.gated_recurrence_bwd(last, last, last, A[D - n:], None, last, None)
+    for k in ("dx", "da_gate", "dx_gate", "dA_log"):
+        assert same(g[k][..., D - n:], r[k]), k
+    ssm.gated_recurrence_bwd(x, x, x, A, None, x, None)   # one row: no second pass
+    del g
+    G = D // 16
+    y, m, s = ssm.group_norm_fwd(x, G, A, return_stats=True)
+    g = ssm.group_norm_bwd(x, x, G, A, None, m, s)
+    last = x[..., D - n:]
+    r = ssm.group_norm_bwd(last, last, n // 16, A[D - n:], None, m[..., G - n // 16:].contiguous(),
+                           s[..., G - n // 16:].contiguous())
+    assert same(g["dx"][..., D - n:], r["dx"]) and same(g["dweight"][D - n:], r["dweight"])
+    wide = torch.ones((2, 1, 1), dtype=torch.bfloat16, device=DEV).expand(2, 1, D + 16).contiguous()
+    w, st = torch.ones(D + 16, device=DEV), torch.ones((2, 1, G + 1), device=DEV)
+    for f in (lambda: ssm.gated_recurrence_bwd(wide, wide, wide, w, None, wide, None),
+              lambda: ssm.group_norm_bwd(wide, wide, G + 1, w, None, st, st),
+              lambda: ssm.group_norm_bwd(x, x, G, A, A, m, s)):   # the bias's sums beside the weight's
+        with pytest.raises(ssm.SsmScanError) as e:
+            f()
+        assert e.value.code == ssm.SSM_ERR_UNSUPPORTED
