@@ -73,6 +73,34 @@ def lens_of(B, L):
 
 # ---- against 64 bits -----------------------------------------------------------
 
+@pytest.mark.parametrize("path,io,B,L,D,lens", [
+    ((2, 16), "bf16", 2, 2200, 4160, [2200, 1300]),      # what training takes, whole lines
+    ((2, 16), "bf16", 1, 4400, 4160, None),              # two spans
+    ((2, 8), "bf16", 1, 2200, 4160, [2177]),
+    ((1, 16), "f32", 1, 4400, 2112, None),
+    ((1, 16), "f32", 2, 2200, 2112, [1990, 2200]),
+    ((1, 16), "bf16", 64, 2100, 64, [2100 - 31 * b for b in range(64)]),
+    ((1, 8), "bf16", 3, 2500, 192, [2500, 0, 2433]),
+    ((1, 8), "f32", 3, 2500, 192, None),
+    ((2, 16), "bf16", 2, 2101, 8256, [2101, 700]),       # backward tiles dealt in pairs
+    ((1, 16), "f32", 1, 2101, 16448, None),
+])
+def test_tiles_of_whole_lines(path, io, B, L, D, lens):
+    """Rows whose pieces are whole lines of 128 bytes, read past the caches; run to run the same bits, and the state
+    in place."""
+    import selective_state_space_scan_amd as ssm
+    assert on_path(path, io, B, L, D) == "tiles"
+    c = gated_inputs(io, B, L, D, 301, wide=B == 2)
+    assert all(c[k].data_ptr() % 128 == 0 and c[k].stride(1) * c[k].element_size() % 128 == 0 for k in ("x", "ag", "xg", "dy"))
+    one, two = gated_both(c, i32(lens)), gated_both(c, i32(lens))
+    sync()
+    assert all(same(a, b) for a, b in zip(outputs(one), outputs(two)))
+    h = c["h0"].clone()
+    y, last = ssm.gated_recurrence_fwd(c["x"], c["ag"], c["xg"], c["A"], i32(lens), h0=h, h_last=h)[:2]
+    assert same(y, one[0]) and same(last, one[1]) and last is h
+    check_gated(io, c, lens, *one)
+
+
 @pytest.mark.parametrize("io", ["f32", "bf16"])
 @pytest.mark.parametrize("L,lens", [(1, None), (9, [8]), (100, None), (128, [128]), (128, [0])])
 def test_one_short_row_of_many_channels(io, L, lens):
