@@ -331,3 +331,56 @@ def test_the_most_columns_that_are_summed():
         with pytest.raises(ssm.SsmScanError) as e:
             f()
         assert e.value.code == ssm.SSM_ERR_UNSUPPORTED
+
+
+# ---- narrow groups ---------------------------------------------------------------
+
+@pytest.mark.parametrize("gate", ["none", "after", "before"])
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("n", [1, 2, 3, 4, 5, 6, 7, 9, 15, 17])
+@pytest.mark.parametrize("groups,rows", [(3, 40), (300, 9), (1, 1)])
+def test_group_norm_narrow_groups(io, n, groups, rows, gate):
+    """Several rows a workgroup, more groups than a workgroup has places, and one group alone."""
+    for rms, bias, silu in ((False, True, True), (True, False, True), (False, True, False)):
+        c = group_inputs(io, 1, rows, n * groups, groups, gate, bias, 331, wide=n % 2 == 0)
+        out = group_both(c, groups, gate, silu, rms)
+        sync()
+        check_group(io, c, groups, gate, silu, rms, None, *out)
+
+
+@pytest.mark.parametrize("gate", ["none", "after", "before"])
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("n,groups", [(1, 7), (2, 5), (3, 5), (4, 5), (5, 5), (7, 3)])
+def test_group_norm_narrow_groups_of_many_rows(io, n, groups, gate):
+    """More rows than the GPU takes at once; run to run the same bits."""
+    L = 9001
+    c = group_inputs(io, 2, L, n * groups, groups, gate, True, 332)
+    lens = [L, L // 3]
+    one, two = (group_both(c, groups, gate, True, False, i32(lens)) for _ in range(2))
+    sync()
+    assert all(same(a, b) for a, b in zip(outputs(one), outputs(two)))
+    check_group(io, c, groups, gate, True, False, lens, *one, rows_depth=256)
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("n", [2, 3, 5, 7])
+def test_group_norm_narrow_groups_padding_and_bad_values(io, n):
+    """Groups whose pieces overlap: padding reaches nothing, and a bad group stays alone."""
+    import torch
+    B, L, G = 3, 20, 9
+    lens = [20, 7, 0]
+    for gate in ("none", "after", "before"):
+        c = group_inputs(io, B, L, n * G, G, gate, True, 333, wide=False)
+        want = outputs(group_both(c, G, gate, True, False, i32(lens)))
+        k = {name: None if t is None else t.clone() for name, t in c.items()}
+        for name in ("x", "dy") + (("z",) if gate != "none" else ()):
+            for b, m in enumerate(lens):
+                k[name][b, m:] = float("nan")
+        assert all(same(a, b) for a, b in zip(outputs(group_both(k, G, gate, True, False, i32(lens))), want))
+        k = dict(c, x=c["x"].clone())
+        k["x"][1, 2, 4 * n] = float("nan")
+        got = outputs(group_both(k, G, gate, True, False, i32(lens)))
+        keep = torch.ones((B, L, n * G), dtype=torch.bool, device=DEV)
+        keep[1, 2, 4 * n:5 * n] = False
+        for a, b in ((got[0], want[0]), (got[3], want[3])):
+            assert same(a[keep], b[keep]) and torch.isnan(a[~keep]).all()
