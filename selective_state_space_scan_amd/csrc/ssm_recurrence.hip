@@ -72,7 +72,7 @@ struct GatedBwdParams {
 
 // 1 - a^2 for a = 2^-s2.  Near s2 = 0, where the difference would cancel, s2 times a
 // polynomial: the one of degree 4 nearest to (1 - 2^-2x) / x on [0, 0.36] by its
-// largest relative error (1.5 U with these coefficients, U = 2^-24; found by
+// largest relative error (1.44 U with these coefficients, U = 2^-24; found by
 // exchange of its extrema).  From there on, 1 - a^2 >= 0.39, the difference loses
 // at most 1.5 times a^2's own rounding.
 __device__ __forceinline__ float one_minus_square(float a, float s2) {
@@ -1043,15 +1043,20 @@ struct Cut {
 // Up to kFew workgroups of 16 channels take whole short rows (us forward / backward:
 // 1 x 512 x 64 7.2 / 9.1 where tiles of a chain take 11 / 15.9, 1 x 512 x 2048 9.0 / 13.1
 // and 11.1 / 16.3; at 1024 of them, 8 x 512 x 2048, their 32-byte pieces cost 44 / 80
-// where tiles take 23 / 44); forward, half as many take rows of up to 1024 steps, 16 a lane
-// (1 x 600 x 64 8.1 for 11.8, 4 x 1024 x 1024 f32 20.8 for 23.7; 504 of them, 8 x 1000 x
-// 1000, 41 for 24.6).  Wider ones take rows of up to 16 waves' steps (256 x 129
+// where tiles take 23 / 44).  Up to 256 of them gain everywhere (2 x 512 x 2048: bf16 12.2
+// / 20.0 for 13.5 / 23, f32 12.3 / 19.8 for 13.8 / 25); from there to kFew they gain and
+// lose: 4 x 256 x 2048 bf16 12.0 / 20.0 for 9.0 / 22.3, f32 12.6 / 19.8 for 10.7 / 24.6; 3 x
+// 512 x 2048 bf16 18.8 / 30.7 for 16.8 / 26.8, f32 17.4 / 31.0 for 18.5 / 31.7; 4 x 512 x
+// 2048 bf16 22.3 / 35.2 for 19.8 / 29.8, f32 20.3 / 46.0 for 23.0 / 36.0.  Forward, half as
+// many take rows of up to 1024 steps, 16 a lane (1 x 600 x 64 8.1 for 11.8, 4 x 1024 x
+// 1024 f32 20.6 for 23.6; at 2 x 1024 x 2048 bf16 20.7 for 20.5; 504 of them, 8 x 1000 x
+// 1000, 41 for 24.5).  Wider ones take rows of up to 16 waves' steps (256 x 129
 // x 512 forward 45.3, tiles 54).  Two bf16 channels a lane read pieces of 256 bytes, 65 us
 // for 78.5 at 8 x 4096 x 1024, but for kFill tiles of 128 x 128 and more; two of fp32
 // cost more registers than they give (102 us at one, 107 at two).
 // Tiles of 16 waves halve the chain's length where there are kMany of them at least (us
-// at 16 / 8 waves, bf16: 8 x 4096 x 1024 65 / 68, 1 x 32768 x 2048 108 / 132; but with
-// 256 of them, 1 x 4096 x 256, 16.7 / 13.3).  Backward, their registers leave one
+// at 16 / 8 waves, bf16: 8 x 4096 x 1024, 1024 of them, 65 / 68, 1 x 32768 x 2048, 2048,
+// 108 / 132; but with 64 of them, 1 x 4096 x 256, 16.7 / 13.3; none measured between).  Backward, their registers leave one
 // workgroup a CU, which took 15 and 8 % longer.
 constexpr int64_t kFew = 512, kFill = 512, kMany = 512;
 Cut cut_of(const ssm_gated_dims* dims, int64_t steps, int64_t wide, int64_t most_waves) {
