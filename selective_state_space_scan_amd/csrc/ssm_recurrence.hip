@@ -1056,8 +1056,8 @@ struct Cut {
 // cost more registers than they give (102 us at one, 107 at two).
 // Tiles of 16 waves halve the chain's length where there are kMany of them at least (us
 // at 16 / 8 waves, bf16: 8 x 4096 x 1024, 1024 of them, 65 / 68, 1 x 32768 x 2048, 2048,
-// 108 / 132; but with 64 of them, 1 x 4096 x 256, 16.7 / 13.3; none measured between).  Backward, their registers leave one
-// workgroup a CU, which took 15 and 8 % longer.
+// 108 / 132; but with 64 of them, 1 x 4096 x 256, 16.7 / 13.3; none measured between).
+// Backward, their registers leave one workgroup a CU, which took 15 and 8 % longer.
 constexpr int64_t kFew = 512, kFill = 512, kMany = 512;
 Cut cut_of(const ssm_gated_dims* dims, int64_t steps, int64_t wide, int64_t most_waves) {
   Cut c;
